@@ -378,6 +378,97 @@ int nvfp4_graph_destroy(void* graph);
  */
 int nvfp4_layer_is_quantized(const char* layer_name, const char* pattern);
 
+/* ---------------------------------------------------------------------------
+ * The operators between a block's linears (dit_*).  bf16 activations; the
+ * conventions above hold (device pointers, stream, status order, no
+ * allocation, no state).  Every statistic and sum is binary32 or wider; each
+ * output is rounded once.
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+  DIT_NORM_NONE = 0,
+  DIT_NORM_LAYER = 1, /* (v - mean) / sqrt(mean((v - mean)^2) + eps) */
+  DIT_NORM_RMS = 2    /* v / sqrt(mean(v^2) + eps) */
+} dit_norm;
+
+typedef enum {
+  DIT_ROTARY_INTERLEAVED = 0, /* pair j: elements 2j, 2j + 1 */
+  DIT_ROTARY_HALF = 1         /* pair j: elements j, j + rotary_dim / 2 */
+} dit_rotary_layout;
+
+/* bf16 heads in memory: element (b, t, h, d) at data + b * batch_stride +
+ * t * token_stride + h * head_stride + d.  Strides are in elements, multiples
+ * of 8 and >= 0; data is 16-byte aligned.  So the query, key and value parts
+ * of one fused projection are taken as they lie. */
+typedef struct {
+  void* data;
+  int64_t batch_stride, token_stride, head_stride;
+} dit_heads;
+
+/*
+ * dit_gated_norm -- the gate and residual after a linear and the norm before
+ * the next one, in one pass:
+ *
+ *   z = y, or post_norm(y) * post_weight
+ *   r = residual_scale * x + gate * z
+ *   h = (norm(r) * weight + bias) * (1 + scale) + shift
+ *
+ *   x               [batch, tokens, channels], fp32 if x_fp32 else bf16, 16-byte aligned.
+ *   y_bf16          optional [batch, tokens, channels] bf16.  NULL: r is x, and
+ *                   gate, post_norm, post_weight and residual must be NULL / 0
+ *                   and residual_scale 1.
+ *   gate, scale, shift  optional vectors, one per batch entry: entry b's at
+ *                   element b * stride (each its own stride, a multiple of 8),
+ *                   fp32 if mod_fp32 else bf16, 16-byte aligned; so chunks of a
+ *                   modulation linear's output are taken as they lie.
+ *   weight, bias, post_weight  optional [channels] fp32, 16-byte aligned.
+ *   batch, tokens >= 0; 0 < channels <= 16384, a multiple of 8.
+ *   norm, post_norm a dit_norm; DIT_NORM_NONE leaves the value as it is.
+ *   eps             > 0.
+ *   residual        optional out, r in x's type.  It may be x itself.
+ *   h_bf16          optional out, bf16 (residual or h_bf16 must be given).  It
+ *                   may be y_bf16 itself.
+ *   amax            optional device float, needs h_bf16: max |h| over the bf16
+ *                   outputs, ready for nvfp4_quantize's amax_in (zeroed first,
+ *                   on `stream`; 0 if there are no rows; not finite if an
+ *                   output is NaN).
+ * h is computed from r before r is rounded.  Deterministic.
+ */
+int dit_gated_norm(const void* x, int x_fp32, const void* y_bf16, const void* gate,
+                   int64_t gate_stride, const void* scale, int64_t scale_stride,
+                   const void* shift, int64_t shift_stride, int mod_fp32, const float* weight,
+                   const float* bias, const float* post_weight, int64_t batch, int64_t tokens,
+                   int64_t channels, int norm, int post_norm, float residual_scale, float eps,
+                   void* residual, void* h_bf16, float* amax, void* stream);
+
+/*
+ * dit_rotary -- rotary positions on query and key heads, one launch for both:
+ *
+ *   z = v, or v / sqrt(mean(v^2) + eps) * weight over the head's dim elements
+ *   pair (a, b) of angle t = 2 pi turns[j] positions[axis[j]]:
+ *     a' = magnitude (a cos t - b sin t),  b' = magnitude (b cos t + a sin t)
+ *
+ * Elements from rotary_dim on are z (copied bit for bit without a weight).
+ *   q, q_out        [batch, tokens, heads, dim]; k, k_out the same with
+ *                   kv_heads, or both NULL with kv_heads 0.  An output may be
+ *                   its input itself; no other overlap.
+ *   positions       [batch, tokens, axes] int32, any value.
+ *   turns           [rotary_dim / 2] fp64: turns per position of each pair;
+ *                   the product is taken in binary64 and reduced to a fraction
+ *                   of a turn, so far positions lose nothing.
+ *   axis            [rotary_dim / 2] int32 in [0, axes), NULL when axes is 1
+ *                   (values outside are taken as the nearest axis).
+ *   q_weight, k_weight  optional [dim] fp32: that tensor's norm.
+ *   dim             a multiple of 8, at most 256; rotary_dim a multiple of 16,
+ *                   0 < rotary_dim <= dim.  1 <= axes <= 16.  heads > 0.
+ *   layout          a dit_rotary_layout.  eps > 0.
+ */
+int dit_rotary(const dit_heads* q, const dit_heads* q_out, int64_t heads, const dit_heads* k,
+               const dit_heads* k_out, int64_t kv_heads, const int32_t* positions, int64_t axes,
+               const double* turns, const int32_t* axis, float magnitude, const float* q_weight,
+               const float* k_weight, float eps, int64_t batch, int64_t tokens, int64_t dim,
+               int64_t rotary_dim, int layout, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

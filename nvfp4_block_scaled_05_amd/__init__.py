@@ -20,7 +20,8 @@ Fp8Tensor = namedtuple("Fp8Tensor", ["codes", "scales"])   # E4M3 [rows, cols], 
 __all__ = ["Nvfp4Tensor", "Fp8Tensor", "Nvfp4Error", "load", "abi_version", "status_string",
            "quantize_workspace_bytes", "quantize_workspace", "quantize", "dequantize", "gemm", "gemm_workspace",
            "gemm_quantized", "gemm_bf16", "layer_is_quantized", "quantize_weight", "linear",
-           "fp8_quantize", "fp8_gemm", "fp8_gemm_workspace"]
+           "fp8_quantize", "fp8_gemm", "fp8_gemm_workspace",
+           "gated_norm", "RotaryPlan", "rotary_plan", "rotary"]
 
 
 _TORCH = None
@@ -407,3 +408,7 @@ def linear(x, weight, name, bias=None, epilogue="none", pattern=None):
     if layer_is_quantized(name, pattern):
         return gemm(quantize(x), weight, bias=bias, epilogue=epilogue)
     return gemm_bf16(x, weight, bias=bias, epilogue=epilogue)
+
+
+# the operators between the linears use the checks above
+from .block_ops import RotaryPlan, gated_norm, rotary, rotary_plan  # noqa: E402

@@ -24,6 +24,16 @@ EPILOGUES = {"none": 0, "gelu": 1}
 #: exported symbols and their (restype, argtypes)
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_F = ctypes.c_float
+_INT = ctypes.c_int
+
+
+class DitHeads(ctypes.Structure):
+    """dit_heads: bf16 heads in memory, strides in elements."""
+    _fields_ = [("data", _P), ("batch_stride", _I64), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+_HEADS = ctypes.POINTER(DitHeads)
 SIGNATURES = {
     "nvfp4_abi_version": (ctypes.c_int, []),
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -46,6 +56,10 @@ SIGNATURES = {
     "nvfp4_graph_launch": (ctypes.c_int, [_P, _P]),
     "nvfp4_graph_destroy": (ctypes.c_int, [_P]),
     "nvfp4_layer_is_quantized": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_char_p]),
+    "dit_gated_norm": (_INT, [_P, _INT, _P, _P, _I64, _P, _I64, _P, _I64, _INT, _P, _P, _P, _I64,
+                              _I64, _I64, _INT, _INT, _F, _F, _P, _P, _P, _P]),
+    "dit_rotary": (_INT, [_HEADS, _HEADS, _I64, _HEADS, _HEADS, _I64, _P, _I64, _P, _P, _F, _P, _P,
+                          _F, _I64, _I64, _I64, _I64, _INT, _P]),
 }
 
 _lib = None

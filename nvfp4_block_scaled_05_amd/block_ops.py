@@ -1,0 +1,263 @@
+"""The operators between a block's linears: Python face of the dit_* entry
+points of include/nvfp4.h, with the argument checks of the package.
+
+Tensors are bf16 on the current HIP device unless said otherwise, calls are
+enqueued on the current stream, and outputs that are not passed in are
+allocated with torch.  Everything is forward only: no output carries a
+gradient.
+"""
+
+import ctypes
+import math
+from collections import namedtuple
+
+from . import _device, _opt, _ptr, _stream, _tensor, _torch
+from ._binding import DitHeads, check, load
+
+NORMS = {"none": 0, "layer": 1, "rms": 2}
+ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
+ROTARY_SCALINGS = ("none", "linear", "ntk", "yarn")
+
+
+def _choice(value, choices, name):
+    if value not in choices:
+        raise ValueError(f"{name} must be one of {sorted(choices)}, got {value!r}")
+    return choices[value]
+
+
+def _rows3(t, name):
+    """(batch, tokens, channels) of a [tokens, channels] or [batch, tokens, channels] tensor."""
+    if not isinstance(t, _torch().Tensor) or t.dim() not in (2, 3):
+        raise ValueError(f"{name}: expected a 2-D or 3-D torch.Tensor")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def _vector(t, name, batch, channels, dtype):
+    """The stride of a [batch, channels] tensor whose rows are dense (a chunk of
+    a wider one), after its checks."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != (batch, channels):
+        raise ValueError(f"{name}: expected a torch.Tensor of shape {(batch, channels)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if channels > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the last dimension must be dense (got strides {tuple(t.stride())})")
+    return t.stride(0) if batch > 1 else 0
+
+
+def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weight=None, bias=None,
+               post_norm="none", post_weight=None, residual_scale=1.0, eps=1e-6, amax=None,
+               out=None, residual_out=None):
+    """The gate and residual after a linear and the norm before the next, in one pass:
+
+        r = residual_scale * x + gate * z,  z = y or post_norm(y) * post_weight
+        h = (norm(r) * weight + bias) * (1 + scale) + shift
+
+    x: [tokens, channels] or [batch, tokens, channels], bf16 or float32 (the
+    residual stream); y: bf16 of the same shape, or None (r is x).  gate, scale,
+    shift: [batch, channels] (batch 1 for a 2-D x), all bf16 or all float32, dense
+    rows of any stride that is a multiple of 8, so chunks of the modulation
+    linear's output are taken as they are.  weight, bias, post_weight: float32
+    [channels].  norm, post_norm: "none", "layer" or "rms".  amax: optional
+    one-element float32 device tensor, set to max |h| for ``quantize``.
+
+    Returns (r, h): r in x's type (x itself when there is no y), h in bf16.
+    ``residual_out`` may be x, ``out`` may be y; channels: a multiple of 8, at
+    most 16384.
+    """
+    torch = _torch()
+    batch, tokens, channels = _rows3(x, "x")
+    fp32 = x.dtype == torch.float32
+    _tensor(x, "x", torch.float32 if fp32 else torch.bfloat16, min_numel=0)
+    if channels <= 0 or channels % 8 or channels > 16384:
+        raise ValueError(f"x: channels must be a positive multiple of 8 up to 16384, got {channels}")
+    norm_id = _choice(norm, NORMS, "norm")
+    post_id = _choice(post_norm, NORMS, "post_norm")
+    if y is None:
+        for name, v in (("gate", gate), ("post_weight", post_weight), ("residual_out", residual_out)):
+            if v is not None:
+                raise ValueError(f"{name} needs y")
+        if post_id or residual_scale != 1.0:
+            raise ValueError("post_norm and residual_scale need y")
+    if not (eps > 0 and math.isfinite(eps) and math.isfinite(residual_scale)):
+        raise ValueError(f"eps must be positive, residual_scale finite; got {eps}, {residual_scale}")
+    _opt(y, "y", torch.bfloat16, x.shape, 0)
+    mod = next((t.dtype for t in (gate, scale, shift) if isinstance(t, torch.Tensor)), torch.bfloat16)
+    if mod not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"gate, scale, shift: dtype {mod}, expected bfloat16 or float32")
+    strides = [0 if t is None else _vector(t, name, batch, channels, mod)
+               for name, t in (("gate", gate), ("scale", scale), ("shift", shift))]
+    _opt(weight, "weight", torch.float32, (channels,))
+    _opt(bias, "bias", torch.float32, (channels,))
+    _opt(post_weight, "post_weight", torch.float32, (channels,))
+    _opt(amax, "amax", torch.float32)
+    _opt(out, "out", torch.bfloat16, x.shape, 0)
+    _opt(residual_out, "residual_out", x.dtype, x.shape, 0)
+    dev = _device(x=x, y=y, gate=gate, scale=scale, shift=shift, weight=weight, bias=bias,
+                  post_weight=post_weight, amax=amax, out=out, residual_out=residual_out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+    if residual_out is None and y is not None:
+        residual_out = torch.empty_like(x)
+    check(load().dit_gated_norm(
+        x.data_ptr(), fp32, _ptr(y), _ptr(gate), strides[0], _ptr(scale), strides[1], _ptr(shift),
+        strides[2], mod == torch.float32, _ptr(weight), _ptr(bias), _ptr(post_weight), batch, tokens,
+        channels, norm_id, post_id, residual_scale, eps, _ptr(residual_out), out.data_ptr(),
+        _ptr(amax), _stream()), "dit_gated_norm")
+    return (x if y is None else residual_out), out
+
+
+#: turns per position (float64) and position axis (int32) of each rotary pair,
+#: the rotated elements per head, the number of axes, and the factor on rotated values
+RotaryPlan = namedtuple("RotaryPlan", ["turns", "axis", "rotary_dim", "axes", "magnitude"])
+
+
+def _yarn_blend(pairs, dim, base, original_length, beta_fast, beta_slow):
+    """How far each pair's frequency is interpolated (0: kept, 1: divided by the
+    factor): none for pairs with more than beta_fast turns over the trained
+    length, fully below beta_slow turns, linear in the pair index between."""
+    def index_of(turns):
+        return dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+    low = max(math.floor(index_of(beta_fast)), 0)
+    high = min(math.ceil(index_of(beta_slow)), dim - 1)
+    width = high - low if high != low else 0.001
+    return [min(max((j - low) / width, 0.0), 1.0) for j in range(pairs)]
+
+
+def rotary_plan(rotary_dim, base=10000.0, axes=None, scaling="none", factor=1.0,
+                original_length=0, beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """The frequencies of ``rotary``, made once per model: pair j of an axis of d
+    elements turns by base ** (-2 j / d) radians a position.
+
+    axes: elements of each position axis (they sum to rotary_dim; text index,
+    image row and image column of a DiT), None for one axis.  scaling, for
+    positions past the trained length by ``factor``:
+      "linear"  every frequency divided by the factor;
+      "ntk"     the base raised to base * factor ** (d / (d - 2));
+      "yarn"    by parts ("YaRN: Efficient Context Window Extension of Large
+                Language Models", section 3): frequencies below beta_slow turns
+                over original_length divided, above beta_fast kept, blended
+                between; rotated values scaled by 0.1 ln(factor) + 1.
+    """
+    torch = _torch()
+    if rotary_dim <= 0 or rotary_dim % 16 or rotary_dim > 256:
+        raise ValueError(f"rotary_dim must be a positive multiple of 16 up to 256, got {rotary_dim}")
+    dims = [rotary_dim] if axes is None else list(axes)
+    if not 1 <= len(dims) <= 16 or any(d <= 0 or d % 2 for d in dims) or sum(dims) != rotary_dim:
+        raise ValueError(f"axes must be up to 16 positive even sizes that sum to {rotary_dim}, got {dims}")
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}, got {scaling!r}")
+    if not (base > 1 and math.isfinite(base) and factor >= 1 and math.isfinite(factor)):
+        raise ValueError(f"base must be above 1 and factor at least 1, got {base}, {factor}")
+    if scaling == "none" and factor != 1.0:
+        raise ValueError(f"factor {factor} needs a scaling")
+    if scaling == "yarn" and not (original_length > 0 and beta_fast > beta_slow > 0):
+        raise ValueError("yarn needs original_length > 0 and beta_fast > beta_slow > 0")
+    turns, axis = [], []
+    for a, d in enumerate(dims):
+        b = base * factor ** (d / (d - 2)) if scaling == "ntk" and d > 2 else base
+        radians = [b ** (-2 * j / d) for j in range(d // 2)]
+        if scaling == "linear":
+            radians = [f / factor for f in radians]
+        if scaling == "yarn":
+            blend = _yarn_blend(d // 2, d, base, original_length, beta_fast, beta_slow)
+            radians = [f * (1 - m) + f / factor * m for f, m in zip(radians, blend)]
+        turns += [f / (2 * math.pi) for f in radians]
+        axis += [a] * (d // 2)
+    return RotaryPlan(torch.tensor(turns, dtype=torch.float64, device=device),
+                      torch.tensor(axis, dtype=torch.int32, device=device), rotary_dim, len(dims),
+                      0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0)
+
+
+def _heads(t, name, out=False):
+    """(batch, tokens, heads, dim) and the C view of bf16 heads [tokens, heads,
+    dim] or [batch, tokens, heads, dim]: dim dense, other strides multiples of
+    8.  ``out``: no element may lie twice."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
+        raise ValueError(f"{name}: expected a 3-D or 4-D torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        shape, stride = (1, *shape), (0, *stride)
+    if shape[3] > 1 and stride[3] != 1:
+        raise ValueError(f"{name}: the last dimension must be dense (got strides {tuple(t.stride())})")
+    view = [0 if n <= 1 else s for n, s in zip(shape[:3], stride[:3])]
+    if any(s % 8 for s in view):
+        raise ValueError(f"{name}: strides must be multiples of 8 (got {tuple(t.stride())})")
+    if out:
+        reach = shape[3]
+        for s, n in sorted((s, n) for s, n in zip(view, shape[:3]) if n > 1):
+            if s < reach:
+                raise ValueError(f"{name}: elements overlap (strides {tuple(t.stride())})")
+            reach = s * n
+    return tuple(shape), DitHeads(t.data_ptr(), *view)
+
+
+def _out_heads(out, like, name):
+    """The C view of an output like ``like``, None when it is not given."""
+    if out is None:
+        return None
+    _, view = _heads(out, name, out=True)
+    if out.shape != like.shape:
+        raise ValueError(f"{name}: shape {tuple(out.shape)}, expected {tuple(like.shape)}")
+    return view
+
+
+def rotary(q, positions, plan, k=None, layout="interleaved", q_weight=None, k_weight=None,
+           eps=1e-6, out=None, k_out=None):
+    """Rotary positions on the query heads and, in the same launch, the key
+    heads; with ``q_weight`` / ``k_weight`` (float32 [dim]) each head is first
+    RMS-normalised (the query/key norm).
+
+    q: [tokens, heads, dim] or [batch, tokens, heads, dim], k the same with its
+    own head count; views of a fused projection are taken as they are.
+    positions: int32 [tokens] or [batch, tokens], with a last dimension of
+    plan.axes when the plan has several axes.  layout: "interleaved" (pairs of
+    neighbours) or "half" (j with j + rotary_dim / 2).  Elements from
+    plan.rotary_dim on are not rotated.  ``out`` / ``k_out`` may be q / k.
+    Returns out, or (out, k_out) when k is given.
+    """
+    torch = _torch()
+    shape, qv = _heads(q, "q")
+    batch, tokens, heads, dim = shape
+    if not isinstance(plan, RotaryPlan):
+        raise ValueError("plan: expected a RotaryPlan (rotary_plan)")
+    if dim % 8 or not plan.rotary_dim <= dim <= 256:
+        raise ValueError(f"q: head size must be a multiple of 8 in [{plan.rotary_dim}, 256], got {dim}")
+    layout_id = _choice(layout, ROTARY_LAYOUTS, "layout")
+    if not (eps > 0 and math.isfinite(eps)):
+        raise ValueError(f"eps must be positive, got {eps}")
+    if not isinstance(positions, torch.Tensor):
+        raise ValueError("positions: expected a torch.Tensor")
+    tail = (plan.axes,) if plan.axes > 1 or positions.dim() == q.dim() - 1 else ()
+    _tensor(positions, "positions", torch.int32, (*q.shape[:-2], *tail), 0)
+    _tensor(plan.turns, "plan.turns", torch.float64, (plan.rotary_dim // 2,))
+    _tensor(plan.axis, "plan.axis", torch.int32, (plan.rotary_dim // 2,))
+    kv_heads, kv = 0, None
+    if k is not None:
+        k_shape, kv = _heads(k, "k")
+        kv_heads = k_shape[2]
+        if k.dim() != q.dim() or (k_shape[:2], k_shape[3]) != (shape[:2], dim):
+            raise ValueError(f"k: shape {tuple(k.shape)} does not go with q's {tuple(q.shape)}")
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    _opt(q_weight, "q_weight", torch.float32, (dim,))
+    _opt(k_weight, "k_weight", torch.float32, (dim,))
+    qo = _out_heads(out, q, "out")
+    ko = None if k is None else _out_heads(k_out, k, "k_out")
+    dev = _device(q=q, k=k, positions=positions, turns=plan.turns, axis=plan.axis,
+                  q_weight=q_weight, k_weight=k_weight, out=out, k_out=k_out)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        qo = _heads(out, "out")[1]
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+        ko = _heads(k_out, "k_out")[1]
+    ref = ctypes.byref
+    check(load().dit_rotary(
+        ref(qv), ref(qo), heads, kv and ref(kv), ko and ref(ko), kv_heads, positions.data_ptr(),
+        plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(), plan.magnitude, _ptr(q_weight),
+        _ptr(k_weight), eps, batch, tokens, dim, plan.rotary_dim, layout_id, _stream()), "dit_rotary")
+    return out if k is None else (out, k_out)

@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cstring>
 #include <regex>
 #include <string>
@@ -62,6 +63,23 @@ int page_pattern_matches(const char* name) {
 // The regex engine recurses once per character of the subject, so a caller's
 // pattern is only applied to names up to this length.
 constexpr size_t kMaxPatternName = 1024;
+
+// Operators between the linears: what their views and vectors must keep.
+
+bool bad_heads(const dit_heads& v) {
+  for (const int64_t s : {v.batch_stride, v.token_stride, v.head_stride})
+    if (s < 0 || s % 8 != 0 || s >= ((int64_t)1 << 40)) return true;
+  return false;
+}
+
+bool finite_positive(float v) { return v > 0.0f && v <= FLT_MAX; }
+
+nvfp4::RotaryHeads rotary_heads(const dit_heads& in, const dit_heads& out, const float* weight,
+                                int64_t heads) {
+  return {static_cast<const uint16_t*>(in.data), in.batch_stride, in.token_stride, in.head_stride,
+          static_cast<uint16_t*>(out.data), out.batch_stride, out.token_stride, out.head_stride,
+          weight, (int)heads};
+}
 
 }  // namespace
 
@@ -313,6 +331,88 @@ int nvfp4_layer_is_quantized(const char* layer_name, const char* pattern) {
   } catch (const std::exception&) {
     return NVFP4_ERR_ARG;
   }
+}
+
+int dit_gated_norm(const void* x, int x_fp32, const void* y_bf16, const void* gate,
+                   int64_t gate_stride, const void* scale, int64_t scale_stride,
+                   const void* shift, int64_t shift_stride, int mod_fp32, const float* weight,
+                   const float* bias, const float* post_weight, int64_t batch, int64_t tokens,
+                   int64_t channels, int norm, int post_norm, float residual_scale, float eps,
+                   void* residual, void* h_bf16, float* amax, void* stream) {
+  if (bad_dim(batch) || bad_dim(tokens) || bad_dim(channels)) return NVFP4_ERR_SHAPE;
+  const bool empty = batch == 0 || tokens == 0;
+  if (!empty && (!x || (!residual && !h_bf16))) return NVFP4_ERR_NULL;
+  if (amax && !empty && !h_bf16) return NVFP4_ERR_NULL;
+  if (channels == 0 || channels % 8 != 0 || channels > 16384) return NVFP4_ERR_SHAPE;
+  if (batch * tokens >= kMaxDim) return NVFP4_ERR_SHAPE;
+  for (const int64_t s : {gate ? gate_stride : 0, scale ? scale_stride : 0, shift ? shift_stride : 0})
+    if (s < 0 || s % 8 != 0 || s >= ((int64_t)1 << 31)) return NVFP4_ERR_SHAPE;
+  for (const void* p : {x, y_bf16, gate, scale, shift, static_cast<const void*>(weight),
+                        static_cast<const void*>(bias), static_cast<const void*>(post_weight),
+                        static_cast<const void*>(residual), static_cast<const void*>(h_bf16)})
+    if (!aligned(p, 16)) return NVFP4_ERR_ALIGN;
+  if (!aligned(amax, 4)) return NVFP4_ERR_ALIGN;
+  for (const int n : {norm, post_norm})
+    if (n != DIT_NORM_NONE && n != DIT_NORM_LAYER && n != DIT_NORM_RMS) return NVFP4_ERR_ARG;
+  if (!finite_positive(eps) || !(residual_scale >= -FLT_MAX && residual_scale <= FLT_MAX))
+    return NVFP4_ERR_ARG;
+  if (!y_bf16 && !empty &&
+      (gate || post_norm != DIT_NORM_NONE || post_weight || residual || residual_scale != 1.0f))
+    return NVFP4_ERR_ARG;
+  int st = check_device();
+  if (st != NVFP4_OK) return st;
+  const nvfp4::GatedNorm a{x, static_cast<const uint16_t*>(y_bf16), gate, scale, shift,
+                           gate_stride, scale_stride, shift_stride, weight, bias, post_weight,
+                           batch * tokens, tokens, (int)channels, norm, post_norm, mod_fp32 != 0,
+                           residual_scale, eps, (float)(1.0 / (double)channels), residual,
+                           static_cast<uint16_t*>(h_bf16), reinterpret_cast<uint32_t*>(amax)};
+  return hip_status(nvfp4::launch_gated_norm(a, x_fp32 != 0, static_cast<hipStream_t>(stream)));
+}
+
+int dit_rotary(const dit_heads* q, const dit_heads* q_out, int64_t heads, const dit_heads* k,
+               const dit_heads* k_out, int64_t kv_heads, const int32_t* positions, int64_t axes,
+               const double* turns, const int32_t* axis, float magnitude, const float* q_weight,
+               const float* k_weight, float eps, int64_t batch, int64_t tokens, int64_t dim,
+               int64_t rotary_dim, int layout, void* stream) {
+  if (bad_dim(batch) || bad_dim(tokens) || bad_dim(heads) || bad_dim(kv_heads))
+    return NVFP4_ERR_SHAPE;
+  const bool empty = batch == 0 || tokens == 0;
+  if (!q || !q_out || (kv_heads > 0 && (!k || !k_out))) return NVFP4_ERR_NULL;
+  if (!empty && (!q->data || !q_out->data || !positions || !turns || (axes > 1 && !axis)))
+    return NVFP4_ERR_NULL;
+  if (!empty && kv_heads > 0 && (!k->data || !k_out->data)) return NVFP4_ERR_NULL;
+  if (heads == 0 || heads + kv_heads > (1 << 16) || batch * tokens >= kMaxDim)
+    return NVFP4_ERR_SHAPE;
+  if (dim <= 0 || dim % 8 != 0 || dim > 256 || rotary_dim <= 0 || rotary_dim % 16 != 0 ||
+      rotary_dim > dim || axes < 1 || axes > 16)
+    return NVFP4_ERR_SHAPE;
+  if (bad_heads(*q) || bad_heads(*q_out)) return NVFP4_ERR_SHAPE;
+  if (kv_heads > 0 && (bad_heads(*k) || bad_heads(*k_out))) return NVFP4_ERR_SHAPE;
+  if (!aligned(q->data, 16) || !aligned(q_out->data, 16) || !aligned(positions, 4) ||
+      !aligned(turns, 8) || !aligned(axis, 4) || !aligned(q_weight, 4) || !aligned(k_weight, 4))
+    return NVFP4_ERR_ALIGN;
+  if (kv_heads > 0 && (!aligned(k->data, 16) || !aligned(k_out->data, 16))) return NVFP4_ERR_ALIGN;
+  if ((layout != DIT_ROTARY_INTERLEAVED && layout != DIT_ROTARY_HALF) || !finite_positive(eps) ||
+      !finite_positive(magnitude))
+    return NVFP4_ERR_ARG;
+  int st = check_device();
+  if (st != NVFP4_OK) return st;
+  nvfp4::Rotary a{};
+  a.q = rotary_heads(*q, *q_out, q_weight, heads);
+  if (kv_heads > 0) a.k = rotary_heads(*k, *k_out, k_weight, kv_heads);
+  a.positions = positions;
+  a.turns = turns;
+  a.axis = axis;
+  a.rows = batch * tokens;
+  a.tokens = tokens;
+  a.axes = (int)axes;
+  a.dim = (int)dim;
+  a.rotary_dim = (int)rotary_dim;
+  a.layout = layout;
+  a.magnitude = magnitude;
+  a.eps = eps;
+  a.inv_dim = (float)(1.0 / (double)dim);
+  return hip_status(nvfp4::launch_rotary(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "nvfp4.h"
+
 namespace nvfp4 {
 
 // Compute units of the current device (256 if the query fails).
@@ -71,5 +73,41 @@ size_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 hipError_t launch_gemm_bf16(const void* x, const void* w, const void* bias, int64_t M, int64_t N,
                             int64_t K, int epilogue, void* y, hipStream_t stream);
+
+// The operators between the linears of a block.  Sizes and strides in elements.
+struct GatedNorm {
+  const void* x;                 // [rows, channels] bf16 or fp32
+  const uint16_t* y;             // [rows, channels] or null
+  const void *gate, *scale, *shift;   // [batch, channels] rows, or null
+  int64_t gate_stride, scale_stride, shift_stride;
+  const float *weight, *bias, *post_weight;
+  int64_t rows, tokens;          // rows = batch * tokens
+  int channels, norm, post_norm;
+  bool mod_fp32;
+  float residual_scale, eps, inv_c;
+  void* residual;                // as x, or null
+  uint16_t* h;                   // or null
+  uint32_t* amax;                // or null
+};
+hipError_t launch_gated_norm(const GatedNorm& a, bool x_fp32, hipStream_t stream);
+
+struct RotaryHeads {
+  const uint16_t* in;
+  int64_t in_batch, in_token, in_head;
+  uint16_t* out;
+  int64_t out_batch, out_token, out_head;
+  const float* weight;           // the norm's, or null: no norm
+  int heads;                     // 0: absent
+};
+struct Rotary {
+  RotaryHeads q, k;
+  const int32_t* positions;      // [rows, axes]
+  const double* turns;           // [rotary_dim / 2]
+  const int32_t* axis;           // [rotary_dim / 2], or null: all 0
+  int64_t rows, tokens;          // rows = batch * tokens
+  int axes, dim, rotary_dim, layout, tokens_per_group;
+  float magnitude, eps, inv_dim;
+};
+hipError_t launch_rotary(Rotary a, hipStream_t stream);
 
 }  // namespace nvfp4

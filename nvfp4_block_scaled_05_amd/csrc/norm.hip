@@ -1,0 +1,273 @@
+// dit_gated_norm: what lies between two linears of a transformer block, in one
+// pass over the tokens.  Per token row of C channels:
+//
+//   z = y                       or  P(y) * post_weight   (P: layer or RMS norm)
+//   r = residual_scale * x + gate * z                    (written; stays unrounded below)
+//   h = (N(r) * weight + bias) * (1 + scale) + shift     (N: layer or RMS norm)
+//
+// layer: (v - mean) / sqrt(mean((v - mean)^2) + eps);  RMS: v / sqrt(mean(v^2) + eps).
+//
+// Bound: HBM.  x and y are read once, r and h written once (8 bytes a channel
+// with a bf16 stream); the vectors over channels (gate, scale, shift, weights)
+// are re-read per row from the caches.  One workgroup owns a row at a time and
+// keeps it in registers between the statistics and the outputs, so each
+// statistic is over values already on chip; mean and variance are two sums, the
+// second of squared distances from the mean, so channels with a large common
+// offset lose nothing.  All of it is binary32; r and h are each rounded once.
+#include "device_common.hpp"
+#include "kernels.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+// Sum over the wave, the same in every lane (a scalar).  Four row-local steps
+// in the vector ALU, then two broadcasts across the 16-lane rows.
+__device__ __forceinline__ float wave_sum(float v) {
+#define NORM_DPP(ctrl, rows)                                                                  \
+  __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, \
+                                                        rows, 0xF, false))
+  v += NORM_DPP(0xB1, 0xF);    // lane ^ 1 within quads
+  v += NORM_DPP(0x4E, 0xF);    // lane ^ 2
+  v += NORM_DPP(0x141, 0xF);   // mirror within 8
+  v += NORM_DPP(0x140, 0xF);   // mirror within 16: every lane has its row's sum
+  v += NORM_DPP(0x142, 0xA);   // rows 1 and 3 take the row before
+  v += NORM_DPP(0x143, 0xC);   // rows 2 and 3 take lane 31
+#undef NORM_DPP
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// Sum over the workgroup's `waves` waves.  `red` alternates between two halves
+// from one sum to the next, so one barrier a sum is enough.
+__device__ __forceinline__ float block_sum(float v, int waves, float (*red)[16], int& half) {
+  v = wave_sum(v);
+  if (waves == 1) return v;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (lane == 0) red[half][wave] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int w = 0; w < waves; ++w) s += red[half][w];
+  half ^= 1;
+  return s;
+}
+
+template <class T> struct Raw;
+template <> struct Raw<uint16_t> { u32x4 v; };            // 8 bf16
+template <> struct Raw<float> { f32x4 lo, hi; };
+
+__device__ __forceinline__ Raw<uint16_t> load8(const uint16_t* p) {
+  return {*reinterpret_cast<const u32x4*>(p)};
+}
+__device__ __forceinline__ Raw<float> load8(const float* p) {
+  return {reinterpret_cast<const f32x4*>(p)[0], reinterpret_cast<const f32x4*>(p)[1]};
+}
+__device__ __forceinline__ void widen(const Raw<uint16_t>& a, float (&f)[8]) {
+  const uint32_t w[4] = {a.v.x, a.v.y, a.v.z, a.v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = __uint_as_float(w[j] << 16);
+    f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void widen(const Raw<float>& a, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[j] = a.lo[j];
+    f[4 + j] = a.hi[j];
+  }
+}
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+  return u32x4{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
+               bf16x2_rne(f[6], f[7])};
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) {
+  *reinterpret_cast<u32x4*>(p) = pack8(f);
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+  reinterpret_cast<f32x4*>(p)[0] = f32x4{f[0], f[1], f[2], f[3]};
+  reinterpret_cast<f32x4*>(p)[1] = f32x4{f[4], f[5], f[6], f[7]};
+}
+
+// 8 entries of a modulation vector, stored as bf16 or fp32.
+__device__ __forceinline__ void vector8(const void* base, bool fp32, int64_t at, float (&f)[8]) {
+  if (fp32)
+    widen(load8(static_cast<const float*>(base) + at), f);
+  else
+    widen(load8(static_cast<const uint16_t*>(base) + at), f);
+}
+
+// v := (v - mean) * rstd of the row, in place; `mine[i]`: chunk i of this
+// thread exists.
+template <int CH>
+__device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&mine)[CH], int kind,
+                                          float inv_c, float eps, int waves, float (*red)[16],
+                                          int& half) {
+  float mean = 0.0f;
+  if (kind == DIT_NORM_LAYER) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[i][j];      // absent chunks hold zeros
+    mean = block_sum(s, waves, red, half) * inv_c;
+  }
+  float q = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[i][j] -= mean;
+      q = mine[i] ? __builtin_fmaf(v[i][j], v[i][j], q) : q;
+    }
+  const float rstd = 1.0f / __builtin_sqrtf(block_sum(q, waves, red, half) * inv_c + eps);
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
+}
+
+// CH: 8-channel chunks a thread holds; chunk i of thread t is t + i * blockDim.
+template <class XT, int CH>
+__global__ __launch_bounds__(1024) void gated_norm_kernel(GatedNorm a) {
+  __shared__ float red[2][16];
+  int half = 0;
+  const int waves = blockDim.x >> 6, chunks = a.channels >> 3;
+  bool mine[CH];
+  int at[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    mine[i] = c < chunks;
+    at[i] = mine[i] ? 8 * c : 0;
+  }
+  const XT* x = static_cast<const XT*>(a.x);
+  XT* r_out = static_cast<XT*>(a.residual);
+  u16x2 top = {0, 0};
+  int64_t row = blockIdx.x;
+  Raw<XT> xr[CH];
+  Raw<uint16_t> yr[CH];
+  auto fetch = [&](int64_t of) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (!mine[i]) continue;
+      xr[i] = load8(x + of * a.channels + at[i]);
+      if (a.y) yr[i] = load8(a.y + of * a.channels + at[i]);
+    }
+  };
+  fetch(row);
+  for (;;) {
+    const int64_t batch = row / a.tokens;
+    float v[CH][8], z[CH][8];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = z[i][j] = 0.0f;
+      if (!mine[i]) continue;
+      widen(xr[i], v[i]);
+      if (a.y) widen(yr[i], z[i]);
+    }
+    const int64_t next = row + gridDim.x;
+    if (next < a.rows) fetch(next);          // the next row's loads run under this row's sums
+    if (a.y) {
+      if (a.post_norm != DIT_NORM_NONE)
+        normalise<CH>(z, mine, a.post_norm, a.inv_c, a.eps, waves, red, half);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        if (!mine[i]) continue;
+        float f[8];
+        if (a.post_weight) {
+          widen(load8(a.post_weight + at[i]), f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[i][j] *= f[j];
+        }
+        if (a.gate) {
+          vector8(a.gate, a.mod_fp32, batch * a.gate_stride + at[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[i][j] *= f[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(a.residual_scale, v[i][j], z[i][j]);
+      }
+    }
+    if (r_out) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (mine[i]) store8(r_out + row * a.channels + at[i], v[i]);
+    }
+    if (a.h) {
+      if (a.norm != DIT_NORM_NONE)
+        normalise<CH>(v, mine, a.norm, a.inv_c, a.eps, waves, red, half);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        if (!mine[i]) continue;
+        float f[8];
+        if (a.weight) {
+          widen(load8(a.weight + at[i]), f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] *= f[j];
+        }
+        if (a.bias) {
+          widen(load8(a.bias + at[i]), f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] += f[j];
+        }
+        if (a.scale) {
+          vector8(a.scale, a.mod_fp32, batch * a.scale_stride + at[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j], f[j], v[i][j]);
+        }
+        if (a.shift) {
+          vector8(a.shift, a.mod_fp32, batch * a.shift_stride + at[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] += f[j];
+        }
+        const u32x4 p = pack8(v[i]);
+        *reinterpret_cast<u32x4*>(a.h + row * a.channels + at[i]) = p;
+        top = max_u16x2(top, max8(p));
+      }
+    }
+    if (next >= a.rows) break;
+    row = next;
+  }
+  if (a.amax) {   // the order of integer maxima does not matter: one atomic a workgroup
+    __shared__ uint32_t wave_top[16];
+    const uint32_t m = wave_max_u32((uint32_t)(top.x > top.y ? top.x : top.y) << 16);
+    if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t t = 0;
+      for (int w = 0; w < waves; ++w) t = max(t, wave_top[w]);
+      atomicMax(a.amax, t);
+    }
+  }
+}
+
+__global__ void zero_amax_kernel(uint32_t* p) { *p = 0u; }
+
+template <class XT, int CH>
+hipError_t launch(const GatedNorm& a, int threads, int64_t grid, hipStream_t stream) {
+  gated_norm_kernel<XT, CH><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gated_norm(const GatedNorm& a, bool x_fp32, hipStream_t stream) {
+  if (a.amax) {
+    zero_amax_kernel<<<1, 1, 0, stream>>>(a.amax);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.rows == 0) return hipSuccess;
+  const int chunks = a.channels / 8;
+  const bool one = chunks <= 64;
+  const int waves = one ? 1 : (chunks + 127) / 128;    // at most 16: channels <= 16384
+  const int64_t cap = (int64_t)compute_units() * (waves <= 4 ? 8 : 32 / waves > 0 ? 32 / waves : 1);
+  const int64_t grid = a.rows < cap ? a.rows : cap;
+  if (x_fp32)
+    return one ? launch<float, 1>(a, 64, grid, stream) : launch<float, 2>(a, 64 * waves, grid, stream);
+  return one ? launch<uint16_t, 1>(a, 64, grid, stream)
+             : launch<uint16_t, 2>(a, 64 * waves, grid, stream);
+}
+
+}  // namespace nvfp4
