@@ -469,6 +469,48 @@ int dit_rotary(const dit_heads* q, const dit_heads* q_out, int64_t heads, const 
                const float* k_weight, float eps, int64_t batch, int64_t tokens, int64_t dim,
                int64_t rotary_dim, int layout, void* stream);
 
+/* Workspace bytes with which dit_cross_attention splits the keys of a call with
+ * few query rows over the compute units; 0 if it would not (or for invalid
+ * sizes). */
+size_t dit_cross_attention_workspace_bytes(int64_t batch, int64_t queries, int64_t keys,
+                                           int64_t heads, int64_t kv_heads, int64_t dim);
+
+/*
+ * dit_cross_attention -- attention of query heads over an encoder's states
+ * (or any keys and values of their own length; no causal order):
+ *
+ *   out[b, t, h] = sum_j w_j v[b, j, g],  w = softmax_j(scale q[b, t, h] . k[b, j, g])
+ *
+ * over the visible keys j of batch entry b, with g = h / (heads / kv_heads).  A
+ * row without a visible key is zeros.  Products and sums are binary32; the
+ * softmax weights are rounded to bf16 for the product with v (a relative 2^-8
+ * each, as the output's own rounding), their sum is not.
+ *
+ *   q, out          [batch, queries, heads, dim]; k, v [batch, keys, kv_heads,
+ *                   dim].  out overlaps no input.
+ *   kv_lengths      optional [batch] int32: entry b sees keys below it (values
+ *                   are taken within [0, keys]).
+ *   key_mask        optional [batch, keys] bytes, entry b's at b * mask_stride:
+ *                   a key is visible where its byte is not 0 (and it is below
+ *                   the length).  Keys and values out of sight are not read or
+ *                   do not count, whatever they hold.
+ *   heads a positive multiple of kv_heads; dim a multiple of 8, at most 128;
+ *   batch, queries, keys >= 0; scale > 0.  k's and v's token strides are
+ *   below 2^23 elements; batch * heads * queries below 2^31.
+ *   workspace       optional, 256-byte aligned, contents on entry irrelevant,
+ *                   owned by the call until it completes: with at least
+ *                   dit_cross_attention_workspace_bytes bytes the keys of a
+ *                   call with few query rows are split over the compute units
+ *                   and joined by a second kernel, in a fixed order; NULL or
+ *                   less: no split.  Deterministic either way; the two differ
+ *                   in the order of the additions.
+ */
+int dit_cross_attention(const dit_heads* q, const dit_heads* k, const dit_heads* v,
+                        const int32_t* kv_lengths, const uint8_t* key_mask, int64_t mask_stride,
+                        int64_t batch, int64_t queries, int64_t keys, int64_t heads,
+                        int64_t kv_heads, int64_t dim, float scale, const dit_heads* out,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,7 +21,8 @@ __all__ = ["Nvfp4Tensor", "Fp8Tensor", "Nvfp4Error", "load", "abi_version", "sta
            "quantize_workspace_bytes", "quantize_workspace", "quantize", "dequantize", "gemm", "gemm_workspace",
            "gemm_quantized", "gemm_bf16", "layer_is_quantized", "quantize_weight", "linear",
            "fp8_quantize", "fp8_gemm", "fp8_gemm_workspace",
-           "gated_norm", "RotaryPlan", "rotary_plan", "rotary"]
+           "gated_norm", "RotaryPlan", "rotary_plan", "rotary",
+           "cross_attention", "cross_attention_workspace"]
 
 
 _TORCH = None
@@ -411,4 +412,5 @@ def linear(x, weight, name, bias=None, epilogue="none", pattern=None):
 
 
 # the operators between the linears use the checks above
-from .block_ops import RotaryPlan, gated_norm, rotary, rotary_plan  # noqa: E402
+from .block_ops import (RotaryPlan, cross_attention, cross_attention_workspace,  # noqa: E402
+                        gated_norm, rotary, rotary_plan)

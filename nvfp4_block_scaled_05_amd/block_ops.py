@@ -11,7 +11,7 @@ import ctypes
 import math
 from collections import namedtuple
 
-from . import _device, _opt, _ptr, _stream, _tensor, _torch
+from . import _NO_WORKSPACE, _device, _opt, _ptr, _stream, _tensor, _torch
 from ._binding import DitHeads, check, load
 
 NORMS = {"none": 0, "layer": 1, "rms": 2}
@@ -261,3 +261,70 @@ def rotary(q, positions, plan, k=None, layout="interleaved", q_weight=None, k_we
         plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(), plan.magnitude, _ptr(q_weight),
         _ptr(k_weight), eps, batch, tokens, dim, plan.rotary_dim, layout_id, _stream()), "dit_rotary")
     return out if k is None else (out, k_out)
+
+
+def cross_attention_workspace(batch, queries, keys, heads, kv_heads, dim, device="cuda"):
+    """A workspace for ``cross_attention`` on these sizes, or None if it would not split."""
+    nbytes = load().dit_cross_attention_workspace_bytes(batch, queries, keys, heads, kv_heads, dim)
+    if nbytes == 0:
+        return None
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+
+
+def cross_attention(q, k, v, kv_lengths=None, key_mask=None, scale=None, out=None,
+                    workspace=_NO_WORKSPACE):
+    """softmax(scale q k^T) v over an encoder's states (no causal order).
+
+    q: [queries, heads, dim] or [batch, queries, heads, dim]; k, v the same with
+    a length and a head count of their own, which divides q's (query heads share
+    key heads in order).  Views of fused projections are taken as they are.
+    dim: a multiple of 8 up to 128.  kv_lengths: int32 [batch], the keys each
+    entry sees; key_mask: bool or uint8 [batch, keys], the keys to see (both:
+    their intersection).  What lies out of sight does not count, whatever it
+    holds; a query that sees no key gets zeros.  scale: dim ** -0.5 by default.
+
+    ``workspace``: a uint8 device tensor from ``cross_attention_workspace``
+    (reused across calls on one stream), None not to split the keys, or left
+    out to have one taken from torch's caching allocator for this call.
+    """
+    torch = _torch()
+    (batch, queries, heads, dim), qv = _heads(q, "q")
+    k_shape, kv = _heads(k, "k")
+    v_shape, vv = _heads(v, "v")
+    if not k.dim() == v.dim() == q.dim() or k_shape != v_shape:
+        raise ValueError(f"k, v: shapes {tuple(k.shape)}, {tuple(v.shape)} do not go together")
+    if k_shape[0] != batch or k_shape[3] != dim:
+        raise ValueError(f"k: shape {tuple(k.shape)} does not go with q's {tuple(q.shape)}")
+    keys, kv_heads = k_shape[1], k_shape[2]
+    if kv_heads <= 0 or heads <= 0 or heads % kv_heads:
+        raise ValueError(f"q has {heads} heads, not a positive multiple of k's {kv_heads}")
+    if dim <= 0 or dim % 8 or dim > 128:
+        raise ValueError(f"q: head size must be a multiple of 8 up to 128, got {dim}")
+    if scale is None:
+        scale = dim ** -0.5
+    if not (scale > 0 and math.isfinite(scale)):
+        raise ValueError(f"scale must be positive, got {scale}")
+    _opt(kv_lengths, "kv_lengths", torch.int32, (batch,))
+    mask_stride = 0
+    if key_mask is not None:
+        if not isinstance(key_mask, torch.Tensor) or tuple(key_mask.shape) != (batch, keys):
+            raise ValueError(f"key_mask: expected a torch.Tensor of shape {(batch, keys)}")
+        if key_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"key_mask: dtype {key_mask.dtype}, expected bool or uint8")
+        if keys > 1 and key_mask.stride(1) != 1:
+            raise ValueError(f"key_mask: the last dimension must be dense (got strides {key_mask.stride()})")
+        mask_stride = key_mask.stride(0) if batch > 1 else 0
+    ov = _out_heads(out, q, "out")
+    ws = None if workspace is _NO_WORKSPACE else _opt(workspace, "workspace", torch.uint8)
+    dev = _device(q=q, k=k, v=v, kv_lengths=kv_lengths, key_mask=key_mask, out=out, workspace=ws)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        ov = _heads(out, "out")[1]
+    if workspace is _NO_WORKSPACE:
+        ws = cross_attention_workspace(batch, queries, keys, heads, kv_heads, dim, dev)
+    ref = ctypes.byref
+    check(load().dit_cross_attention(
+        ref(qv), ref(kv), ref(vv), _ptr(kv_lengths), _ptr(key_mask), mask_stride, batch, queries,
+        keys, heads, kv_heads, dim, scale, ref(ov), _ptr(ws), 0 if ws is None else ws.numel(),
+        _stream()), "dit_cross_attention")
+    return out

@@ -72,6 +72,17 @@ bool bad_heads(const dit_heads& v) {
   return false;
 }
 
+// Sizes dit_cross_attention does not take.  Rows and their tiles are counted in
+// 32 bits, as are the keys of one tile past the last.
+bool bad_attention(int64_t batch, int64_t queries, int64_t keys, int64_t heads, int64_t kv_heads,
+                   int64_t dim) {
+  if (bad_dim(batch) || bad_dim(queries) || bad_dim(keys) || keys > kMaxDim - 256) return true;
+  if (heads <= 0 || heads > (1 << 16) || kv_heads <= 0 || kv_heads > heads || heads % kv_heads != 0)
+    return true;
+  if (dim <= 0 || dim % 8 != 0 || dim > 128) return true;
+  return batch * heads >= kMaxDim || (queries > 0 && batch * heads >= kMaxDim / queries);
+}
+
 bool finite_positive(float v) { return v > 0.0f && v <= FLT_MAX; }
 
 nvfp4::RotaryHeads rotary_heads(const dit_heads& in, const dit_heads& out, const float* weight,
@@ -413,6 +424,58 @@ int dit_rotary(const dit_heads* q, const dit_heads* q_out, int64_t heads, const 
   a.eps = eps;
   a.inv_dim = (float)(1.0 / (double)dim);
   return hip_status(nvfp4::launch_rotary(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t dit_cross_attention_workspace_bytes(int64_t batch, int64_t queries, int64_t keys,
+                                           int64_t heads, int64_t kv_heads, int64_t dim) {
+  if (bad_attention(batch, queries, keys, heads, kv_heads, dim)) return 0;
+  return nvfp4::attention_workspace_bytes(batch, queries, keys, heads, kv_heads, dim);
+}
+
+int dit_cross_attention(const dit_heads* q, const dit_heads* k, const dit_heads* v,
+                        const int32_t* kv_lengths, const uint8_t* key_mask, int64_t mask_stride,
+                        int64_t batch, int64_t queries, int64_t keys, int64_t heads,
+                        int64_t kv_heads, int64_t dim, float scale, const dit_heads* out,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (bad_dim(batch) || bad_dim(queries) || bad_dim(keys)) return NVFP4_ERR_SHAPE;
+  const bool empty = batch == 0 || queries == 0;
+  if (!q || !k || !v || !out) return NVFP4_ERR_NULL;
+  if (!empty && (!q->data || !out->data || (keys > 0 && (!k->data || !v->data))))
+    return NVFP4_ERR_NULL;
+  if (bad_attention(batch, queries, keys, heads, kv_heads, dim)) return NVFP4_ERR_SHAPE;
+  for (const dit_heads* h : {q, k, v, out})
+    if (bad_heads(*h)) return NVFP4_ERR_SHAPE;
+  // a tile's 64 rows are addressed with 32-bit offsets
+  if (k->token_stride >= (1 << 23) || v->token_stride >= (1 << 23)) return NVFP4_ERR_SHAPE;
+  if (key_mask && (mask_stride < 0 || mask_stride >= ((int64_t)1 << 40))) return NVFP4_ERR_SHAPE;
+  for (const dit_heads* h : {q, k, v, out})
+    if (!aligned(h->data, 16)) return NVFP4_ERR_ALIGN;
+  if (!aligned(kv_lengths, 4) || !aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
+  if (!finite_positive(scale)) return NVFP4_ERR_ARG;
+  int st = check_device();
+  if (st != NVFP4_OK) return st;
+  if (empty) return NVFP4_OK;
+  nvfp4::Attention a{};
+  a.q = static_cast<const uint16_t*>(q->data);
+  a.k = static_cast<const uint16_t*>(k->data);
+  a.v = static_cast<const uint16_t*>(v->data);
+  a.out = static_cast<uint16_t*>(out->data);
+  a.q_batch = q->batch_stride, a.q_token = q->token_stride, a.q_head = q->head_stride;
+  a.k_batch = k->batch_stride, a.k_token = k->token_stride, a.k_head = k->head_stride;
+  a.v_batch = v->batch_stride, a.v_token = v->token_stride, a.v_head = v->head_stride;
+  a.o_batch = out->batch_stride, a.o_token = out->token_stride, a.o_head = out->head_stride;
+  a.lengths = kv_lengths;
+  a.mask = key_mask;
+  a.mask_stride = mask_stride;
+  a.batch = (int)batch;
+  a.queries = (int)queries;
+  a.keys = (int)keys;
+  a.kv_heads = (int)kv_heads;
+  a.group = (int)(heads / kv_heads);
+  a.dim = (int)dim;
+  a.scale = scale;
+  return hip_status(nvfp4::launch_attention(a, workspace, workspace ? workspace_bytes : 0,
+                                            static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -110,4 +110,26 @@ struct Rotary {
 };
 hipError_t launch_rotary(Rotary a, hipStream_t stream);
 
+struct Attention {
+  const uint16_t *q, *k, *v;
+  uint16_t* out;
+  int64_t q_batch, q_token, q_head, k_batch, k_token, k_head;
+  int64_t v_batch, v_token, v_head, o_batch, o_token, o_head;
+  const int32_t* lengths;        // [batch] keys each batch entry sees, or null
+  const uint8_t* mask;           // [batch][keys], nonzero: seen; or null
+  int64_t mask_stride;
+  int batch, queries, keys, kv_heads, group, dim;   // group: query heads per kv head
+  float scale;
+  // filled in by the launch
+  int64_t row_tiles;
+  int splits;
+  float* part;                   // [batch][kv head][split][row][padded dim]
+  float2* stats;                 // [batch][kv head][split][row]: maximum, sum
+};
+// Workspace bytes launch_attention can use to split the keys (0: no split).
+size_t attention_workspace_bytes(int64_t batch, int64_t queries, int64_t keys, int64_t heads,
+                                 int64_t kv_heads, int64_t dim);
+hipError_t launch_attention(Attention a, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
 }  // namespace nvfp4

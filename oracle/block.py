@@ -50,3 +50,23 @@ def rotary(v, positions, radians, axis, rotary_dim, layout="interleaved", magnit
         w = (z[..., a] + 1j * z[..., b]) * turn
         out[..., a], out[..., b] = w.real, w.imag
     return out
+
+
+def attention(q, k, v, visible, scale):
+    """q [batch, queries, heads, dim]; k, v [batch, keys, kv_heads, dim]; visible
+    [batch, keys] booleans.  Keys out of sight are left out of every sum (they
+    may hold anything); a query with none left gets zeros.  Returns the output
+    and the same sum over |v|."""
+    out, size = np.zeros(q.shape), np.zeros(q.shape)
+    group = q.shape[2] // k.shape[2]
+    for b in range(q.shape[0]):
+        at = np.flatnonzero(visible[b])
+        if not at.size:
+            continue
+        for h in range(q.shape[2]):
+            s = (q[b, :, h] @ k[b, at, h // group].T) * scale
+            w = np.exp(s - s.max(1, keepdims=True))
+            w /= w.sum(1, keepdims=True)
+            out[b, :, h] = w @ v[b, at, h // group]
+            size[b, :, h] = w @ np.abs(v[b, at, h // group])
+    return out, size
