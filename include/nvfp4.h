@@ -511,6 +511,42 @@ int dit_cross_attention(const dit_heads* q, const dit_heads* k, const dit_heads*
                         int64_t kv_heads, int64_t dim, float scale, const dit_heads* out,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* Workspace bytes dit_lora_add needs (0 for no rows or invalid sizes). */
+size_t dit_lora_workspace_bytes(int64_t rows, int64_t inner, int64_t rank);
+
+/*
+ * dit_lora_add -- low-rank adapters of many requests beside a projection that
+ * they share (dit_lora_add after nvfp4_gemm on the quantized base weight):
+ *
+ *   out[m] = bf16_rne( epi( y[m] + scales[a] * up[a] (down[a] x[m]) ) ),  a = ids[m]
+ *
+ * and out[m] = bf16_rne(epi(y[m])) for a row whose id is outside [0, adapters)
+ * (-1: no adapter).  An epilogue that belongs after the adapters (the up
+ * projection's GELU) is asked for here, and nvfp4_gemm called without it.
+ *   y_bf16          [rows, outer]; x_bf16 [rows, inner], the projection's input
+ *                   before it was quantized.
+ *   down            [adapters, rank, inner] bf16; up [adapters, outer, rank]
+ *                   bf16.  Adapters of a lower rank are padded with zeros.
+ *   ids             [rows] int32: the adapter of each row, in any order (rows
+ *                   of one request lying together are fastest).
+ *   scales          optional [adapters] fp32.
+ *   rows, outer >= 0; inner and outer multiples of 8; rank a multiple of 8, 8
+ *   to 128; adapters > 0.  bf16 pointers 16-byte aligned.
+ *   epilogue        an nvfp4_epilogue.
+ *   out_bf16        out [rows, outer]; may be y_bf16 itself (rows without an
+ *                   adapter then stay as they are under NVFP4_EPI_NONE).
+ *   out_amax        optional device float: max |out| for nvfp4_quantize's
+ *                   amax_in (set by this call; 0 if out is empty).
+ *   workspace       dit_lora_workspace_bytes bytes, 256-byte aligned, contents
+ *                   on entry irrelevant, owned by the call until it completes.
+ * Sums are binary32; the rank inner products are rounded to bf16 for the second
+ * product.  Deterministic.
+ */
+int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const void* up,
+                 const int32_t* ids, const float* scales, int64_t rows, int64_t inner,
+                 int64_t outer, int64_t rank, int64_t adapters, int epilogue, void* out_bf16,
+                 float* out_amax, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

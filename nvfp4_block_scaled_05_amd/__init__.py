@@ -22,7 +22,7 @@ __all__ = ["Nvfp4Tensor", "Fp8Tensor", "Nvfp4Error", "load", "abi_version", "sta
            "gemm_quantized", "gemm_bf16", "layer_is_quantized", "quantize_weight", "linear",
            "fp8_quantize", "fp8_gemm", "fp8_gemm_workspace",
            "gated_norm", "RotaryPlan", "rotary_plan", "rotary",
-           "cross_attention", "cross_attention_workspace"]
+           "cross_attention", "cross_attention_workspace", "lora_add", "lora_workspace"]
 
 
 _TORCH = None
@@ -413,4 +413,4 @@ def linear(x, weight, name, bias=None, epilogue="none", pattern=None):
 
 # the operators between the linears use the checks above
 from .block_ops import (RotaryPlan, cross_attention, cross_attention_workspace,  # noqa: E402
-                        gated_norm, rotary, rotary_plan)
+                        gated_norm, lora_add, lora_workspace, rotary, rotary_plan)

@@ -60,6 +60,9 @@ SIGNATURES = {
                               _I64, _I64, _INT, _INT, _F, _F, _P, _P, _P, _P]),
     "dit_rotary": (_INT, [_HEADS, _HEADS, _I64, _HEADS, _HEADS, _I64, _P, _I64, _P, _P, _F, _P, _P,
                           _F, _I64, _I64, _I64, _I64, _INT, _P]),
+    "dit_lora_workspace_bytes": (ctypes.c_size_t, [_I64] * 3),
+    "dit_lora_add": (_INT, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _INT, _P, _P, _P,
+                            ctypes.c_size_t, _P]),
     "dit_cross_attention_workspace_bytes": (ctypes.c_size_t, [_I64] * 6),
     "dit_cross_attention": (_INT, [_HEADS, _HEADS, _HEADS, _P, _P, _I64, _I64, _I64, _I64, _I64,
                                    _I64, _I64, _F, _HEADS, _P, ctypes.c_size_t, _P]),

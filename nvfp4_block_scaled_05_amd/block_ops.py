@@ -11,7 +11,7 @@ import ctypes
 import math
 from collections import namedtuple
 
-from . import _NO_WORKSPACE, _device, _opt, _ptr, _stream, _tensor, _torch
+from . import _NO_WORKSPACE, _device, _epilogue, _matrix, _opt, _ptr, _stream, _tensor, _torch
 from ._binding import DitHeads, check, load
 
 NORMS = {"none": 0, "layer": 1, "rms": 2}
@@ -327,4 +327,62 @@ def cross_attention(q, k, v, kv_lengths=None, key_mask=None, scale=None, out=Non
         ref(qv), ref(kv), ref(vv), _ptr(kv_lengths), _ptr(key_mask), mask_stride, batch, queries,
         keys, heads, kv_heads, dim, scale, ref(ov), _ptr(ws), 0 if ws is None else ws.numel(),
         _stream()), "dit_cross_attention")
+    return out
+
+
+def lora_workspace(rows, inner, rank, device="cuda"):
+    """A workspace for ``lora_add`` on these sizes."""
+    nbytes = load().dit_lora_workspace_bytes(rows, inner, rank)
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+
+
+def lora_add(y, x, down, up, ids, scales=None, epilogue="none", y_amax=None, out=None,
+             workspace=_NO_WORKSPACE):
+    """Low-rank adapters of many requests beside a projection they share:
+
+        out[m] = epi(y[m] + scales[a] * up[a] @ (down[a] @ x[m])),  a = ids[m]
+
+    y: [rows, outer], the shared projection's output (``gemm`` without an
+    epilogue); x: [rows, inner], its input before quantization; down:
+    [adapters, rank, inner], up: [adapters, outer, rank], lower ranks padded
+    with zeros; ids: int32 [rows], -1 for a row without an adapter (any value
+    outside [0, adapters) is); scales: optional float32 [adapters].  epilogue:
+    "none" or "gelu", applied to every row after the sum; y_amax: optional
+    one-element float32 device tensor, set to max |out| for ``quantize``.
+    inner and outer are multiples of 8, rank a multiple of 8 up to 128.
+
+    Returns out: y itself, updated in place, unless ``out`` is given.
+    ``workspace``: from ``lora_workspace`` (reused across calls on one stream),
+    or left out to have one taken from torch's caching allocator for this call.
+    """
+    torch = _torch()
+    rows, outer = _matrix(y, "y", torch.bfloat16)
+    x_rows, inner = _matrix(x, "x", torch.bfloat16)
+    if x_rows != rows:
+        raise ValueError(f"x: {x_rows} rows, y has {rows}")
+    if not isinstance(down, torch.Tensor) or down.dim() != 3:
+        raise ValueError("down: expected a 3-D torch.Tensor")
+    adapters, rank, _ = down.shape
+    if adapters <= 0 or rank <= 0 or rank % 8 or rank > 128:
+        raise ValueError(f"down: needs adapters and a rank that is a multiple of 8 up to 128, got {tuple(down.shape)}")
+    if inner <= 0 or inner % 8 or outer % 8:
+        raise ValueError(f"inner and outer must be multiples of 8, got {inner} and {outer}")
+    _tensor(down, "down", torch.bfloat16, (adapters, rank, inner))
+    _tensor(up, "up", torch.bfloat16, (adapters, outer, rank))
+    _tensor(ids, "ids", torch.int32, (rows,))
+    _opt(scales, "scales", torch.float32, (adapters,))
+    epi = _epilogue(epilogue)
+    _opt(y_amax, "y_amax", torch.float32)
+    _opt(out, "out", torch.bfloat16, (rows, outer))
+    ws = None if workspace is _NO_WORKSPACE else _tensor(workspace, "workspace", torch.uint8)
+    dev = _device(y=y, x=x, down=down, up=up, ids=ids, scales=scales, y_amax=y_amax, out=out,
+                  workspace=ws)
+    if out is None:
+        out = y
+    if ws is None:
+        ws = lora_workspace(rows, inner, rank, dev)
+    check(load().dit_lora_add(y.data_ptr(), x.data_ptr(), down.data_ptr(), up.data_ptr(),
+                              ids.data_ptr(), _ptr(scales), rows, inner, outer, rank, adapters, epi,
+                              out.data_ptr(), _ptr(y_amax), ws.data_ptr(), ws.numel(), _stream()),
+          "dit_lora_add")
     return out

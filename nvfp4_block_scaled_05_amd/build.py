@@ -48,7 +48,8 @@ SANITIZE_FLAGS = [
 ]
 
 SOURCES = ["quantize.hip", "gemm_nvfp4.hip", "gemm_nvfp4_quant.hip", "gemm.hip", "fp8.hip",
-           "norm.hip", "rotary.hip", "attention.hip", "api.cpp"]
+           "norm.hip", "rotary.hip", "attention.hip", "lora.hip",
+           "api.cpp"]
 # test-only library: conversion probes and the calibration kernels of the
 # roofline measurement (isa_probe.h, calib.h beside the sources)
 PROBE_SOURCES = ["isa_probe.hip", "calib.hip"]

@@ -83,6 +83,13 @@ bool bad_attention(int64_t batch, int64_t queries, int64_t keys, int64_t heads, 
   return batch * heads >= kMaxDim || (queries > 0 && batch * heads >= kMaxDim / queries);
 }
 
+// Sizes dit_lora_add does not take (element offsets within a row are 32-bit).
+bool bad_lora(int64_t rows, int64_t inner, int64_t outer, int64_t rank, int64_t adapters) {
+  if (bad_dim(rows) || inner <= 0 || inner % 8 != 0 || inner >= (1 << 28)) return true;
+  if (outer < 0 || outer % 8 != 0 || outer >= (1 << 28)) return true;
+  return rank <= 0 || rank % 8 != 0 || rank > 128 || adapters <= 0 || adapters >= kMaxDim;
+}
+
 bool finite_positive(float v) { return v > 0.0f && v <= FLT_MAX; }
 
 nvfp4::RotaryHeads rotary_heads(const dit_heads& in, const dit_heads& out, const float* weight,
@@ -476,6 +483,47 @@ int dit_cross_attention(const dit_heads* q, const dit_heads* k, const dit_heads*
   a.scale = scale;
   return hip_status(nvfp4::launch_attention(a, workspace, workspace ? workspace_bytes : 0,
                                             static_cast<hipStream_t>(stream)));
+}
+
+size_t dit_lora_workspace_bytes(int64_t rows, int64_t inner, int64_t rank) {
+  if (rows <= 0 || bad_lora(rows, inner, 8, rank, 1)) return 0;
+  return nvfp4::lora_workspace_bytes(rows, inner, rank);
+}
+
+int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const void* up,
+                 const int32_t* ids, const float* scales, int64_t rows, int64_t inner,
+                 int64_t outer, int64_t rank, int64_t adapters, int epilogue, void* out_bf16,
+                 float* out_amax, void* workspace, size_t workspace_bytes, void* stream) {
+  if (bad_dim(rows) || bad_dim(outer)) return NVFP4_ERR_SHAPE;
+  const bool empty = rows == 0 || outer == 0;
+  if (!empty && (!y_bf16 || !x_bf16 || !down || !up || !ids || !out_bf16 || !workspace))
+    return NVFP4_ERR_NULL;
+  if (bad_lora(rows, inner, outer, rank, adapters)) return NVFP4_ERR_SHAPE;
+  for (const void* p : {y_bf16, x_bf16, down, up, static_cast<const void*>(out_bf16)})
+    if (!aligned(p, 16)) return NVFP4_ERR_ALIGN;
+  if (!aligned(ids, 4) || !aligned(scales, 4) || !aligned(out_amax, 4) || !aligned(workspace, 256))
+    return NVFP4_ERR_ALIGN;
+  if (epilogue != NVFP4_EPI_NONE && epilogue != NVFP4_EPI_GELU) return NVFP4_ERR_ARG;
+  if (!empty && workspace_bytes < nvfp4::lora_workspace_bytes(rows, inner, rank))
+    return NVFP4_ERR_WORKSPACE;
+  int st = check_device();
+  if (st != NVFP4_OK) return st;
+  nvfp4::Lora a{};
+  a.y = static_cast<const uint16_t*>(y_bf16);
+  a.x = static_cast<const uint16_t*>(x_bf16);
+  a.down = static_cast<const uint16_t*>(down);
+  a.up = static_cast<const uint16_t*>(up);
+  a.ids = ids;
+  a.scales = scales;
+  a.rows = rows;
+  a.inner = (int)inner;
+  a.outer = (int)outer;
+  a.rank = (int)rank;
+  a.adapters = (int)adapters;
+  a.epilogue = epilogue;
+  a.out = static_cast<uint16_t*>(out_bf16);
+  a.amax = reinterpret_cast<uint32_t*>(out_amax);
+  return hip_status(nvfp4::launch_lora(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

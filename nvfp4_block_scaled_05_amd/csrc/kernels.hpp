@@ -132,4 +132,21 @@ size_t attention_workspace_bytes(int64_t batch, int64_t queries, int64_t keys, i
 hipError_t launch_attention(Attention a, void* workspace, size_t workspace_bytes,
                             hipStream_t stream);
 
+struct Lora {
+  const uint16_t *y, *x;         // [rows, outer], [rows, inner]
+  const uint16_t *down, *up;     // [adapters, rank, inner], [adapters, outer, rank]
+  const int32_t* ids;            // [rows]; outside [0, adapters): no adapter
+  const float* scales;           // [adapters], or null: 1
+  int64_t rows;
+  int inner, outer, rank, adapters, epilogue;
+  uint16_t* out;                 // may be y
+  uint32_t* amax;                // or null
+  // filled in by the launch
+  float* t;                      // [slices][rows][padded rank]
+  int slices, slice;
+  bool skip_idle;
+};
+size_t lora_workspace_bytes(int64_t rows, int64_t inner, int64_t rank);
+hipError_t launch_lora(Lora a, void* workspace, hipStream_t stream);
+
 }  // namespace nvfp4

@@ -70,3 +70,26 @@ def attention(q, k, v, visible, scale):
             out[b, :, h] = w @ v[b, at, h // group]
             size[b, :, h] = w @ np.abs(v[b, at, h // group])
     return out, size
+
+
+def lora_add(y, x, down, up, ids, scales=None):
+    """y + s_a up_a (down_a x) per row, a = ids[row] (rows with an id outside the
+    adapters: y).  Returns the sum and, per element, sum_j |up| s |down| |x|
+    taken over both products (the size of its terms)."""
+    out, size = y.copy(), np.zeros(y.shape)
+    for a in range(down.shape[0]):
+        m = ids == a
+        s = 1.0 if scales is None else scales[a]
+        out[m] += s * (x[m] @ down[a].T) @ up[a].T
+        size[m] = abs(s) * (np.abs(x[m]) @ np.abs(down[a]).T) @ np.abs(up[a]).T
+    return out, size
+
+
+def lora_rank_size(x, down, up, ids, scales=None):
+    """Per element sum_j |up_j| |s t_j|: the size of the second product's terms."""
+    size = np.zeros((x.shape[0], up.shape[1]))
+    for a in range(down.shape[0]):
+        m = ids == a
+        s = 1.0 if scales is None else scales[a]
+        size[m] = np.abs(s * (x[m] @ down[a].T)) @ np.abs(up[a]).T
+    return size

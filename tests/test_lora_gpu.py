@@ -1,0 +1,145 @@
+"""lora_add against its definition in binary64, element by element.
+
+Bounds, fixed before the first run: the output rounding is UBF of the value;
+each of the rank inner products t_j is rounded to bf16, so their sum with up is
+off by UBF sum |up_j t_j|; the binary32 sums (inner + rank terms and a few
+more) add (inner + rank + 32) U32 of the size of all terms, and the sum with y
+2 U32 of the value.  GELU's slope is at most 1.13 and its approximation 2e-5 of
+its value."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scaled_05_amd as nv
+import oracle.block as ob
+from nvfp4_block_scaled_05_amd.graph import capture
+from tests.block_util import U32, UBF, assert_within, f64, normal
+
+pytestmark = pytest.mark.gpu
+
+
+def make(seed, rows, inner, outer, rank, adapters, ids=None):
+    rng = np.random.default_rng(seed)
+    if ids is None:
+        ids = rng.integers(-1, adapters, rows)
+    return dict(y=normal(rng, (rows, outer)), x=normal(rng, (rows, inner)),
+                down=normal(rng, (adapters, rank, inner), inner ** -0.5),
+                up=normal(rng, (adapters, outer, rank), 0.5),
+                ids=torch.from_numpy(np.asarray(ids)).int().cuda(),
+                scales=torch.from_numpy(rng.random(adapters) + 0.5).float().cuda())
+
+
+def gelu(z):
+    return 0.5 * z * np.vectorize(math.erfc)(-z / math.sqrt(2)) if z.size else z
+
+
+def check(got, d, epilogue="none"):
+    a = {k: f64(v) for k, v in d.items()}
+    a["ids"] = d["ids"].cpu().numpy()
+    want, size = ob.lora_add(**a)
+    args = {k: a[k] for k in ("x", "down", "up", "ids", "scales") if k in a}
+    inner, rank = d["x"].shape[1], d["down"].shape[1]
+    err = (UBF * ob.lora_rank_size(**args) + (inner + rank + 32) * U32 * size) * 1.01 + 2 * U32 * np.abs(want)
+    if epilogue == "gelu":
+        want = gelu(want)
+        err = 1.13 * err + 2e-5 * np.abs(want)
+    assert_within(got, want, err + UBF * np.abs(want), epilogue)
+
+
+@pytest.mark.parametrize("epilogue", ["none", "gelu"])
+@pytest.mark.parametrize("rows,inner,outer,rank,adapters", [
+    (1, 8, 8, 8, 1), (1, 64, 64, 16, 2), (15, 40, 24, 8, 3), (16, 256, 128, 16, 2), (17, 264, 136, 24, 5),
+    (33, 1024, 520, 32, 4), (64, 72, 2056, 40, 3), (100, 2056, 64, 64, 6), (48, 3072, 1024, 16, 12),
+    (31, 520, 88, 72, 2), (129, 512, 264, 128, 3), (700, 136, 72, 16, 1)])
+def test_shapes(rows, inner, outer, rank, adapters, epilogue):
+    d = make(rows + inner, rows, inner, outer, rank, adapters)
+    out = torch.empty_like(d["y"])
+    before = d["y"].clone()
+    got = nv.lora_add(**d, epilogue=epilogue, out=out)
+    assert got is out and torch.equal(d["y"], before)
+    check(got, d, epilogue)
+    # in place: the same bits
+    assert torch.equal(nv.lora_add(**d, epilogue=epilogue), out) and torch.equal(d["y"], out)
+
+
+def test_requests_in_runs_and_any_order():
+    rng = np.random.default_rng(1)
+    runs = np.repeat([2, -1, 0, 1, 2, 7, 3], [40, 16, 1, 90, 0, 5, 31])     # 7: not an adapter
+    d = make(2, len(runs), 320, 200, 16, 4, runs)
+    a = nv.lora_add(**d, out=torch.empty_like(d["y"]))
+    check(a, d)
+    p = torch.from_numpy(rng.permutation(len(runs))).cuda()
+    e = dict(d, y=d["y"][p].contiguous(), x=d["x"][p].contiguous(), ids=d["ids"][p].contiguous())
+    assert torch.equal(nv.lora_add(**e), a[p])
+
+
+def test_one_adapter_a_row():
+    d = make(3, 70, 512, 136, 16, 70, np.arange(70)[::-1].copy())
+    check(nv.lora_add(**d, out=torch.empty_like(d["y"])), d)
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 4, 2 ** 31 - 1])
+def test_rows_without_an_adapter(bad):
+    d = make(4, 50, 128, 72, 8, 4, np.full(50, bad))
+    before = d["y"].clone()
+    assert torch.equal(nv.lora_add(**d), before)
+    amax = torch.zeros(1, device="cuda")
+    assert torch.equal(nv.lora_add(**d, y_amax=amax, out=torch.empty_like(before)), before)
+    assert amax.item() == before.abs().max().item()
+
+
+def test_other_requests_do_not_reach_a_row():
+    d = make(5, 32, 256, 72, 16, 3, np.arange(32) % 3)
+    want = nv.lora_add(**d, out=torch.empty_like(d["y"]))
+    d["down"][1] = float("nan")
+    d["up"][1] = float("inf")
+    d["x"][4] = float("nan")                       # a row of adapter 1
+    got = nv.lora_add(**d, out=torch.empty_like(d["y"]))
+    mine = torch.arange(32, device="cuda") % 3 == 1
+    assert torch.equal(got[~mine], want[~mine]) and torch.isnan(got[mine]).all()
+
+
+def test_no_scales_and_padded_rank():
+    d = make(6, 40, 256, 136, 32, 3)
+    d["down"][1, 8:] = 0                           # adapter 1 is of rank 8
+    d["up"][1, :, 8:] = float(0)
+    del d["scales"]
+    check(nv.lora_add(**d, out=torch.empty_like(d["y"])), d)
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+@pytest.mark.parametrize("epilogue", ["none", "gelu"])
+def test_amax_feeds_the_quantizer(rows, epilogue):
+    d = make(7, rows, 264, 320, 16, 4)
+    amax = torch.full((1,), 1e30, device="cuda")
+    h = nv.lora_add(**d, epilogue=epilogue, y_amax=amax)
+    assert amax.item() == h.abs().max().item()
+    a, b = nv.quantize(h, amax=amax), nv.quantize(h)
+    assert all(torch.equal(u, v) for u, v in zip(a[:3], b[:3]))
+
+
+def test_empty_calls():
+    d = make(8, 0, 64, 64, 8, 1)
+    amax = torch.ones(1, device="cuda")
+    assert nv.lora_add(**d, y_amax=amax).shape == (0, 64) and amax.item() == 0
+
+
+def test_captured_and_workspace_reuse():
+    d = make(9, 40, 1024, 264, 16, 4)
+    out = torch.empty_like(d["y"])
+    amax = torch.zeros(1, device="cuda")
+    ws = nv.lora_workspace(40, 1024, 16)
+    ws.fill_(255)
+    g = capture(lambda: nv.lora_add(**d, epilogue="gelu", y_amax=amax, out=out, workspace=ws))
+    for i in range(3):
+        d["ids"].copy_(d["ids"].roll(7))
+        d["x"].mul_(-1)
+        want_max = torch.zeros(1, device="cuda")
+        want = nv.lora_add(**d, epilogue="gelu", y_amax=want_max, out=torch.empty_like(out))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(amax, want_max)
