@@ -402,13 +402,23 @@ def quantize_weight(w):
     return quantize(w)
 
 
-def linear(x, weight, name, bias=None, epilogue="none", pattern=None):
+def linear(x, weight, name, bias=None, epilogue="none", pattern=None, lora=None):
     """One linear layer as the patched model runs it: NVFP4 (quantize x, then
     the block-scaled GEMM against the pre-quantized ``weight``) when the layer
-    predicate selects it, else the bf16 passthrough on the bf16 ``weight``."""
+    predicate selects it, else the bf16 passthrough on the bf16 ``weight``.
+
+    ``lora``: optional (down, up, ids, scales), the adapters of the rows'
+    requests (``lora_add``): added to the layer's output from the unquantized x,
+    before the epilogue."""
+    own = "none" if lora is not None else epilogue
     if layer_is_quantized(name, pattern):
-        return gemm(quantize(x), weight, bias=bias, epilogue=epilogue)
-    return gemm_bf16(x, weight, bias=bias, epilogue=epilogue)
+        y = gemm(quantize(x), weight, bias=bias, epilogue=own)
+    else:
+        y = gemm_bf16(x, weight, bias=bias, epilogue=own)
+    if lora is None:
+        return y
+    down, up, ids, scales = lora
+    return lora_add(y, x, down, up, ids, scales=scales, epilogue=epilogue)
 
 
 # the operators between the linears use the checks above

@@ -58,7 +58,8 @@ def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weigh
     shift: [batch, channels] (batch 1 for a 2-D x), all bf16 or all float32, dense
     rows of any stride that is a multiple of 8, so chunks of the modulation
     linear's output are taken as they are.  weight, bias, post_weight: float32
-    [channels].  norm, post_norm: "none", "layer" or "rms".  amax: optional
+    [channels].  norm, post_norm: "none", "layer" or "rms"; norm None: only r
+    is wanted (the last residual of a model), h is None.  amax: optional
     one-element float32 device tensor, set to max |h| for ``quantize``.
 
     Returns (r, h): r in x's type (x itself when there is no y), h in bf16.
@@ -71,7 +72,7 @@ def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weigh
     _tensor(x, "x", torch.float32 if fp32 else torch.bfloat16, min_numel=0)
     if channels <= 0 or channels % 8 or channels > 16384:
         raise ValueError(f"x: channels must be a positive multiple of 8 up to 16384, got {channels}")
-    norm_id = _choice(norm, NORMS, "norm")
+    norm_id = _choice("none" if norm is None else norm, NORMS, "norm")
     post_id = _choice(post_norm, NORMS, "post_norm")
     if y is None:
         for name, v in (("gate", gate), ("post_weight", post_weight), ("residual_out", residual_out)):
@@ -79,6 +80,13 @@ def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weigh
                 raise ValueError(f"{name} needs y")
         if post_id or residual_scale != 1.0:
             raise ValueError("post_norm and residual_scale need y")
+    if norm is None:
+        for name, v in (("scale", scale), ("shift", shift), ("weight", weight), ("bias", bias),
+                        ("amax", amax), ("out", out)):
+            if v is not None:
+                raise ValueError(f"{name} needs a norm")
+        if y is None:
+            raise ValueError("norm None needs y")
     if not (eps > 0 and math.isfinite(eps) and math.isfinite(residual_scale)):
         raise ValueError(f"eps must be positive, residual_scale finite; got {eps}, {residual_scale}")
     _opt(y, "y", torch.bfloat16, x.shape, 0)
@@ -95,14 +103,14 @@ def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weigh
     _opt(residual_out, "residual_out", x.dtype, x.shape, 0)
     dev = _device(x=x, y=y, gate=gate, scale=scale, shift=shift, weight=weight, bias=bias,
                   post_weight=post_weight, amax=amax, out=out, residual_out=residual_out)
-    if out is None:
+    if out is None and norm is not None:
         out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
     if residual_out is None and y is not None:
         residual_out = torch.empty_like(x)
     check(load().dit_gated_norm(
         x.data_ptr(), fp32, _ptr(y), _ptr(gate), strides[0], _ptr(scale), strides[1], _ptr(shift),
         strides[2], mod == torch.float32, _ptr(weight), _ptr(bias), _ptr(post_weight), batch, tokens,
-        channels, norm_id, post_id, residual_scale, eps, _ptr(residual_out), out.data_ptr(),
+        channels, norm_id, post_id, residual_scale, eps, _ptr(residual_out), _ptr(out),
         _ptr(amax), _stream()), "dit_gated_norm")
     return (x if y is None else residual_out), out
 
