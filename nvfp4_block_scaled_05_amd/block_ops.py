@@ -19,6 +19,20 @@ ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
 ROTARY_SCALINGS = ("none", "linear", "ntk", "yarn")
 
 
+def _place(first, named):
+    """_device on a dict of tensors, for calls of a few microseconds: the common
+    case (all on the current GPU) is one integer comparison a tensor.  Returns
+    the device of ``first``, one of them."""
+    at = first.get_device()
+    good = at >= 0
+    for t in named.values():
+        if t is not None and t.get_device() != at:
+            good = False
+    if not good or at != _torch().cuda.current_device():
+        return _device(**named)                      # raises, with the name
+    return first.device
+
+
 def _choice(value, choices, name):
     if value not in choices:
         raise ValueError(f"{name} must be one of {sorted(choices)}, got {value!r}")
@@ -90,26 +104,32 @@ def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weigh
     if not (eps > 0 and math.isfinite(eps) and math.isfinite(residual_scale)):
         raise ValueError(f"eps must be positive, residual_scale finite; got {eps}, {residual_scale}")
     _opt(y, "y", torch.bfloat16, x.shape, 0)
-    mod = next((t.dtype for t in (gate, scale, shift) if isinstance(t, torch.Tensor)), torch.bfloat16)
-    if mod not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"gate, scale, shift: dtype {mod}, expected bfloat16 or float32")
-    strides = [0 if t is None else _vector(t, name, batch, channels, mod)
-               for name, t in (("gate", gate), ("scale", scale), ("shift", shift))]
+    mod = None                                # the type of the first vector; all have it
+    strides = [0, 0, 0]
+    for i, v in enumerate((gate, scale, shift)):
+        if v is not None:
+            name = ("gate", "scale", "shift")[i]
+            if mod is None:
+                mod = getattr(v, "dtype", None)
+                if mod not in (torch.bfloat16, torch.float32):
+                    raise ValueError(f"{name}: dtype {mod}, expected bfloat16 or float32")
+            strides[i] = _vector(v, name, batch, channels, mod)
     _opt(weight, "weight", torch.float32, (channels,))
     _opt(bias, "bias", torch.float32, (channels,))
     _opt(post_weight, "post_weight", torch.float32, (channels,))
     _opt(amax, "amax", torch.float32)
     _opt(out, "out", torch.bfloat16, x.shape, 0)
     _opt(residual_out, "residual_out", x.dtype, x.shape, 0)
-    dev = _device(x=x, y=y, gate=gate, scale=scale, shift=shift, weight=weight, bias=bias,
-                  post_weight=post_weight, amax=amax, out=out, residual_out=residual_out)
+    dev = _place(x, {"x": x, "y": y, "gate": gate, "scale": scale, "shift": shift, "weight": weight,
+                  "bias": bias, "post_weight": post_weight, "amax": amax, "out": out,
+                  "residual_out": residual_out})
     if out is None and norm is not None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(x) if not fp32 else torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
     if residual_out is None and y is not None:
         residual_out = torch.empty_like(x)
     check(load().dit_gated_norm(
         x.data_ptr(), fp32, _ptr(y), _ptr(gate), strides[0], _ptr(scale), strides[1], _ptr(shift),
-        strides[2], mod == torch.float32, _ptr(weight), _ptr(bias), _ptr(post_weight), batch, tokens,
+        strides[2], mod is torch.float32, _ptr(weight), _ptr(bias), _ptr(post_weight), batch, tokens,
         channels, norm_id, post_id, residual_scale, eps, _ptr(residual_out), _ptr(out),
         _ptr(amax), _stream()), "dit_gated_norm")
     return (x if y is None else residual_out), out
@@ -186,21 +206,36 @@ def _heads(t, name, out=False):
         raise ValueError(f"{name}: expected a 3-D or 4-D torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 3:
-        shape, stride = (1, *shape), (0, *stride)
-    if shape[3] > 1 and stride[3] != 1:
+    if t.dim() == 4:
+        (b, n, h, d), (sb, sn, sh, sd) = t.shape, t.stride()
+    else:
+        (n, h, d), (sn, sh, sd) = t.shape, t.stride()
+        b, sb = 1, 0
+    if sd != 1 and d > 1:
         raise ValueError(f"{name}: the last dimension must be dense (got strides {tuple(t.stride())})")
-    view = [0 if n <= 1 else s for n, s in zip(shape[:3], stride[:3])]
-    if any(s % 8 for s in view):
+    # the stride of a dimension that is never stepped along means nothing
+    if b <= 1:
+        sb = 0
+    if n <= 1:
+        sn = 0
+    if h <= 1:
+        sh = 0
+    if (sb | sn | sh) & 7:
         raise ValueError(f"{name}: strides must be multiples of 8 (got {tuple(t.stride())})")
     if out:
-        reach = shape[3]
-        for s, n in sorted((s, n) for s, n in zip(view, shape[:3]) if n > 1):
+        reach = d
+        for s, size in sorted((s, size) for s, size in ((sb, b), (sn, n), (sh, h)) if size > 1):
             if s < reach:
                 raise ValueError(f"{name}: elements overlap (strides {tuple(t.stride())})")
-            reach = s * n
-    return tuple(shape), DitHeads(t.data_ptr(), *view)
+            reach = s * size
+    return (b, n, h, d), DitHeads(t.data_ptr(), sb, sn, sh)
+
+
+def _new_heads(shape, shape4, dev):
+    """A new dense output of ``shape`` (``shape4`` with its batch) and its C view."""
+    t = _torch().empty(shape, dtype=_torch().bfloat16, device=dev)
+    _, n, h, d = shape4
+    return t, DitHeads(t.data_ptr(), n * h * d, h * d, d)
 
 
 def _out_heads(out, like, name):
@@ -255,14 +290,12 @@ def rotary(q, positions, plan, k=None, layout="interleaved", q_weight=None, k_we
     _opt(k_weight, "k_weight", torch.float32, (dim,))
     qo = _out_heads(out, q, "out")
     ko = None if k is None else _out_heads(k_out, k, "k_out")
-    dev = _device(q=q, k=k, positions=positions, turns=plan.turns, axis=plan.axis,
-                  q_weight=q_weight, k_weight=k_weight, out=out, k_out=k_out)
+    dev = _place(q, {"q": q, "k": k, "positions": positions, "turns": plan.turns, "axis": plan.axis,
+                  "q_weight": q_weight, "k_weight": k_weight, "out": out, "k_out": k_out})
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        qo = _heads(out, "out")[1]
+        out, qo = _new_heads(q.shape, shape, dev)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
-        ko = _heads(k_out, "k_out")[1]
+        k_out, ko = _new_heads(k.shape, k_shape, dev)
     ref = ctypes.byref
     check(load().dit_rotary(
         ref(qv), ref(qo), heads, kv and ref(kv), ko and ref(ko), kv_heads, positions.data_ptr(),
@@ -324,10 +357,10 @@ def cross_attention(q, k, v, kv_lengths=None, key_mask=None, scale=None, out=Non
         mask_stride = key_mask.stride(0) if batch > 1 else 0
     ov = _out_heads(out, q, "out")
     ws = None if workspace is _NO_WORKSPACE else _opt(workspace, "workspace", torch.uint8)
-    dev = _device(q=q, k=k, v=v, kv_lengths=kv_lengths, key_mask=key_mask, out=out, workspace=ws)
+    dev = _place(q, {"q": q, "k": k, "v": v, "kv_lengths": kv_lengths, "key_mask": key_mask,
+                  "out": out, "workspace": ws})
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        ov = _heads(out, "out")[1]
+        out, ov = _new_heads(q.shape, (batch, queries, heads, dim), dev)
     if workspace is _NO_WORKSPACE:
         ws = cross_attention_workspace(batch, queries, keys, heads, kv_heads, dim, dev)
     ref = ctypes.byref
@@ -383,8 +416,8 @@ def lora_add(y, x, down, up, ids, scales=None, epilogue="none", y_amax=None, out
     _opt(y_amax, "y_amax", torch.float32)
     _opt(out, "out", torch.bfloat16, (rows, outer))
     ws = None if workspace is _NO_WORKSPACE else _tensor(workspace, "workspace", torch.uint8)
-    dev = _device(y=y, x=x, down=down, up=up, ids=ids, scales=scales, y_amax=y_amax, out=out,
-                  workspace=ws)
+    dev = _place(y, {"y": y, "x": x, "down": down, "up": up, "ids": ids, "scales": scales,
+                  "y_amax": y_amax, "out": out, "workspace": ws})
     if out is None:
         out = y
     if ws is None:

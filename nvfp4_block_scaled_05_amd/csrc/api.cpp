@@ -80,12 +80,15 @@ bool bad_attention(int64_t batch, int64_t queries, int64_t keys, int64_t heads, 
   if (heads <= 0 || heads > (1 << 16) || kv_heads <= 0 || kv_heads > heads || heads % kv_heads != 0)
     return true;
   if (dim <= 0 || dim % 8 != 0 || dim > 128) return true;
-  return batch * heads >= kMaxDim || (queries > 0 && batch * heads >= kMaxDim / queries);
+  if (batch * heads >= kMaxDim || (queries > 0 && batch * heads >= kMaxDim / queries)) return true;
+  // at most 2^23 workgroups before the keys are split (only small calls are)
+  return batch * kv_heads * ((queries * (heads / kv_heads) + 127) / 128) > (1 << 23);
 }
 
 // Sizes dit_lora_add does not take (element offsets within a row are 32-bit).
 bool bad_lora(int64_t rows, int64_t inner, int64_t outer, int64_t rank, int64_t adapters) {
-  if (bad_dim(rows) || inner <= 0 || inner % 8 != 0 || inner >= (1 << 28)) return true;
+  if (bad_dim(rows) || rows >= (1 << 27)) return true;
+  if (inner <= 0 || inner % 8 != 0 || inner >= (1 << 28)) return true;
   if (outer < 0 || outer % 8 != 0 || outer >= (1 << 28)) return true;
   return rank <= 0 || rank % 8 != 0 || rank > 128 || adapters <= 0 || adapters >= kMaxDim;
 }

@@ -1,6 +1,8 @@
 // dit_cross_attention: softmax(scale q k^T) v of query heads over the keys and
 // values of an encoder (or of any other length), with key heads shared by
 // groups of query heads, key lengths and a key mask.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "kernels.hpp"
 
@@ -11,7 +13,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kKeys = 64;                       // keys per tile
 constexpr uint32_t kNoData = 0x80000000u;       // a lane offset past every tile: loads zeros
 
 // Where a 16-byte piece of a K / V row lies in its LDS row: pieces are permuted
@@ -27,224 +28,450 @@ __device__ __forceinline__ int v_swizzle(int key) {
   return DP == 128 ? ((key & 3) << 2) : (((key >> 1) & 1) << 2);
 }
 
-// 16 bytes per lane from base + offset straight into LDS; offsets from kNoData
-// up are out of the resource's range and load zeros.
-__device__ __forceinline__ void tile_load(const void* base, uint32_t offset, void* lds) {
+// 16 bytes per lane from base + offset straight into LDS, `to` bytes into the
+// array `lds`; offsets from kNoData up are out of the resource's range and load
+// zeros.  (LDS positions are an array and one offset throughout: the compiler
+// then still knows which array an access is to, and does not make reads of one
+// wait for loads in flight into the other.)
+__device__ __forceinline__ void tile_load(const void* base, uint32_t offset, uint8_t* lds, int to) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<void*>(base), (short)0, (int)kNoData, kBufferWord3);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
-                                           offset, 0, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      r, (__attribute__((address_space(3))) void*)(lds + to), 16, offset, 0, 0, 0);
 }
 
-__device__ __forceinline__ s16x4 transposed4(const uint8_t* lds) {
+__device__ __forceinline__ s16x4 transposed4(const uint8_t* lds, int at) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (__attribute__((address_space(3))) s16x4*)const_cast<uint8_t*>(lds));
+      (__attribute__((address_space(3))) s16x4*)const_cast<uint8_t*>(lds + at));
 }
 
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
-// The other half-wave's value of `v` (lane ^ 32).
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+// This lane's value with the one of lane ^ 32 (permlane32_swap of v with itself
+// leaves the lower half's values in the first result, the upper's in the second).
+__device__ __forceinline__ float halves_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
-template <int DP, int RB>
+// The running state of a wave's 32 query rows over tiles of 32 * KB keys.
+template <int DP, int KB>
 struct Attend {
   static constexpr int kSteps = DP / 16;        // MFMA steps over the head size
   static constexpr int kBlocks = DP / 32;       // 32-row blocks of the transposed output
   static constexpr int kPieces = DP / 8;        // 16-byte pieces of a row
-  static constexpr int kLoads = kKeys * kPieces / 256;   // per thread and operand
-  static constexpr int kRows = 4 * 32 * RB;     // query rows a workgroup takes
-  static constexpr int kTileBytes = kKeys * DP * 2;
+  static constexpr int kKeys = 32 * KB;
+  static constexpr int kRowBytes = DP * 2;
+  static constexpr int kTileBytes = kKeys * kRowBytes;
+  static constexpr uint64_t kAll = KB == 2 ? ~0ull : 0xFFFFFFFFull;   // every key of a tile seen
 
-  bf16x8 q[RB][kSteps];
-  f32x16 o[RB][kBlocks];
-  float top[RB], sum[RB];                       // running maximum (times c) and sum, per query
+  bf16x8 q[kSteps];
+  f32x16 o[kBlocks];
+  float top, sum;                               // running maximum (times c) and sum, per query
   float c;                                      // scale * log2(e)
   int lane, half, col;
-  uint32_t k_off[kLoads], v_off[kLoads];
 
-  __device__ __forceinline__ void issue(const uint16_t* k, const uint16_t* v, uint64_t seen,
-                                        uint8_t* lds_k, uint8_t* lds_v) const {
-    const int wave = wave_id();
+  __device__ __forceinline__ void start(float scale) {
+    lane = threadIdx.x & 63;
+    half = lane >> 5;
+    col = lane & 31;
+    c = scale * 1.44269504f;
+    top = -__builtin_inff();
+    sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int at = (wave * kLoads + i) * 1024;
-      uint32_t ko = k_off[i], vo = v_off[i];
-      if (seen != ~0ull) {                      // keys out of sight load as zeros
-        const int key = (at >> 4) / kPieces + lane / kPieces;
-        if (!((seen >> key) & 1)) ko = vo = kNoData;
-      }
-      tile_load(k, ko, lds_k + at);
-      tile_load(v, vo, lds_v + at);
-    }
+    for (int b = 0; b < kBlocks; ++b) o[b] = f32x16{};
   }
 
-  // One tile of 64 keys, the bits of `seen` the visible ones.
-  __device__ __forceinline__ void tile(const uint8_t* lds_k, const uint8_t* lds_v, uint64_t seen) {
-    f32x16 s[RB][2];
+  // K fragment st of 32-key block kb: 8 elements of key `col` of the block.
+  static __device__ __forceinline__ u32x4 k_frag(const uint8_t* lds_k, int kb, int st, int col, int half) {
+    const int key = kb * 32 + col;
+    return *reinterpret_cast<const u32x4*>(
+        lds_k + (key * kRowBytes + (((2 * st + half) ^ k_swizzle<DP>(key)) << 4)));
+  }
+  // V fragment of 16-key group g and 32-column block b, transposed.  A lane's 8
+  // probabilities of group g are those of keys 16 g + 4 half + {0..3, 8..11};
+  // the rows of V are taken in the same order, so P needs no exchange of lanes.
+  static __device__ __forceinline__ u32x4 v_frag(const uint8_t* lds_v, int g, int b, int lane) {
+    const int row4 = (lane & 15) >> 2, quad = lane & 3, side = (lane >> 4) & 1, half = lane >> 5;
+    u32x2 v[2];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) s[r][0] = s[r][1] = f32x16{};
-    // S^T = K Q^T: column = query, row = key
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      const int key = kb * 32 + col;
-#pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
-        const u32x4 f = *reinterpret_cast<const u32x4*>(
-            lds_k + key * (DP * 2) + (((2 * st + half) ^ k_swizzle<DP>(key)) << 4));
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-          s[r][kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), q[r][st], s[r][kb], 0, 0, 0);
-      }
+    for (int u = 0; u < 2; ++u) {
+      const int key = 16 * g + 8 * u + 4 * half + row4;
+      const int piece = 4 * b + 2 * side + (quad >> 1);
+      v[u] = __builtin_bit_cast(
+          u32x2, transposed4(lds_v, key * kRowBytes + ((piece ^ v_swizzle<DP>(key)) << 4) + (quad & 1) * 8));
     }
-    if (seen != ~0ull) {
+    return u32x4{v[0].x, v[0].y, v[1].x, v[1].y};
+  }
+
+  // The scores of a tile (S^T: column = query, row = key) become probabilities;
+  // the bits of `seen` are its visible keys (at least one).
+  __device__ __forceinline__ void weigh(f32x16 (&s)[KB], uint64_t seen) {
+    if (seen != kAll) {
       const uint64_t mine = seen >> (4 * half);
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool on = (mine >> (32 * kb + 8 * (i / 4) + i % 4)) & 1;
-#pragma unroll
-          for (int r = 0; r < RB; ++r) s[r][kb][i] = on ? s[r][kb][i] : -__builtin_inff();
-        }
+        for (int i = 0; i < 16; ++i)
+          s[kb][i] = (mine >> (32 * kb + 8 * (i / 4) + i % 4)) & 1 ? s[kb][i] : -__builtin_inff();
     }
-    bf16x8 p[RB][4];
+    float m = s[0][0];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      float m = s[r][0][0];
+    for (int i = 1; i < 16 * KB; ++i) m = __builtin_fmaxf(m, s[i / 16][i % 16]);
+    m = halves_max(m) * c;
+    // the sums are rescaled only when the maximum has grown by more than 2^8:
+    // until then they are at most that much larger than with the true maximum
+    if (__any(m > top + 8.0f)) {
+      const float now = __builtin_fmaxf(top, m);
+      const float f = __builtin_amdgcn_exp2f(top - now);
+      top = now;
+      sum *= f;
 #pragma unroll
-      for (int i = 1; i < 32; ++i) m = __builtin_fmaxf(m, s[r][i / 16][i % 16]);
-      m = __builtin_fmaxf(m, other_half(m)) * c;
-      if (__any(m > top[r] + 8.0f)) {           // sums may reach 2^8 times the true ones
-        const float now = __builtin_fmaxf(top[r], m);
-        const float f = __builtin_amdgcn_exp2f(top[r] - now);
-        top[r] = now;
-        sum[r] *= f;
+      for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
+        for (int i = 0; i < 16; ++i) o[b][i] *= f;
+    }
+  }
+  // Probabilities of 16-key group g, rounded for the product with V; their sum
+  // takes them unrounded.
+  __device__ __forceinline__ bf16x8 probabilities(const f32x16 (&s)[KB], int g, float (&t)[4]) const {
+    float e[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[r][b][i] *= f;
+    for (int i = 0; i < 8; ++i) {
+      e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g % 2) + i], c, -top));
+      t[i % 4] += e[i];
+    }
+    return as_bf16x8(u32x4{bf16x2_rne(e[0], e[1]), bf16x2_rne(e[2], e[3]), bf16x2_rne(e[4], e[5]),
+                           bf16x2_rne(e[6], e[7])});
+  }
+  // O^T += V^T P^T over the tile, each group's fragments read while the group
+  // before it is multiplied.
+  __device__ __forceinline__ void gather(const f32x16 (&s)[KB], const uint8_t* lds_v, u32x4 (&first)[kBlocks]) {
+    float t[4] = {};
+    u32x4 vf[2][kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) vf[0][b] = first[b];
+    bf16x8 p = probabilities(s, 0, t);
+#pragma unroll
+    for (int g = 0; g < 2 * KB; ++g) {
+      bf16x8 pn = p;
+      if (g + 1 < 2 * KB) {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) vf[(g + 1) & 1][b] = v_frag(lds_v, g + 1, b, lane);
       }
-      float e[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i / 16][i % 16], c, -top[r]));
-      float t = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) t += e[i];
-      sum[r] += t;
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        p[r][g] = as_bf16x8(u32x4{bf16x2_rne(e[8 * g], e[8 * g + 1]), bf16x2_rne(e[8 * g + 2], e[8 * g + 3]),
-                                  bf16x2_rne(e[8 * g + 4], e[8 * g + 5]), bf16x2_rne(e[8 * g + 6], e[8 * g + 7])});
-    }
-    // O^T += V^T P^T.  A lane's 8 probabilities of 16-key group g are those of
-    // keys 16 g + 4 half + {0..3, 8..11}; the transposing reads take V's rows
-    // in the same order, so P needs no exchange between lanes.
-    const int row4 = (lane & 15) >> 2, quad = lane & 3, side = (lane >> 4) & 1;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
+      for (int b = 0; b < kBlocks; ++b)
+        o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vf[g & 1][b]), p, o[b], 0, 0, 0);
+      if (g + 1 < 2 * KB) pn = probabilities(s, g + 1, t);
+      if (g + 1 < 2 * KB) __builtin_amdgcn_sched_group_barrier(0x100, 2 * kBlocks, 0);    // DS reads
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        s16x4 v[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int key = 16 * g + 8 * u + 4 * half + row4;
-          const int piece = 4 * b + 2 * side + (quad >> 1);
-          v[u] = transposed4(lds_v + key * (DP * 2) + ((piece ^ v_swizzle<DP>(key)) << 4) + (quad & 1) * 8);
-        }
-        const u32x2 lo = __builtin_bit_cast(u32x2, v[0]), hi = __builtin_bit_cast(u32x2, v[1]);
-        const bf16x8 f = as_bf16x8(u32x4{lo.x, lo.y, hi.x, hi.y});
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-          o[r][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p[r][g], o[r][b], 0, 0, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                               // MFMA
+        if (g + 1 < 2 * KB) __builtin_amdgcn_sched_group_barrier(0x002, 32 / kBlocks, 0); // VALU
       }
+      p = pn;
+    }
+    sum += (t[0] + t[1]) + (t[2] + t[3]);
+  }
+
+  // The same with every group's fragments read and waited for in one asm block:
+  // the compiler does not see LDS reads there, so it puts no wait of its own (for
+  // every load in flight) before them.  `at`: where block b's rows of V start in
+  // LDS for this lane; the caller has waited for the tile.
+  __device__ __forceinline__ void gather_in_flight(const f32x16 (&s)[KB], const uint32_t (&at)[kBlocks]) {
+    float t[4] = {};
+    const auto group = [&](auto gc) {
+      constexpr int g = decltype(gc)::value, lo = 16 * g * kRowBytes, hi = lo + 8 * kRowBytes;
+      u32x2 v[kBlocks][2];
+      if constexpr (kBlocks == 4)
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+            "ds_read_b64_tr_b16 %2, %9 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+            "ds_read_b64_tr_b16 %4, %10 offset:%12\n\tds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+            "ds_read_b64_tr_b16 %6, %11 offset:%12\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1]), "=&v"(v[2][0]), "=&v"(v[2][1]),
+              "=&v"(v[3][0]), "=&v"(v[3][1])
+            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(lo), "n"(hi)
+            : "memory");
+      else
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %4 offset:%6\n\tds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+            "ds_read_b64_tr_b16 %2, %5 offset:%6\n\tds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
+            : "v"(at[0]), "v"(at[1]), "n"(lo), "n"(hi)
+            : "memory");
+      const bf16x8 p = probabilities(s, g, t);
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+        o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            as_bf16x8(u32x4{v[b][0].x, v[b][0].y, v[b][1].x, v[b][1].y}), p, o[b], 0, 0, 0);
+    };
+    group(std::integral_constant<int, 0>{});
+    group(std::integral_constant<int, 1>{});
+    if constexpr (KB == 2) {
+      group(std::integral_constant<int, 2>{});
+      group(std::integral_constant<int, 3>{});
+    }
+    sum += (t[0] + t[1]) + (t[2] + t[3]);
+  }
+  // Where block b's rows of V start for this lane, in a tile at `lds`.
+  __device__ __forceinline__ void v_rows(uint8_t* lds, uint32_t (&at)[kBlocks]) const {
+    const int row4 = (lane & 15) >> 2, quad = lane & 3, side = (lane >> 4) & 1, key = 4 * half + row4;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+      at[b] = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds + key * kRowBytes +
+              (((4 * b + 2 * side + (quad >> 1)) ^ v_swizzle<DP>(key)) << 4) + (quad & 1) * 8;
+  }
+
+  // One tile in LDS.
+  __device__ __forceinline__ void tile(const uint8_t* lds_k, const uint8_t* lds_v, uint64_t seen) {
+    f32x16 s[KB];
+    u32x4 kf[KB][kSteps];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      s[kb] = f32x16{};
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) kf[kb][st] = k_frag(lds_k, kb, st, col, half);
+    }
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st)
+        s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf[kb][st]), q[st], s[kb], 0, 0, 0);
+    u32x4 vf[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) vf[b] = v_frag(lds_v, 0, b, lane);
+    __builtin_amdgcn_sched_group_barrier(0x100, kSteps, 0);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * kBlocks; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    weigh(s, seen);
+    gather(s, lds_v, vf);
+  }
+};
+
+// Global -> LDS loads of one tile by WAVES waves (this one the `wave`-th).  Keys
+// out of sight and pieces past the head size load as zeros.
+template <int DP, int KB, int WAVES>
+struct TileLoader {
+  using A = Attend<DP, KB>;
+  static constexpr int kLoads = A::kKeys * A::kPieces / (64 * WAVES);   // per operand
+  uint32_t k_off[kLoads], v_off[kLoads];
+  int key[kLoads], at[kLoads];
+
+  __device__ __forceinline__ void start(const Attention& a, int wave) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      at[i] = (wave * kLoads + i) * 1024;
+      const int n = (wave * kLoads + i) * 64 + lane, piece = n % A::kPieces;
+      key[i] = n / A::kPieces;
+      const int kp = piece ^ k_swizzle<DP>(key[i]), vp = piece ^ v_swizzle<DP>(key[i]);
+      k_off[i] = 8 * kp < a.dim ? (uint32_t)(key[i] * a.k_token * 2 + kp * 16) : kNoData;
+      v_off[i] = 8 * vp < a.dim ? (uint32_t)(key[i] * a.v_token * 2 + vp * 16) : kNoData;
+    }
+  }
+  __device__ __forceinline__ void issue(const uint16_t* k, const uint16_t* v, uint64_t seen,
+                                        uint8_t* lds_k, uint8_t* lds_v) const {
+    if (seen == A::kAll) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) tile_load(k, k_off[i], lds_k, at[i]);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) tile_load(v, v_off[i], lds_v, at[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        tile_load(k, k_off[i] | (((uint32_t)(~seen >> key[i]) & 1u) * kNoData), lds_k, at[i]);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        tile_load(v, v_off[i] | (((uint32_t)(~seen >> key[i]) & 1u) * kNoData), lds_v, at[i]);
     }
   }
 };
 
-template <int DP, int RB>
-__global__ __launch_bounds__(256, RB == 1 ? 2 : 1) void attention_kernel(Attention a) {
-  using A = Attend<DP, RB>;
+// Which part of the problem a workgroup has.
+struct Place {
+  int64_t pair, batch;                          // pair: (batch, kv head, split)
+  int kvh, split, row_tile, keys;
+  const uint16_t *k, *v;
+  const uint8_t* mask;
+};
+
+__device__ __forceinline__ Place place_of(const Attention& a) {
+  Place p;
+  // Workgroups are dealt to the 8 XCDs in turn.  With row tiles that share a
+  // (batch, kv head, split)'s keys, eight such pairs run side by side, each on
+  // one XCD, whose L2 keeps its keys; entries of unequal lengths are spread over
+  // all of them.  (One contiguous range of pairs per XCD would give an XCD one
+  // batch entry: 242 us against 167 for a CFG pair of 512 and 77 text states.)
+  // Fewer than 2^24 workgroups, so 32 bits do.
+  const uint32_t pos = blockIdx.x, tiles = (uint32_t)a.row_tiles, splits = (uint32_t)a.splits;
+  const uint32_t heads = (uint32_t)a.batch * (uint32_t)a.kv_heads;
+  uint32_t bh;
+  if (tiles == 1) {                              // every head's first split, then the second ones, ...
+    p.split = (int)(pos / heads);
+    bh = pos - (uint32_t)p.split * heads;
+    p.pair = (int64_t)bh * splits + p.split;
+    p.row_tile = 0;
+  } else {
+    const uint32_t pairs = heads * splits, full = pairs / kXcds * kXcds;
+    uint32_t pair;
+    if (pos < full * tiles) {
+      const uint32_t slot = pos / kXcds;
+      pair = slot / tiles * kXcds + pos % kXcds;
+      p.row_tile = (int)(slot % tiles);
+    } else {
+      const uint32_t rest = pos - full * tiles;
+      pair = full + rest / tiles;
+      p.row_tile = (int)(rest % tiles);
+    }
+    p.pair = pair;
+    bh = pair / splits;
+    p.split = (int)(pair - bh * splits);
+  }
+  const uint32_t batch = bh / (uint32_t)a.kv_heads;
+  p.batch = batch;
+  p.kvh = (int)(bh - batch * (uint32_t)a.kv_heads);
+  p.keys = a.keys;
+  if (a.lengths) p.keys = min(max(__builtin_amdgcn_readfirstlane(a.lengths[p.batch]), 0), a.keys);
+  p.k = a.k + p.batch * a.k_batch + p.kvh * a.k_head;
+  p.v = a.v + p.batch * a.v_batch + p.kvh * a.v_head;
+  p.mask = a.mask ? a.mask + p.batch * a.mask_stride : nullptr;
+  return p;
+}
+
+// The visible keys among the KEYS from `first` on (wave-uniform).
+template <int KEYS>
+__device__ __forceinline__ uint64_t seen_from(const Place& p, int first, int lane) {
+  const int n = p.keys - first;
+  uint64_t s = n >= KEYS ? (KEYS == 64 ? ~0ull : (1ull << (KEYS & 63)) - 1) : n <= 0 ? 0 : (1ull << n) - 1;
+  if (p.mask) s &= __ballot(lane < n && lane < KEYS && p.mask[first + lane] != 0);
+  return s;
+}
+
+// Row = token * group + head within the group (fewer than 2^31 rows a call).
+__device__ __forceinline__ int64_t row_offset(const Attention& a, const Place& p, int64_t row, int64_t batch,
+                                              int64_t token_stride, int64_t head_stride) {
+  const uint32_t r = (uint32_t)row, g = (uint32_t)a.group;
+  const uint32_t token = g == 1 ? r : r / g;
+  return p.batch * batch + token * token_stride + (int64_t)(p.kvh * g + (r - token * g)) * head_stride;
+}
+__device__ __forceinline__ const uint16_t* query_row(const Attention& a, const Place& p, int64_t row) {
+  return a.q + row_offset(a, p, row, a.q_batch, a.q_token, a.q_head);
+}
+__device__ __forceinline__ uint16_t* output_row(const Attention& a, const Place& p, int64_t row) {
+  return a.out + row_offset(a, p, row, a.o_batch, a.o_token, a.o_head);
+}
+
+// A lane's walk over rows: first, first + by, ... as (token, head in the group),
+// stepped without a division; rows past the last stay at the last token.
+struct RowStep {
+  int token, head, by_token, by_head, group, last;
+  __device__ __forceinline__ RowStep(const Attention& a, const Place& p, int64_t first, int by) {
+    const uint32_t r = (uint32_t)first, g = (uint32_t)a.group;
+    group = a.group;
+    last = a.queries - 1;
+    token = (int)(g == 1 ? r : r / g);
+    head = (int)(r - (uint32_t)token * g);
+    by_token = by / group;
+    by_head = by - by_token * group;
+  }
+  __device__ __forceinline__ void next() {
+    token += by_token;
+    head += by_head;
+    if (head >= group) {
+      head -= group;
+      ++token;
+    }
+  }
+  __device__ __forceinline__ int64_t offset(const Attention& a, const Place& p, int64_t token_stride,
+                                            int64_t head_stride) const {
+    return (int64_t)min(token, last) * token_stride + (int64_t)(p.kvh * group + head) * head_stride;
+  }
+};
+
+// Many query rows: the four waves of a workgroup have 32 rows each and share the
+// tiles of 64 keys.
+template <int DP>
+__global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
+  using A = Attend<DP, 2>;
+  constexpr int kRowPieces = A::kPieces, kRowsPerLoad = 64 / kRowPieces;
   __shared__ __attribute__((aligned(1024))) uint8_t k0[A::kTileBytes], v0[A::kTileBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t k1[A::kTileBytes], v1[A::kTileBytes];
-  A w;
-  w.lane = threadIdx.x & 63;
-  w.half = w.lane >> 5;
-  w.col = w.lane & 31;
+  const Place p = place_of(a);
   const int wave = wave_id();
-  const int64_t pos = xcd_order(blockIdx.x, gridDim.x);
-  const int64_t pair = pos / a.row_tiles;                       // (batch, kv head, split)
-  const int row_tile = (int)(pos - pair * a.row_tiles);
-  const int64_t bh = pair / a.splits;
-  const int split = (int)(pair - bh * a.splits);
-  const int64_t batch = bh / a.kv_heads;
-  const int kvh = (int)(bh - batch * a.kv_heads);
-
-  int keys = a.keys;
-  if (a.lengths) keys = min(max(__builtin_amdgcn_readfirstlane(a.lengths[batch]), 0), keys);
-  const uint8_t* mask = a.mask ? a.mask + batch * a.mask_stride : nullptr;
-  const int tiles = (keys + kKeys - 1) / kKeys, share = (tiles + a.splits - 1) / a.splits;
-  const int last = min((split + 1) * share, tiles);
-
-  // this wave's query rows: row = token * group + head within the group
-  const int64_t row0 = (int64_t)row_tile * A::kRows + wave * 32 * RB + w.col;
-  const int64_t rows = (int64_t)a.queries * a.group;
-#pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    int64_t row = row0 + 32 * r;
-    row = row < rows ? row : rows - 1;
-    const int64_t token = row / a.group, head = kvh * a.group + (row - token * a.group);
-    const uint16_t* p = a.q + batch * a.q_batch + token * a.q_token + head * a.q_head;
-#pragma unroll
-    for (int st = 0; st < A::kSteps; ++st) {
-      const int at = 16 * st + 8 * w.half;
-      u32x4 f = u32x4{0u, 0u, 0u, 0u};
-      if (at < a.dim) f = *reinterpret_cast<const u32x4*>(p + at);
-      w.q[r][st] = as_bf16x8(f);
-    }
-    w.top[r] = -__builtin_inff();
-    w.sum[r] = 0.0f;
-#pragma unroll
-    for (int b = 0; b < A::kBlocks; ++b) w.o[r][b] = f32x16{};
-  }
-  w.c = a.scale * 1.44269504f;
-#pragma unroll
-  for (int i = 0; i < A::kLoads; ++i) {
-    const int at = (wave * A::kLoads + i) * 64 + w.lane;
-    const int key = at / A::kPieces, piece = at % A::kPieces;
-    const int kp = piece ^ k_swizzle<DP>(key), vp = piece ^ v_swizzle<DP>(key);
-    w.k_off[i] = 8 * kp < a.dim ? (uint32_t)(key * a.k_token * 2 + kp * 16) : kNoData;
-    w.v_off[i] = 8 * vp < a.dim ? (uint32_t)(key * a.v_token * 2 + vp * 16) : kNoData;
-  }
-  const uint16_t* kp = a.k + batch * a.k_batch + kvh * a.k_head;
-  const uint16_t* vp = a.v + batch * a.v_batch + kvh * a.v_head;
-
-  // the visible keys of tile t, and the next tile that has any
-  auto seen_in = [&](int t) -> uint64_t {
-    const int n = keys - t * kKeys;
-    uint64_t s = n >= kKeys ? ~0ull : (1ull << n) - 1;
-    if (mask) s &= __ballot(w.lane < n && mask[(int64_t)t * kKeys + w.lane] != 0);
-    return s;
-  };
+  A w;
+  w.start(a.scale);
+  TileLoader<DP, 2, 4> load;
+  load.start(a, wave);
+  const int tiles = (p.keys + A::kKeys - 1) / A::kKeys;
+  const int share = (tiles + a.splits - 1) / a.splits;
+  const int last = min((p.split + 1) * share, tiles);
+  // the next tile after t that has a visible key
   auto next = [&](int t, uint64_t& seen) {
     for (++t; t < last; ++t)
-      if ((seen = seen_in(t)) != 0) break;
+      if ((seen = seen_from<64>(p, t * A::kKeys, w.lane)) != 0) break;
     return t;
   };
   uint64_t seen = 0, seen_next = 0;
-  int t = next(split * share - 1, seen);
+  int t = next(p.split * share - 1, seen);
   if (t < last)
-    w.issue(kp + (int64_t)t * kKeys * a.k_token, vp + (int64_t)t * kKeys * a.v_token, seen, k0, v0);
-  // every wave of the workgroup sees the same lengths and mask, so all take
-  // the same turns and meet at every barrier
+    load.issue(p.k + (int64_t)t * A::kKeys * a.k_token, p.v + (int64_t)t * A::kKeys * a.v_token, seen, k0, v0);
+
+  // this wave's query rows (row = token * group + head within the group), read
+  // a whole row at a time and turned into fragments through its own 32 rows of
+  // the second buffers, which no tile uses yet
+  const int64_t rows = (int64_t)a.queries * a.group;
+  const int64_t row0 = (int64_t)p.row_tile * 128 + wave * 32;
+  uint8_t* own = (wave < 2 ? k1 : v1) + (wave & 1) * (32 * A::kRowBytes);
+  {
+    u32x4 f[32 / kRowsPerLoad];
+    const int piece = w.lane % kRowPieces;
+    const int at = 8 * piece < a.dim ? 8 * piece : 0;
+    RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad);
+#pragma unroll
+    for (int i = 0; i < 32 / kRowsPerLoad; ++i, step.next())
+      f[i] = *reinterpret_cast<const u32x4*>(a.q + p.batch * a.q_batch +
+                                             step.offset(a, p, a.q_token, a.q_head) + at);
+    if (8 * piece >= a.dim) {
+#pragma unroll
+      for (int i = 0; i < 32 / kRowsPerLoad; ++i) f[i] = u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int i = 0; i < 32 / kRowsPerLoad; ++i) {
+      const int r = i * kRowsPerLoad + w.lane / kRowPieces;
+      *reinterpret_cast<u32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4)) = f[i];
+    }
+#pragma unroll
+    for (int st = 0; st < A::kSteps; ++st)
+      w.q[st] = as_bf16x8(*reinterpret_cast<const u32x4*>(
+          own + w.col * A::kRowBytes + (((2 * st + w.half) ^ k_swizzle<DP>(w.col)) << 4)));
+  }
+
+  // every wave sees the same lengths and mask, so all take the same turns and
+  // meet at every barrier
 #define ATTEND_TURN(kc, vc, kn, vn)                                                              \
   {                                                                                              \
     const int tn = next(t, seen_next);                                                           \
     __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt(0) lgkmcnt(0): own loads in LDS, reads done */   \
-    asm volatile("s_barrier" ::: "memory"); /* everyone's is, and the other buffers are free */ \
+    asm volatile("s_barrier" ::: "memory"); /* everyone's are, and the other buffers are free */ \
     if (tn < last)                                                                               \
-      w.issue(kp + (int64_t)tn * kKeys * a.k_token, vp + (int64_t)tn * kKeys * a.v_token,        \
-              seen_next, kn, vn);                                                                \
+      load.issue(p.k + (int64_t)tn * A::kKeys * a.k_token,                                       \
+                 p.v + (int64_t)tn * A::kKeys * a.v_token, seen_next, kn, vn);                   \
     w.tile(kc, vc, seen);                                                                        \
     t = tn;                                                                                      \
     seen = seen_next;                                                                            \
@@ -256,63 +483,255 @@ __global__ __launch_bounds__(256, RB == 1 ? 2 : 1) void attention_kernel(Attenti
   }
 #undef ATTEND_TURN
 
-#pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    const int64_t row = row0 + 32 * r;
-    const float l = w.sum[r] + other_half(w.sum[r]);
-    if (a.splits > 1) {      // unnormalised partial sums, the maximum and the sum
-      if (row >= rows) continue;
-      const int64_t slot = pair * rows + row;
-      float* out = a.part + slot * DP;
-#pragma unroll
-      for (int b = 0; b < A::kBlocks; ++b)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<f32x4*>(out + 32 * b + 8 * g + 4 * w.half) =
-              f32x4{w.o[r][b][4 * g], w.o[r][b][4 * g + 1], w.o[r][b][4 * g + 2], w.o[r][b][4 * g + 3]};
-      if (w.half == 0) a.stats[slot] = float2{w.top[r], l};
-      continue;
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // no key seen: zeros
-    const int64_t token = (row < rows ? row : 0) / a.group;
-    const int64_t head = kvh * a.group + (row < rows ? row - token * a.group : 0);
-    uint16_t* out = a.out + batch * a.o_batch + token * a.o_token + head * a.o_head;
+  const float l = halves_sum(w.sum);
+  const int64_t row = row0 + w.col;
+  if (a.splits > 1) {      // unnormalised partial sums, the maximum and the sum
+    if (row >= rows) return;
+    const int64_t slot = p.pair * rows + row;
+    float* out = a.part + slot * DP;
 #pragma unroll
     for (int b = 0; b < A::kBlocks; ++b)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int at = 32 * b + 8 * g + 4 * w.half;
-        const u32x2 v = u32x2{bf16x2_rne(w.o[r][b][4 * g] * inv, w.o[r][b][4 * g + 1] * inv),
-                              bf16x2_rne(w.o[r][b][4 * g + 2] * inv, w.o[r][b][4 * g + 3] * inv)};
-        if (row < rows && at < a.dim) *reinterpret_cast<u32x2*>(out + at) = v;
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4*>(out + 32 * b + 8 * g + 4 * w.half) =
+            f32x4{w.o[b][4 * g], w.o[b][4 * g + 1], w.o[b][4 * g + 2], w.o[b][4 * g + 3]};
+    if (w.half == 0) a.stats[slot] = float2{w.top, l};
+    return;
+  }
+  // through the wave's rows of LDS again, so that whole rows are stored
+  __syncthreads();
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // no key seen: zeros
+#pragma unroll
+  for (int b = 0; b < A::kBlocks; ++b)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<u32x2*>(own + w.col * A::kRowBytes + (((4 * b + g) ^ k_swizzle<DP>(w.col)) << 4) +
+                                8 * w.half) =
+          u32x2{bf16x2_rne(w.o[b][4 * g] * inv, w.o[b][4 * g + 1] * inv),
+                bf16x2_rne(w.o[b][4 * g + 2] * inv, w.o[b][4 * g + 3] * inv)};
+  const int piece = w.lane % kRowPieces;
+  RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad);
+#pragma unroll
+  for (int i = 0; i < 32 / kRowsPerLoad; ++i, step.next()) {
+    const int r = i * kRowsPerLoad + w.lane / kRowPieces;
+    const u32x4 f =
+        *reinterpret_cast<const u32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4));
+    if (row0 + r < rows && 8 * piece < a.dim)
+      *reinterpret_cast<u32x4*>(a.out + p.batch * a.o_batch + step.offset(a, p, a.o_token, a.o_head) +
+                                8 * piece) = f;
+  }
+}
+
+// Few query rows (at most 32 per kv head: single tokens): a workgroup's four
+// waves have the same rows and every fourth tile of 32 keys each, so no wave
+// waits for another; they are joined at the end.  What is left is the stream of
+// keys and values: K fragments go straight to registers (each element is used
+// by one lane once), V through LDS of the wave's own for the transposed reads,
+// both a tile ahead of their use.
+template <int DP>
+__global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
+  using A = Attend<DP, 1>;
+  __shared__ __attribute__((aligned(1024))) uint8_t even[4 * A::kTileBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t odd[4 * A::kTileBytes];
+  const Place p = place_of(a);
+  const int64_t rows = (int64_t)a.queries * a.group;
+  const int first = p.split * a.share * 4;       // a split is `share` groups of four tiles
+  if (a.splits > 1 && first * A::kKeys >= p.keys) {        // past this entry's length
+    if (threadIdx.x < rows) a.stats[p.pair * rows + threadIdx.x] = float2{-__builtin_inff(), 0.0f};
+    return;
+  }
+  const int wave = wave_id();
+  A w;
+  w.start(a.scale);
+  const uint16_t* q = query_row(a, p, w.col < rows ? w.col : rows - 1);
+  constexpr int kLoads = A::kKeys * A::kPieces / 64;
+  uint32_t k_off[A::kSteps], v_off[kLoads];
+#pragma unroll
+  for (int st = 0; st < A::kSteps; ++st) {
+    const int at = 16 * st + 8 * w.half;
+    u32x4 f = u32x4{0u, 0u, 0u, 0u};
+    if (at < a.dim) f = *reinterpret_cast<const u32x4*>(q + at);
+    w.q[st] = as_bf16x8(f);
+    k_off[st] = at < a.dim ? (uint32_t)(w.col * a.k_token * 2 + at * 2) : kNoData;
+  }
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int n = i * 64 + w.lane, key = n / A::kPieces, vp = (n % A::kPieces) ^ v_swizzle<DP>(key);
+    v_off[i] = 8 * vp < a.dim ? (uint32_t)(key * a.v_token * 2 + vp * 16) : kNoData;
+  }
+  const int last = min(first + a.share * 4, (p.keys + A::kKeys - 1) / A::kKeys);
+  auto next = [&](int t, uint64_t& seen) {
+    for (t += 4; t < last; t += 4)
+      if ((seen = seen_from<32>(p, t * A::kKeys, w.lane)) != 0) break;
+    return t;
+  };
+  u32x4 kf[A::kSteps];
+  // keys out of sight load as zeros
+  auto load_k = [&](int t, uint64_t seen) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(p.k + (int64_t)t * A::kKeys * a.k_token), (short)0, (int)kNoData, kBufferWord3);
+    const uint32_t hide = ((uint32_t)(~seen >> w.col) & 1u) * kNoData;
+#pragma unroll
+    for (int st = 0; st < A::kSteps; ++st)
+      kf[st] = __builtin_amdgcn_raw_buffer_load_b128(r, k_off[st] | hide, 0, 0);
+  };
+  const int own = wave * A::kTileBytes;          // this wave's part of `even` and `odd`
+  uint32_t even_at[A::kBlocks], odd_at[A::kBlocks];
+  w.v_rows(even + own, even_at);
+  w.v_rows(odd + own, odd_at);
+  auto load_v = [&](int t, uint64_t seen, uint8_t* lds) {
+    const uint16_t* v = p.v + (int64_t)t * A::kKeys * a.v_token;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int key = (i * 64 + w.lane) / A::kPieces;
+      tile_load(v, v_off[i] | (((uint32_t)(~seen >> key) & 1u) * kNoData), lds, own + i * 1024);
+    }
+  };
+  uint64_t seen = 0, seen_next = 0;
+  int t = next(first + wave - 4, seen);
+  constexpr int kAhead = A::kSteps + kLoads;     // loads of one tile: 16 or 8
+  static_assert(kAhead < 64, "vmcnt counts to 63");
+  // the scores take the K registers, which the next tile's loads then refill;
+  // lgkmcnt(0): the reads of the V buffer that is filled next are done;
+  // vmcnt(kAhead): all but the next tile's loads are
+#define ATTEND_TURN(cur, nxt)                                                                    \
+  {                                                                                              \
+    const int tn = next(t, seen_next);                                                           \
+    f32x16 s[1] = {f32x16{}};                                                                    \
+    _Pragma("unroll") for (int st = 0; st < A::kSteps; ++st) s[0] =                              \
+        __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf[st]), w.q[st], s[0], 0, 0, 0);      \
+    __builtin_amdgcn_s_waitcnt(0xC07F);                                                          \
+    if (tn < last) {                                                                             \
+      load_k(tn, seen_next);                                                                     \
+      load_v(tn, seen_next, nxt);                                                                \
+      __builtin_amdgcn_s_waitcnt(0x0F70 | (kAhead & 15) | ((kAhead >> 4) << 14));                \
+    } else {                                                                                     \
+      __builtin_amdgcn_s_waitcnt(0x0F70);                                                        \
+    }                                                                                            \
+    asm volatile("" ::: "memory");                                                               \
+    w.weigh(s, seen);                                                                            \
+    w.gather_in_flight(s, cur##_at);                                                             \
+    t = tn;                                                                                      \
+    seen = seen_next;                                                                            \
+  }
+  if (t < last) {
+    load_k(t, seen);
+    load_v(t, seen, even);
+    // the query fragments are waited for here (they came first), not in the
+    // loop, where the wait would cover the loads in flight
+#pragma unroll
+    for (int st = 0; st < A::kSteps; ++st) asm volatile("" : "+v"(w.q[st]));
+    for (;;) {
+      ATTEND_TURN(even, odd)
+      if (t >= last) break;
+      ATTEND_TURN(odd, even)
+      if (t >= last) break;
+    }
+  }
+#undef ATTEND_TURN
+
+  // the four waves' states meet in LDS, in wave order: first the maxima and sums,
+  // then the outputs, half the columns at a time (32 rows x DP / 2 of each wave
+  // in binary32 are what `even` holds)
+  float* park = reinterpret_cast<float*>(even);
+  float(*park_top)[32] = reinterpret_cast<float(*)[32]>(odd);
+  float(*park_sum)[32] = park_top + 4;
+  float *all_top = park_top[8], *all_sum = park_top[9];
+  const float l = halves_sum(w.sum);
+  __syncthreads();
+  if (w.half == 0) {
+    park_top[wave][w.col] = w.top;
+    park_sum[wave][w.col] = l;
+  }
+  __syncthreads();
+  float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (park_sum[i][w.col] != 0.0f) top = __builtin_fmaxf(top, park_top[i][w.col]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (park_sum[i][w.col] != 0.0f)
+      sum = __builtin_fmaf(park_sum[i][w.col], __builtin_amdgcn_exp2f(park_top[i][w.col] - top), sum);
+  const float mine = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(w.top - top);
+  if (wave == 0 && w.half == 0) {
+    all_top[w.col] = top;
+    all_sum[w.col] = sum;
+  }
+  const int here = (int)rows;                    // at most 32
+  constexpr int kPart = DP / 2;
+  for (int part = 0; part < 2; ++part) {
+    if (w.col < here) {
+#pragma unroll
+      for (int b = 0; b < A::kBlocks; ++b) {
+        if (b / (A::kBlocks / 2) != part) continue;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          f32x4 v = f32x4{};
+          if (l != 0.0f)
+            v = f32x4{w.o[b][4 * g], w.o[b][4 * g + 1], w.o[b][4 * g + 2], w.o[b][4 * g + 3]} * mine;
+          *reinterpret_cast<f32x4*>(park + (wave * 32 + w.col) * kPart + 32 * (b % (A::kBlocks / 2)) +
+                                    8 * g + 4 * w.half) = v;
+        }
       }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < here * (kPart / 4); e += 256) {
+      const int r = e / (kPart / 4), d = (e % (kPart / 4)) * 4, col = part * kPart + d;
+      f32x4 s = f32x4{};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += *reinterpret_cast<const f32x4*>(park + (i * 32 + r) * kPart + d);
+      const float total = all_sum[r];
+      if (a.splits > 1) {
+        const int64_t slot = p.pair * rows + r;
+        *reinterpret_cast<f32x4*>(a.part + slot * DP + col) = s;
+        if (col == 0) a.stats[slot] = float2{all_top[r], total};
+      } else if (col < a.dim) {
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        *reinterpret_cast<u32x2*>(output_row(a, p, r) + col) =
+            u32x2{bf16x2_rne(s[0] * inv, s[1] * inv), bf16x2_rne(s[2] * inv, s[3] * inv)};
+      }
+    }
+    __syncthreads();
   }
 }
 
 // Joins the splits of a row, one wave per row: partial sums weighted by
-// 2^(their maximum - the largest), in split order.
+// 2^(their maximum - the largest), in split order.  Lane s holds split s's
+// maximum and sum (at most 64 splits).
 template <int DP>
 __global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
   const int lane = threadIdx.x & 63;
   const int64_t rows = (int64_t)a.queries * a.group;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);      // (batch, kv head, row)
+  const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();      // (batch, kv head, row)
   if (at >= (int64_t)a.batch * a.kv_heads * rows) return;
   const int64_t bh = at / rows, row = at - bh * rows;
-  float top = -__builtin_inff();
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 st = a.stats[(bh * a.splits + s) * rows + row];
-    if (st.y != 0.0f) top = __builtin_fmaxf(top, st.x);
-  }
-  float l = 0.0f, o[DP / 64] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const int64_t slot = (bh * a.splits + s) * rows + row;
-    const float2 st = a.stats[slot];
-    if (st.y == 0.0f) continue;                  // this split saw no key
-    const float f = __builtin_amdgcn_exp2f(st.x - top);
-    l = __builtin_fmaf(st.y, f, l);
+  const int64_t first = bh * a.splits * rows + row;
+  float2 st = float2{0.0f, 0.0f};
+  if (lane < a.splits) st = a.stats[first + lane * rows];
+  float top = st.y != 0.0f ? st.x : -__builtin_inff();
 #pragma unroll
-    for (int j = 0; j < DP / 64; ++j)
-      o[j] = __builtin_fmaf(a.part[slot * DP + lane * (DP / 64) + j], f, o[j]);
+  for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off, 64));
+  const float weight = st.y != 0.0f ? __builtin_amdgcn_exp2f(st.x - top) : 0.0f;
+  const float part_sum = st.y != 0.0f ? st.y * weight : 0.0f;
+  float l = 0.0f, o[DP / 64] = {};
+  constexpr int U = 8;                           // loads in flight
+  for (int s0 = 0; s0 < a.splits; s0 += U) {
+    float v[U][DP / 64];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float* from = a.part + (first + min(s0 + u, a.splits - 1) * rows) * DP + lane * (DP / 64);
+#pragma unroll
+      for (int j = 0; j < DP / 64; ++j) v[u][j] = from[j];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float f = __shfl(weight, (s0 + u) & 63, 64), y = __shfl(part_sum, (s0 + u) & 63, 64);
+      // past the splits, or a split that saw no key (what it left is not read)
+      if (s0 + u >= a.splits || (f == 0.0f && y == 0.0f)) continue;
+      l += y;
+#pragma unroll
+      for (int j = 0; j < DP / 64; ++j) o[j] = __builtin_fmaf(v[u][j], f, o[j]);
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int64_t batch = bh / a.kv_heads, token = row / a.group;
@@ -326,27 +745,30 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
   }
 }
 
-template <int DP, int RB>
-hipError_t launch(Attention a, hipStream_t stream) {
-  const int64_t rows = (int64_t)a.queries * a.group;
-  a.row_tiles = (rows + Attend<DP, RB>::kRows - 1) / Attend<DP, RB>::kRows;
-  const int64_t grid = (int64_t)a.batch * a.kv_heads * a.splits * a.row_tiles;
-  attention_kernel<DP, RB><<<dim3((unsigned)grid), dim3(256), 0, stream>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t all = (int64_t)a.batch * a.kv_heads * rows;
-  attention_join_kernel<DP><<<dim3((unsigned)((all + 3) / 4)), dim3(256), 0, stream>>>(a);
-  return hipGetLastError();
-}
+// How a call is run.  `few`: at most 32 rows per kv head, the kernel whose waves
+// share the rows.  Its splits are of a fixed number of keys, so entries of
+// unequal lengths cost their own keys only: enough for four workgroups a
+// compute unit, each at least 256 keys.  The other kernel splits as many ways
+// as give every compute unit two workgroups, each split at least four tiles.
+struct Plan {
+  bool few;
+  int splits, share;
+};
 
-// Ways the keys are split: as many as give every compute unit two workgroups,
-// each split keeping at least four tiles.
-int splits_for(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys) {
-  const int64_t groups = batch * kv_heads * ((rows + 127) / 128);
-  const int64_t tiles = (keys + kKeys - 1) / kKeys;
-  int64_t s = 2 * compute_units() / (groups > 0 ? groups : 1);
+Plan plan_for(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys) {
+  const int64_t heads = batch * kv_heads > 0 ? batch * kv_heads : 1;
+  if (rows <= 32) {
+    const int64_t groups = (keys + 127) / 128;           // of four tiles of 32
+    int64_t share = groups * heads / (4 * compute_units());
+    if (share < 2) share = 2;
+    if (share < (groups + 63) / 64) share = (groups + 63) / 64;
+    const int64_t splits = (groups + share - 1) / share;
+    return {true, (int)(splits < 1 ? 1 : splits), (int)share};
+  }
+  const int64_t groups = heads * ((rows + 127) / 128), tiles = (keys + 63) / 64;
+  int64_t s = 2 * compute_units() / groups;
   if (s > tiles / 4) s = tiles / 4;
-  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  return {false, (int)(s < 1 ? 1 : s > 64 ? 64 : s), 0};
 }
 
 int padded_dim(int64_t dim) { return dim <= 64 ? 64 : 128; }
@@ -357,24 +779,41 @@ size_t attention_workspace_bytes(int64_t batch, int64_t queries, int64_t keys, i
                                  int64_t kv_heads, int64_t dim) {
   if (batch == 0 || queries == 0) return 0;
   const int64_t rows = queries * (heads / kv_heads);
-  const int splits = splits_for(batch, kv_heads, rows, keys);
+  const int splits = plan_for(batch, kv_heads, rows, keys).splits;
   if (splits == 1) return 0;
   return (size_t)(batch * kv_heads * splits * rows) * (padded_dim(dim) * 4 + 8);
 }
 
 hipError_t launch_attention(Attention a, void* workspace, size_t workspace_bytes,
                             hipStream_t stream) {
-  const int64_t rows = (int64_t)a.queries * a.group;
-  a.splits = splits_for(a.batch, a.kv_heads, rows, a.keys);
-  const size_t need = attention_workspace_bytes(a.batch, a.queries, a.keys,
-                                                (int64_t)a.kv_heads * a.group, a.kv_heads, a.dim);
-  if (!workspace || workspace_bytes < need) a.splits = 1;
+  const int64_t rows = (int64_t)a.queries * a.group, bh = (int64_t)a.batch * a.kv_heads;
+  const Plan plan = plan_for(a.batch, a.kv_heads, rows, a.keys);
+  const int dp = padded_dim(a.dim);
+  a.splits = plan.splits;
+  a.share = plan.share;
+  const size_t need = (size_t)(bh * a.splits * rows) * (dp * 4 + 8);
+  if (a.splits > 1 && (!workspace || workspace_bytes < need)) {
+    a.share *= a.splits;
+    a.splits = 1;
+  }
   if (a.splits > 1) {
     a.part = static_cast<float*>(workspace);
-    a.stats = reinterpret_cast<float2*>(a.part + (int64_t)a.batch * a.kv_heads * a.splits * rows *
-                                                    padded_dim(a.dim));
+    a.stats = reinterpret_cast<float2*>(a.part + bh * a.splits * rows * dp);
   }
-  return padded_dim(a.dim) == 64 ? launch<64, 1>(a, stream) : launch<128, 1>(a, stream);
+  a.row_tiles = plan.few ? 1 : (rows + 127) / 128;
+  const dim3 grid((unsigned)(bh * a.splits * a.row_tiles)), block(256);
+  if (plan.few)
+    dp == 64 ? attention_few_kernel<64><<<grid, block, 0, stream>>>(a)
+             : attention_few_kernel<128><<<grid, block, 0, stream>>>(a);
+  else
+    dp == 64 ? attention_kernel<64><<<grid, block, 0, stream>>>(a)
+             : attention_kernel<128><<<grid, block, 0, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const dim3 join((unsigned)((bh * rows + 3) / 4));
+  dp == 64 ? attention_join_kernel<64><<<join, block, 0, stream>>>(a)
+           : attention_join_kernel<128><<<join, block, 0, stream>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace nvfp4

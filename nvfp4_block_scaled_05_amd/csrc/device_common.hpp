@@ -253,6 +253,33 @@ __device__ __forceinline__ void buffer_load_lds(const void* base, uint32_t lane_
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 4, lane_off, scalar_off, 0, 0);
 }
 
+// Sums over neighbouring lanes in the vector ALU's lane-permuting operand: after
+// group_sum<N> every lane has the sum over its aligned group of N lanes (N up to
+// 16 without LDS).
+#define NVFP4_LANES(v, ctrl, rows)                                                            \
+  __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, \
+                                                        rows, 0xF, false))
+template <int N>
+__device__ __forceinline__ float group_sum(float v) {
+  if (N >= 2) v += NVFP4_LANES(v, 0xB1, 0xF);     // lane ^ 1
+  if (N >= 4) v += NVFP4_LANES(v, 0x4E, 0xF);     // lane ^ 2
+  if (N >= 8) v += NVFP4_LANES(v, 0x141, 0xF);    // mirrored within 8
+  if (N >= 16) v += NVFP4_LANES(v, 0x140, 0xF);   // mirrored within 16
+  if (N >= 32) v += __shfl_xor(v, 16, 64);
+  if (N >= 64) v += __shfl_xor(v, 32, 64);
+  return v;
+}
+
+// Sum over the wave as a scalar, without LDS: row sums, then two broadcasts
+// across the 16-lane rows gather them in lane 63.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = group_sum<16>(v);
+  v += NVFP4_LANES(v, 0x142, 0xA);   // rows 1 and 3 take the row before
+  v += NVFP4_LANES(v, 0x143, 0xC);   // rows 2 and 3 take lane 31
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+#undef NVFP4_LANES
+
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) {
@@ -262,6 +289,12 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return v;
 }
 
+// Raise the amax word to `bits` (a magnitude's binary32 pattern).  The order of
+// integer maxima does not matter; the word only grows, so a workgroup that reads
+// one already as large leaves the atomic out.
+__device__ __forceinline__ void raise_amax(uint32_t* amax, uint32_t bits) {
+  if (bits > __hip_atomic_load(amax, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(amax, bits);
+}
 
 // ------------------------------------------------------------- quantizer --
 // Shared by the quantize kernel and the GEMM epilogue that writes NVFP4

@@ -122,7 +122,7 @@ struct Attention {
   float scale;
   // filled in by the launch
   int64_t row_tiles;
-  int splits;
+  int splits, share;             // share: groups of four 32-key tiles a split has
   float* part;                   // [batch][kv head][split][row][padded dim]
   float2* stats;                 // [batch][kv head][split][row]: maximum, sum
 };

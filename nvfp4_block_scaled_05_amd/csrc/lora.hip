@@ -38,140 +38,170 @@ __device__ __forceinline__ int row_adapter(const Lora& a, int64_t row) {
   return id >= 0 && id < a.adapters ? id : -1;
 }
 
+// Depth of one group of steps of a wave of the first kernel, all loaded at once
+// (9 to 24 16-byte loads a lane), and the most waves of its workgroup.
+constexpr int group_steps(int rt, int mt) { return rt * mt <= 2 ? 8 : rt * mt <= 4 ? 4 : 1; }
+constexpr int kDownWaves = 12;
+
 // t[slice][row][16 * RT]: this slice's part of s_a * down_a x.  RT: 16-wide
-// tiles over the rank; the four waves take every fourth group of U 32-deep
-// steps of the slice and add their sums in wave order.
-template <int RT>
-__global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(Lora a) {
-  constexpr int U = RT <= 2 ? 8 : (RT <= 4 ? 4 : 2);
-  __shared__ float red[4][RT * 4][64];
+// tiles over the rank, MT: row tiles of the workgroup.  It has as many waves (up
+// to 12) as the slice has groups of steps, so that one round of loads takes it
+// through the slice; their sums are added in wave order.
+template <int RT, int MT>
+__global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(Lora a) {
+  constexpr int U = group_steps(RT, MT);
+  __shared__ float red[kDownWaves][MT * RT * 4][64];
+  const int waves = blockDim.x >> 6;
   if (a.amax && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.amax = 0u;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int r = lane & 15, q = lane >> 4;
-  const int64_t row0 = (int64_t)blockIdx.x * kRowTile;
-  const int64_t row = row0 + r < a.rows ? row0 + r : a.rows - 1;
-  const int id = row_adapter(a, row0 + r);
+  const int64_t row0 = (int64_t)blockIdx.x * (kRowTile * MT);
+  const int id = row_adapter(a, row0 + lane % (kRowTile * MT));      // rows past the last: none
   const int k_end = min(a.inner, (int)(blockIdx.y + 1) * a.slice);
-  const uint16_t* x = a.x + row * a.inner + 8 * q;
-  float t[RT][4] = {};
-  uint64_t todo = __ballot(lane < 16 && id >= 0);
+  const uint16_t* x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) x[m] = a.x + min(row0 + 16 * m + r, a.rows - 1) * a.inner + 8 * q;
+  // element e of a lane: row tile e / (4 RT), column 16 (e / 4 % RT) + lane % 16,
+  // row 4 (lane / 16) + e % 4; rows without an adapter stay zero
+#pragma unroll
+  for (int e = 0; e < MT * RT * 4; ++e) red[wave][e][lane] = 0.0f;
+  uint64_t todo = __ballot(lane < kRowTile * MT && id >= 0);
   while (todo) {
     const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-    const uint32_t same = (uint32_t)__ballot(lane < 16 && id == cur);
-    todo &= ~(uint64_t)same;
-    f32x4 acc[RT];
+    const uint64_t same = __ballot(lane < kRowTile * MT && id == cur);
+    todo &= ~same;
+    f32x4 acc[MT][RT];
 #pragma unroll
-    for (int c = 0; c < RT; ++c) acc[c] = f32x4{};
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int c = 0; c < RT; ++c) acc[m][c] = f32x4{};
     const uint16_t* down = a.down + (int64_t)cur * a.rank * a.inner + 8 * q;
-    for (int k = blockIdx.y * a.slice + wave * 32 * U; k < k_end; k += 4 * 32 * U) {
-      u32x4 xa[U], wb[U][RT];
+    // columns past the rank read its last row; no one reads what they compute
+    const uint16_t* col[RT];
+#pragma unroll
+    for (int c = 0; c < RT; ++c) col[c] = down + (int64_t)min(16 * c + r, a.rank - 1) * a.inner;
+    int k = blockIdx.y * a.slice + wave * 32 * U;
+    for (; k + 32 * U <= k_end; k += waves * 32 * U) {
+      u32x4 xa[U][MT], wb[U][RT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int at = k + 32 * u;
-        const bool in = at + 8 * q < k_end;
-        xa[u] = load16(x + at, in);
 #pragma unroll
-        for (int c = 0; c < RT; ++c)
-          wb[u][c] = load16(down + (int64_t)(16 * c + r) * a.inner + at, in && 16 * c + r < a.rank);
+        for (int m = 0; m < MT; ++m) xa[u][m] = *reinterpret_cast<const u32x4*>(x[m] + k + 32 * u);
+#pragma unroll
+        for (int c = 0; c < RT; ++c) wb[u][c] = *reinterpret_cast<const u32x4*>(col[c] + k + 32 * u);
       }
+      __builtin_amdgcn_sched_barrier(0);       // every load of the group before its first product
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int c = 0; c < RT; ++c)
-          acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xa[u]), frag(wb[u][c]), acc[c], 0, 0, 0);
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int c = 0; c < RT; ++c)
+            acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xa[u][m]), frag(wb[u][c]), acc[m][c], 0, 0, 0);
+    }
+    for (int end = min(k + 32 * U, k_end); k < end; k += 32) {     // the last, shorter group
+      const bool in = k + 8 * q < k_end;
+#pragma unroll
+      for (int c = 0; c < RT; ++c) {
+        const u32x4 wb = load16(col[c] + k, in);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(load16(x[m] + k, in)), frag(wb), acc[m][c], 0, 0, 0);
+      }
     }
     const float s = a.scales ? a.scales[cur] : 1.0f;
 #pragma unroll
-    for (int c = 0; c < RT; ++c)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((same >> (4 * q + i)) & 1) t[c][i] = acc[c][i] * s;
+      for (int c = 0; c < RT; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((same >> (16 * m + 4 * q + i)) & 1) red[wave][(m * RT + c) * 4 + i][lane] = acc[m][c][i] * s;
   }
-#pragma unroll
-  for (int c = 0; c < RT; ++c)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][c * 4 + i][lane] = t[c][i];
   __syncthreads();
-  // element e of a lane: column 16 (e / 4) + lane % 16, row 4 (lane / 16) + e % 4
-  for (int e = wave; e < RT * 4; e += 4) {
-    const float v = ((red[0][e][lane] + red[1][e][lane]) + red[2][e][lane]) + red[3][e][lane];
-    const int64_t to = row0 + 4 * q + e % 4;
-    if (to < a.rows) a.t[((int64_t)blockIdx.y * a.rows + to) * (16 * RT) + 16 * (e / 4) + r] = v;
+  for (int e = wave; e < MT * RT * 4; e += waves) {
+    float v = red[0][e][lane];
+    for (int w = 1; w < waves; ++w) v += red[w][e][lane];
+    const int64_t to = row0 + 16 * (e / (4 * RT)) + 4 * q + e % 4;
+    if (to < a.rows) a.t[((int64_t)blockIdx.y * a.rows + to) * (16 * RT) + 16 * (e / 4 % RT) + r] = v;
   }
 }
 
-// out = epi(y + up_a t).  A wave takes 16 rows and 128 columns at a time.  The
-// weight is the MFMA's first operand, so a lane holds columns of one row; the
-// weight rows of a pair of tiles are dealt so that the 4 + 4 columns a lane
-// gets are 8 neighbours (16 bytes of y and out).
-template <int RT>
+// out = epi(y + up_a t).  A wave takes MT row tiles and 128 columns at a time, the
+// column blocks of the rows side by side, so y and out are read and written in
+// long pieces (with a workgroup's waves on four row tiles of one column block
+// instead, sharing the adapter's weights in the cache: 58 us against 55).  The weight is the MFMA's first operand, so a lane holds columns
+// of one row; the weight rows of a pair of MFMA tiles are dealt so that the 4 + 4
+// columns a lane gets are 8 neighbours (16 bytes of y and out).
+template <int RT, int MT>
 __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
   constexpr int KS = (RT + 1) / 2;             // 32-deep steps over the rank
   const int lane = threadIdx.x & 63;
   const int r = lane & 15, q = lane >> 4;
-  const int64_t row_tiles = (a.rows + kRowTile - 1) / kRowTile;
-  const int64_t items = row_tiles * ((a.outer + kColBlock * kColBlocks - 1) / (kColBlock * kColBlocks));
+  const int col_items = (a.outer + kColBlock * kColBlocks - 1) / (kColBlock * kColBlocks);
+  const int64_t items = (a.rows + kRowTile * MT - 1) / (kRowTile * MT) * col_items;
   u16x2 top = {0, 0};
   for (int64_t item = (int64_t)blockIdx.x * 4 + wave_id(); item < items; item += (int64_t)gridDim.x * 4) {
-    const int64_t col_item = item / row_tiles;
-    const int64_t row = (item - col_item * row_tiles) * kRowTile + r;
-    const int col0 = (int)col_item * kColBlock * kColBlocks;
-    const bool live = row < a.rows;
-    const int id = row_adapter(a, row);
-    uint64_t todo = __ballot(lane < 16 && id >= 0);
-    if (!todo && a.skip_idle) continue;        // in place, nothing to add
-    u32x4 yv[kColBlocks];
+    const int64_t row_item = items < (1ll << 31) ? (int64_t)((uint32_t)item / (uint32_t)col_items) : item / col_items;
+    const int64_t row0 = row_item * (kRowTile * MT) + r;
+    const int col0 = (int)(item - row_item * col_items) * kColBlock * kColBlocks;
+    int id[MT], first = -1;
+    uint64_t any = 0;
+    bool uniform = true;                       // one adapter at most
 #pragma unroll
-    for (int b = 0; b < kColBlocks; ++b) {
-      const int col = col0 + kColBlock * b + 8 * q;
-      yv[b] = load16(a.y + row * a.outer + col, live && col < a.outer);
+    for (int m = 0; m < MT; ++m) {
+      id[m] = row_adapter(a, row0 + 16 * m);
+      const uint64_t has = __ballot(lane < 16 && id[m] >= 0);
+      if (has && first < 0) first = __builtin_amdgcn_readlane(id[m], __builtin_ctzll(has));
+      uniform &= has == __ballot(lane < 16 && id[m] >= 0 && id[m] == first);
+      any |= has;
     }
-    bf16x8 tf[KS];
+    if (!any && a.skip_idle) continue;         // in place, nothing to add
+    // rows and columns past the last read the last row's, the first column's;
+    // what they compute is not stored
+    u32x4 yv[MT][kColBlocks];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      f32x4 lo = f32x4{}, hi = f32x4{};
-      if (live && id >= 0 && 32 * s + 8 * q < a.rank)
-        for (int sl = 0; sl < a.slices; ++sl) {
-          const float* p = a.t + (sl * a.rows + row) * (16 * RT) + 32 * s + 8 * q;
-          lo += reinterpret_cast<const f32x4*>(p)[0];
-          hi += reinterpret_cast<const f32x4*>(p)[1];
-        }
-      // rounded to bf16 for the product with up: a relative 2^-8 of each of
-      // the adapter's `rank` terms
-      tf[s] = frag(u32x4{bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]), bf16x2_rne(hi[0], hi[1]),
-                         bf16x2_rne(hi[2], hi[3])});
-    }
-    f32x4 d[kColBlocks][2];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int b = 0; b < kColBlocks; ++b) d[b][0] = d[b][1] = f32x4{};
-    while (todo) {
-      const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-      todo &= ~__ballot(lane < 16 && id == cur);
-      const uint16_t* up = a.up + (int64_t)cur * a.outer * a.rank;
+      for (int b = 0; b < kColBlocks; ++b) {
+        const int col = col0 + kColBlock * b + 8 * q;
+        yv[m][b] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+            a.y + min(row0 + 16 * m, a.rows - 1) * a.outer + (col < a.outer ? col : 0)));
+      }
+    bf16x8 tf[MT][KS];
 #pragma unroll
-      for (int b = 0; b < kColBlocks; ++b)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int n = col0 + kColBlock * b + 8 * (r >> 2) + 4 * p + (r & 3);
-          f32x4 acc = f32x4{};
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            const u32x4 f = load16(up + (int64_t)n * a.rank + 32 * s + 8 * q,
-                                   n < a.outer && 32 * s + 8 * q < a.rank);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(f), tf[s], acc, 0, 0, 0);
+      for (int s = 0; s < KS; ++s) {
+        f32x4 lo = f32x4{}, hi = f32x4{};
+        if (id[m] >= 0 && 32 * s + 8 * q < a.rank)
+          for (int sl = 0; sl < a.slices; ++sl) {
+            const float* p = a.t + (sl * a.rows + row0 + 16 * m) * (16 * RT) + 32 * s + 8 * q;
+            lo += reinterpret_cast<const f32x4*>(p)[0];
+            hi += reinterpret_cast<const f32x4*>(p)[1];
           }
-          if (id == cur) d[b][p] = acc;
-        }
-    }
-#pragma unroll
-    for (int b = 0; b < kColBlocks; ++b) {
+        // rounded to bf16 for the product with up: a relative 2^-8 of each of
+        // the adapter's `rank` terms
+        tf[m][s] = frag(u32x4{bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]), bf16x2_rne(hi[0], hi[1]),
+                              bf16x2_rne(hi[2], hi[3])});
+      }
+    // columns past the last read it; depth past the rank is zeros
+    auto weights = [&](int of, int b, int p, int s) {
+      const int n = min(col0 + kColBlock * b + 8 * (r >> 2) + 4 * p + (r & 3), a.outer - 1);
+      const int j = 32 * s + 8 * q;
+      const u32x4 f = *reinterpret_cast<const u32x4*>(a.up + ((int64_t)of * a.outer + n) * a.rank +
+                                                      (j < a.rank ? j : 0));
+      return j < a.rank ? f : u32x4{0u, 0u, 0u, 0u};
+    };
+    auto finish = [&](int m, int b, const f32x4 (&d)[2]) {
+      const int64_t row = row0 + 16 * m;
       const int col = col0 + kColBlock * b + 8 * q;
-      const uint32_t w[4] = {yv[b].x, yv[b].y, yv[b].z, yv[b].w};
+      const uint32_t w[4] = {yv[m][b].x, yv[m][b].y, yv[m][b].z, yv[m][b].w};
       float f[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16) + d[b][j / 2][2 * (j & 1)];
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) + d[b][j / 2][2 * (j & 1) + 1];
+        f[2 * j] = __uint_as_float(w[j] << 16) + d[j / 2][2 * (j & 1)];
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) + d[j / 2][2 * (j & 1) + 1];
       }
       if (a.epilogue == NVFP4_EPI_GELU) {
 #pragma unroll
@@ -179,10 +209,57 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
       }
       const u32x4 v = u32x4{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
                             bf16x2_rne(f[6], f[7])};
-      if (live && col < a.outer) {
-        *reinterpret_cast<u32x4*>(a.out + row * a.outer + col) = v;
+      if (row < a.rows && col < a.outer) {
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(a.out + row * a.outer + col));
         top = max_u16x2(top, max8(v));
       }
+    };
+    if (uniform) {                             // its weights all at once
+      u32x4 uf[KS][kColBlocks][2];
+      if (first >= 0) {
+#pragma unroll
+        for (int b = 0; b < kColBlocks; ++b)
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) uf[s][b][p] = weights(first, b, p, s);
+      }
+#pragma unroll
+      for (int b = 0; b < kColBlocks; ++b)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          f32x4 d[2] = {f32x4{}, f32x4{}};
+          if (first >= 0) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+#pragma unroll
+              for (int s = 0; s < KS; ++s)
+                d[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(uf[s][b][p]), tf[m][s], d[p], 0, 0, 0);
+              if (id[m] < 0) d[p] = f32x4{};   // a row of none beside it
+            }
+          }
+          finish(m, b, d);
+        }
+    } else {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int b = 0; b < kColBlocks; ++b) {
+          f32x4 d[2] = {f32x4{}, f32x4{}};
+          for (uint64_t left = __ballot(lane < 16 && id[m] >= 0); left;) {
+            const int cur = __builtin_amdgcn_readlane(id[m], __builtin_ctzll(left));
+            left &= ~__ballot(lane < 16 && id[m] == cur);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              f32x4 acc = f32x4{};
+#pragma unroll
+              for (int s = 0; s < KS; ++s)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(weights(cur, b, p, s)), tf[m][s], acc, 0, 0, 0);
+              if (id[m] == cur) d[p] = acc;
+            }
+          }
+          finish(m, b, d);
+        }
     }
   }
   if (a.amax) {
@@ -191,33 +268,53 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
     if (lane == 0) wave_top[threadIdx.x >> 6] = m;
     __syncthreads();
     if (threadIdx.x == 0)
-      atomicMax(a.amax, max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3])));
+      raise_amax(a.amax, max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3])));
   }
 }
 
 __global__ void zero_lora_amax_kernel(uint32_t* p) { *p = 0u; }
 
-// Slices of `inner` in the first kernel: enough that the row tiles fill the
-// compute units twice, each at least 512 deep (one group of steps per wave).
+int rank_tiles(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+
+// Slices of `inner` in the first kernel, while the row tiles alone leave compute
+// units without work: at most 8, each at least 512 deep (the second kernel adds
+// them up, for every column block again).
 int slices_for(int64_t rows, int64_t inner) {
   const int64_t tiles = (rows + kRowTile - 1) / kRowTile;
-  int64_t s = 2 * compute_units() / (tiles > 0 ? tiles : 1);
+  int64_t s = compute_units() / (tiles > 0 ? tiles : 1);
   if (s > inner / 512) s = inner / 512;
-  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
-
-int rank_tiles(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
 template <int RT>
 hipError_t launch(const Lora& a, hipStream_t stream) {
   const int64_t tiles = (a.rows + kRowTile - 1) / kRowTile;
-  lora_down_kernel<RT><<<dim3((unsigned)tiles, a.slices), dim3(kLoraThreads), 0, stream>>>(a);
+  // a workgroup of 12 waves fills a compute unit: two row tiles each (every weight
+  // fragment then serves both) where that saves rounds over the compute units: at
+  // 4608 rows of 3072, rank 32, 144 workgroups take 15 us, 288 take 20
+  const int64_t units = compute_units();
+  const int64_t one = (tiles + units - 1) / units, two = ((tiles + 1) / 2 + units - 1) / units;
+  const int mt = RT <= 2 && 4 * two < 3 * one ? 2 : 1;
+  const int groups = (a.slice + 32 * group_steps(RT, mt) - 1) / (32 * group_steps(RT, mt));
+  const dim3 block(64 * (groups < kDownWaves ? groups : kDownWaves));
+  const dim3 down((unsigned)((tiles + mt - 1) / mt), a.slices);
+  if (mt == 2)
+    lora_down_kernel<RT, RT <= 2 ? 2 : 1><<<down, block, 0, stream>>>(a);
+  else
+    lora_down_kernel<RT, 1><<<down, block, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t waves = tiles * ((a.outer + kColBlock * kColBlocks - 1) / (kColBlock * kColBlocks));
-  const int64_t cap = (int64_t)compute_units() * 8;
+  // two row tiles a wave (the adapter's weights then serve both: 48 us against 55
+  // at 4608 x 9216, rank 32) where that still leaves every compute unit 16 waves
+  const int64_t cols = (a.outer + kColBlock * kColBlocks - 1) / (kColBlock * kColBlocks);
+  const int64_t cap = units * 64;
+  const int up = RT <= 2 && tiles * cols >= 32 * units ? 2 : 1;
+  const int64_t waves = (tiles + up - 1) / up * cols;
   const int64_t grid = (waves + 3) / 4 < cap ? (waves + 3) / 4 : cap;
-  lora_up_kernel<RT><<<dim3((unsigned)grid), dim3(kLoraThreads), 0, stream>>>(a);
+  if (up == 2)
+    lora_up_kernel<RT, RT <= 2 ? 2 : 1><<<dim3((unsigned)grid), dim3(kLoraThreads), 0, stream>>>(a);
+  else
+    lora_up_kernel<RT, 1><<<dim3((unsigned)grid), dim3(kLoraThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
 

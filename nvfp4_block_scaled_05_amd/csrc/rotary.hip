@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kRotThreads = 256;
 constexpr int kRotEntries = 512;   // (cos, sin) pairs a workgroup keeps: 4 KB of LDS
+constexpr int kRotTokens = 4;      // and tokens (at 16896 tokens of 48 heads: 2: 100 us, 4: 95, 8: 103)
 
 __device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -36,95 +37,137 @@ __device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
 // One head is held by LANES neighbouring lanes of 8 elements each (the ones
 // past dim / 8 idle), so a head's norm is a sum over LANES lanes and the half
 // layout's partner elements are one lane exchange away.
-template <int LANES>
+template <int LANES, bool HALF, bool NORM>
 __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
   __shared__ float2 turn[kRotEntries];
+  __shared__ int64_t place[kRotTokens][4];       // where each token's heads start: q, k, q out, k out
   const int pairs = a.rotary_dim / 2;
-  const int64_t first = (int64_t)blockIdx.x * a.tokens_per_group;
-  const int here = (int)(a.rows - first < a.tokens_per_group ? a.rows - first : a.tokens_per_group);
-  for (int e = threadIdx.x; e < here * pairs; e += kRotThreads) {
-    const int t = e / pairs, j = e - t * pairs;
-    // an axis index outside the positions' axes reads the nearest one
-    const int ax = a.axis ? min(max(a.axis[j], 0), a.axes - 1) : 0;
-    const double rev = a.turns[j] * (double)a.positions[(first + t) * a.axes + ax];
-    const float part = (float)(rev - __builtin_rint(rev));    // [-1/2, 1/2]
-    float s, c;
-    sincospif(2.0f * part, &s, &c);
-    turn[e] = float2{c * a.magnitude, s * a.magnitude};
-  }
-  __syncthreads();
   const int chunk = threadIdx.x % LANES, slot = threadIdx.x / LANES;
-  const int chunks = a.dim / 8, rot_chunks = a.rotary_dim / 8;
-  const bool mine = chunk < chunks;
-  const bool turned = chunk < rot_chunks;
+  const int rot_chunks = a.rotary_dim / 8, half_chunks = rot_chunks / 2;
+  const bool mine = chunk < a.dim / 8, turned = chunk < rot_chunks;
   const int heads = a.q.heads + a.k.heads;
-  const int half_chunks = rot_chunks / 2;
   // the half layout's partner chunk: that many lanes up or down
   const bool upper = chunk >= half_chunks;
-  const int partner = (threadIdx.x & 63) + (upper ? -half_chunks : half_chunks);
-  for (int base = 0; base < here * heads; base += kRotThreads / LANES) {
-    const int item = base + slot;
-    const bool live = item < here * heads && mine;
-    const int t = item / heads, head = item - t * heads;
-    const bool is_q = head < a.q.heads;
-    const RotaryHeads& v = is_q ? a.q : a.k;
-    const int hd = is_q ? head : head - a.q.heads;
-    const int64_t row = first + t, batch = row / a.tokens, token = row - batch * a.tokens;
-    u32x4 raw = u32x4{0u, 0u, 0u, 0u};
-    if (live)
-      raw = *reinterpret_cast<const u32x4*>(v.in + batch * v.in_batch + token * v.in_token +
-                                            hd * v.in_head + 8 * chunk);
-    float f[8];
-    unpack8(raw, f);
-    float rstd = 1.0f;
-    if (v.weight) {
-      float q = 0.0f;
+  const int partner = chunk + (upper ? -half_chunks : half_chunks);
+  const int partner_lane = (threadIdx.x & 63) - chunk + partner;
+  float wq[8], wk[8], pq[8], pk[8];              // the norms' weights of this lane's and its partner's elements
+  if (NORM) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q = __builtin_fmaf(f[j], f[j], q);
-#pragma unroll
-      for (int o = LANES / 2; o >= 1; o >>= 1) q += __shfl_xor(q, o, 64);
-      rstd = 1.0f / __builtin_sqrtf(q * a.inv_dim + a.eps);
-      if (live) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * v.weight[8 * chunk + j];
+    for (int j = 0; j < 8; ++j) {
+      wq[j] = a.q.weight && mine ? a.q.weight[8 * chunk + j] : 1.0f;
+      wk[j] = a.k.weight && mine ? a.k.weight[8 * chunk + j] : 1.0f;
+      if (HALF) {
+        pq[j] = a.q.weight && turned ? a.q.weight[8 * partner + j] : 1.0f;
+        pk[j] = a.k.weight && turned ? a.k.weight[8 * partner + j] : 1.0f;
       }
     }
-    u32x4 out;
-    if (a.layout == DIT_ROTARY_INTERLEAVED) {
-      if (live && turned) {
+  }
+  for (int64_t first = (int64_t)blockIdx.x * a.tokens_per_group; first < a.rows;
+       first += (int64_t)gridDim.x * a.tokens_per_group) {
+    const int here = (int)(a.rows - first < a.tokens_per_group ? a.rows - first : a.tokens_per_group);
+    for (int e = threadIdx.x; e < here * pairs; e += kRotThreads) {
+      const int t = e / pairs, j = e - t * pairs;
+      // an axis index outside the positions' axes reads the nearest one
+      const int ax = a.axis ? min(max(a.axis[j], 0), a.axes - 1) : 0;
+      const double rev = a.turns[j] * (double)a.positions[(first + t) * a.axes + ax];
+      const float part = (float)(rev - __builtin_rint(rev));    // [-1/2, 1/2]
+      float s, c;
+      sincospif(2.0f * part, &s, &c);
+      turn[e] = float2{c * a.magnitude, s * a.magnitude};
+    }
+    if (threadIdx.x < here) {
+      const uint32_t row = (uint32_t)(first + threadIdx.x), batch = row / (uint32_t)a.tokens;
+      const int64_t token = row - batch * (uint32_t)a.tokens;
+      place[threadIdx.x][0] = batch * a.q.in_batch + token * a.q.in_token;
+      place[threadIdx.x][1] = batch * a.k.in_batch + token * a.k.in_token;
+      place[threadIdx.x][2] = batch * a.q.out_batch + token * a.q.out_token;
+      place[threadIdx.x][3] = batch * a.k.out_batch + token * a.k.out_token;
+    }
+    __syncthreads();
+    const int items = here * heads;
+    int t = 0, head = slot;                      // item = t * heads + head
+    while (head >= heads) head -= heads, ++t;
+    u32x4 raw = u32x4{0u, 0u, 0u, 0u};
+    auto fetch = [&](int tt, int hh) {
+      const bool is_q = hh < a.q.heads;
+      const RotaryHeads& v = is_q ? a.q : a.k;
+      const int64_t at = place[tt][is_q ? 0 : 1] + (is_q ? hh : hh - a.q.heads) * v.in_head + 8 * chunk;
+      return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(v.in + at));
+    };
+    if (slot < items && mine) raw = fetch(t, head);
+    for (int base = 0; base < items; base += kRotThreads / LANES) {
+      const bool live = base + slot < items && mine;
+      const u32x4 now = raw;
+      const int t_now = t, head_now = head;
+      head += kRotThreads / LANES;
+      while (head >= heads) head -= heads, ++t;
+      // the next item's load runs under this one's arithmetic
+      if (base + slot + kRotThreads / LANES < items && mine) raw = fetch(t, head);
+      const bool is_q = head_now < a.q.heads;
+      const bool normed = NORM && (is_q ? a.q.weight : a.k.weight) != nullptr;
+      float f[8], g[8];
+      unpack8(now, f);
+      if (HALF)
+        unpack8(u32x4{(uint32_t)__shfl((int)now.x, partner_lane, 64), (uint32_t)__shfl((int)now.y, partner_lane, 64),
+                      (uint32_t)__shfl((int)now.z, partner_lane, 64), (uint32_t)__shfl((int)now.w, partner_lane, 64)},
+                g);
+      if (NORM) {
+        float q = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 cs = turn[t * pairs + 4 * chunk + j];
-          const float x = f[2 * j], y = f[2 * j + 1];
-          f[2 * j] = x * cs.x - y * cs.y;
-          f[2 * j + 1] = y * cs.x + x * cs.y;
-        }
-      }
-    } else {
-      float g[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = __shfl(f[j], partner, 64);
-      if (live && turned) {
+        for (int j = 0; j < 8; ++j) q = __builtin_fmaf(f[j], f[j], q);
+        q = group_sum<LANES>(q);
+        const float rstd = normed ? __builtin_amdgcn_rsqf(q * a.inv_dim + a.eps) : 1.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float2 cs = turn[t * pairs + 8 * (upper ? chunk - half_chunks : chunk) + j];
-          f[j] = upper ? f[j] * cs.x + g[j] * cs.y : f[j] * cs.x - g[j] * cs.y;
+          f[j] = f[j] * rstd * (is_q ? wq[j] : wk[j]);
+          if (HALF) g[j] = g[j] * rstd * (is_q ? pq[j] : pk[j]);
         }
       }
+      if (live && turned) {
+        if (HALF) {
+          const float2* cs = turn + t_now * pairs + 8 * (upper ? partner : chunk);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 v = cs[j];
+            f[j] = __builtin_fmaf(f[j], v.x, g[j] * (upper ? v.y : -v.y));
+          }
+        } else {
+          const float2* cs = turn + t_now * pairs + 4 * chunk;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = cs[j];
+            const float x = f[2 * j], y = f[2 * j + 1];
+            f[2 * j] = __builtin_fmaf(x, v.x, -(y * v.y));
+            f[2 * j + 1] = __builtin_fmaf(y, v.x, x * v.y);
+          }
+        }
+      }
+      u32x4 out = u32x4{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
+                        bf16x2_rne(f[6], f[7])};
+      if (!normed && !turned) out = now;         // untouched elements keep their bits
+      if (live) {
+        const RotaryHeads& v = is_q ? a.q : a.k;
+        const int64_t at = place[t_now][is_q ? 2 : 3] + (is_q ? head_now : head_now - a.q.heads) * v.out_head;
+        __builtin_nontemporal_store(out, reinterpret_cast<u32x4*>(v.out + at + 8 * chunk));
+      }
     }
-    out = u32x4{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
-                bf16x2_rne(f[6], f[7])};
-    if (!v.weight && !turned) out = raw;      // untouched elements keep their bits
-    if (live)
-      *reinterpret_cast<u32x4*>(v.out + batch * v.out_batch + token * v.out_token +
-                                hd * v.out_head + 8 * chunk) = out;
+    __syncthreads();                             // before the next tokens' table
   }
+}
+
+template <int LANES, bool HALF>
+hipError_t launch_norm(const Rotary& a, int64_t grid, hipStream_t stream) {
+  if (a.q.weight || a.k.weight)
+    rotary_kernel<LANES, HALF, true><<<dim3((unsigned)grid), dim3(kRotThreads), 0, stream>>>(a);
+  else
+    rotary_kernel<LANES, HALF, false><<<dim3((unsigned)grid), dim3(kRotThreads), 0, stream>>>(a);
+  return hipGetLastError();
 }
 
 template <int LANES>
 hipError_t launch(const Rotary& a, int64_t grid, hipStream_t stream) {
-  rotary_kernel<LANES><<<dim3((unsigned)grid), dim3(kRotThreads), 0, stream>>>(a);
-  return hipGetLastError();
+  return a.layout == DIT_ROTARY_HALF ? launch_norm<LANES, true>(a, grid, stream)
+                                     : launch_norm<LANES, false>(a, grid, stream);
 }
 
 }  // namespace
@@ -135,10 +178,11 @@ hipError_t launch_rotary(Rotary a, hipStream_t stream) {
   // would leave compute units without a workgroup
   const int64_t fill = (a.rows + 4 * compute_units() - 1) / (4 * compute_units());
   int per = kRotEntries / (a.rotary_dim / 2);
-  if (per > 8) per = 8;
+  if (per > kRotTokens) per = kRotTokens;
   if (per > fill) per = (int)fill;
   a.tokens_per_group = per;
-  const int64_t grid = (a.rows + per - 1) / per;
+  const int64_t groups = (a.rows + per - 1) / per;
+  const int64_t grid = groups < (1 << 20) ? groups : (1 << 20);    // the kernel strides over the rest
   const int chunks = a.dim / 8;
   if (chunks <= 4) return launch<4>(a, grid, stream);
   if (chunks <= 8) return launch<8>(a, grid, stream);
