@@ -305,53 +305,44 @@ struct TileLoader {
 
 // Which part of the problem a workgroup has.
 struct Place {
-  int64_t pair, batch;                          // pair: (batch, kv head, split)
-  int kvh, split, row_tile, keys;
+  int64_t batch;
+  int kvh, row_tile, keys;
   const uint16_t *k, *v;
   const uint8_t* mask;
 };
 
-__device__ __forceinline__ Place place_of(const Attention& a) {
-  Place p;
-  // Workgroups are dealt to the 8 XCDs in turn.  With row tiles that share a
-  // (batch, kv head, split)'s keys, eight such pairs run side by side, each on
-  // one XCD, whose L2 keeps its keys; entries of unequal lengths are spread over
-  // all of them.  (One contiguous range of pairs per XCD would give an XCD one
-  // batch entry: 242 us against 167 for a CFG pair of 512 and 77 text states.)
-  // Fewer than 2^24 workgroups, so 32 bits do.
-  const uint32_t pos = blockIdx.x, tiles = (uint32_t)a.row_tiles, splits = (uint32_t)a.splits;
-  const uint32_t heads = (uint32_t)a.batch * (uint32_t)a.kv_heads;
-  uint32_t bh;
-  if (tiles == 1) {                              // every head's first split, then the second ones, ...
-    p.split = (int)(pos / heads);
-    bh = pos - (uint32_t)p.split * heads;
-    p.pair = (int64_t)bh * splits + p.split;
-    p.row_tile = 0;
-  } else {
-    const uint32_t pairs = heads * splits, full = pairs / kXcds * kXcds;
-    uint32_t pair;
-    if (pos < full * tiles) {
-      const uint32_t slot = pos / kXcds;
-      pair = slot / tiles * kXcds + pos % kXcds;
-      p.row_tile = (int)(slot % tiles);
-    } else {
-      const uint32_t rest = pos - full * tiles;
-      pair = full + rest / tiles;
-      p.row_tile = (int)(rest % tiles);
-    }
-    p.pair = pair;
-    bh = pair / splits;
-    p.split = (int)(pair - bh * splits);
-  }
+// A (batch, kv head) and the keys its entry sees.
+__device__ __forceinline__ void place_head(const Attention& a, Place& p, uint32_t bh) {
   const uint32_t batch = bh / (uint32_t)a.kv_heads;
   p.batch = batch;
   p.kvh = (int)(bh - batch * (uint32_t)a.kv_heads);
-  p.keys = a.keys;
-  if (a.lengths) p.keys = min(max(__builtin_amdgcn_readfirstlane(a.lengths[p.batch]), 0), a.keys);
   p.k = a.k + p.batch * a.k_batch + p.kvh * a.k_head;
   p.v = a.v + p.batch * a.v_batch + p.kvh * a.v_head;
   p.mask = a.mask ? a.mask + p.batch * a.mask_stride : nullptr;
-  return p;
+}
+__device__ __forceinline__ int seen_keys(const Attention& a, const Place& p) {
+  return a.lengths ? min(max(__builtin_amdgcn_readfirstlane(a.lengths[p.batch]), 0), a.keys) : a.keys;
+}
+
+// Work unit u: a row tile of a (batch, kv head).  Workgroups are dealt to the 8
+// XCDs in turn; eight heads run side by side, each on one XCD, whose L2 keeps its
+// keys, so entries of unequal lengths are spread over all of them.  (One
+// contiguous range of heads per XCD gives an XCD one batch entry: 237 us against
+// 190 for a CFG pair of 512 and 77 text states.)
+__device__ __forceinline__ void place_unit(const Attention& a, Place& p, uint32_t u) {
+  const uint32_t tiles = (uint32_t)a.row_tiles, heads = (uint32_t)a.batch * (uint32_t)a.kv_heads;
+  const uint32_t full = heads / kXcds * kXcds;
+  uint32_t bh;
+  if (u < full * tiles) {
+    const uint32_t slot = u / kXcds;
+    bh = slot / tiles * kXcds + u % kXcds;
+    p.row_tile = (int)(slot % tiles);
+  } else {
+    const uint32_t rest = u - full * tiles;
+    bh = full + rest / tiles;
+    p.row_tile = (int)(rest % tiles);
+  }
+  place_head(a, p, bh);
 }
 
 // The visible keys among the KEYS from `first` on (wave-uniform).
@@ -412,15 +403,34 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
   constexpr int kRowPieces = A::kPieces, kRowsPerLoad = 64 / kRowPieces;
   __shared__ __attribute__((aligned(1024))) uint8_t k0[A::kTileBytes], v0[A::kTileBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t k1[A::kTileBytes], v1[A::kTileBytes];
-  const Place p = place_of(a);
+  // every unit's first split, then the second ones, ...
+  Place p;
+  const uint32_t split = blockIdx.x / (uint32_t)a.units, unit = blockIdx.x - split * (uint32_t)a.units;
+  place_unit(a, p, unit);
   const int wave = wave_id();
   A w;
   w.start(a.scale);
+
+  // this wave's query rows (row = token * group + head within the group), read
+  // a whole row at a time, before anything that waits
+  const int64_t rows = (int64_t)a.queries * a.group;
+  const int64_t row0 = (int64_t)p.row_tile * 128 + wave * 32;
+  const int piece = w.lane % kRowPieces;
+  u32x4 qrow[32 / kRowsPerLoad];
+  {
+    const int at = 8 * piece < a.dim ? 8 * piece : 0;
+    RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad);
+#pragma unroll
+    for (int i = 0; i < 32 / kRowsPerLoad; ++i, step.next())
+      qrow[i] = *reinterpret_cast<const u32x4*>(a.q + p.batch * a.q_batch +
+                                                step.offset(a, p, a.q_token, a.q_head) + at);
+  }
+  p.keys = seen_keys(a, p);
   TileLoader<DP, 2, 4> load;
   load.start(a, wave);
   const int tiles = (p.keys + A::kKeys - 1) / A::kKeys;
   const int share = (tiles + a.splits - 1) / a.splits;
-  const int last = min((p.split + 1) * share, tiles);
+  const int last = min(((int)split + 1) * share, tiles);
   // the next tile after t that has a visible key
   auto next = [&](int t, uint64_t& seen) {
     for (++t; t < last; ++t)
@@ -428,33 +438,19 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
     return t;
   };
   uint64_t seen = 0, seen_next = 0;
-  int t = next(p.split * share - 1, seen);
+  int t = next((int)split * share - 1, seen);
   if (t < last)
     load.issue(p.k + (int64_t)t * A::kKeys * a.k_token, p.v + (int64_t)t * A::kKeys * a.v_token, seen, k0, v0);
 
-  // this wave's query rows (row = token * group + head within the group), read
-  // a whole row at a time and turned into fragments through its own 32 rows of
-  // the second buffers, which no tile uses yet
-  const int64_t rows = (int64_t)a.queries * a.group;
-  const int64_t row0 = (int64_t)p.row_tile * 128 + wave * 32;
+  // the query rows become fragments through 32 rows of the second buffers, which
+  // no tile uses yet
   uint8_t* own = (wave < 2 ? k1 : v1) + (wave & 1) * (32 * A::kRowBytes);
   {
-    u32x4 f[32 / kRowsPerLoad];
-    const int piece = w.lane % kRowPieces;
-    const int at = 8 * piece < a.dim ? 8 * piece : 0;
-    RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad);
-#pragma unroll
-    for (int i = 0; i < 32 / kRowsPerLoad; ++i, step.next())
-      f[i] = *reinterpret_cast<const u32x4*>(a.q + p.batch * a.q_batch +
-                                             step.offset(a, p, a.q_token, a.q_head) + at);
-    if (8 * piece >= a.dim) {
-#pragma unroll
-      for (int i = 0; i < 32 / kRowsPerLoad; ++i) f[i] = u32x4{0u, 0u, 0u, 0u};
-    }
 #pragma unroll
     for (int i = 0; i < 32 / kRowsPerLoad; ++i) {
       const int r = i * kRowsPerLoad + w.lane / kRowPieces;
-      *reinterpret_cast<u32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4)) = f[i];
+      *reinterpret_cast<u32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4)) =
+          8 * piece < a.dim ? qrow[i] : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int st = 0; st < A::kSteps; ++st)
@@ -484,10 +480,8 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
 #undef ATTEND_TURN
 
   const float l = halves_sum(w.sum);
-  const int64_t row = row0 + w.col;
   if (a.splits > 1) {      // unnormalised partial sums, the maximum and the sum
-    if (row >= rows) return;
-    const int64_t slot = p.pair * rows + row;
+    const int64_t slot = ((int64_t)unit * a.splits + split) * 128 + wave * 32 + w.col;
     float* out = a.part + slot * DP;
 #pragma unroll
     for (int b = 0; b < A::kBlocks; ++b)
@@ -509,7 +503,6 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
                                 8 * w.half) =
           u32x2{bf16x2_rne(w.o[b][4 * g] * inv, w.o[b][4 * g + 1] * inv),
                 bf16x2_rne(w.o[b][4 * g + 2] * inv, w.o[b][4 * g + 3] * inv)};
-  const int piece = w.lane % kRowPieces;
   RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad);
 #pragma unroll
   for (int i = 0; i < 32 / kRowsPerLoad; ++i, step.next()) {
@@ -533,11 +526,16 @@ __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
   using A = Attend<DP, 1>;
   __shared__ __attribute__((aligned(1024))) uint8_t even[4 * A::kTileBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t odd[4 * A::kTileBytes];
-  const Place p = place_of(a);
+  // every head's first split, then the second ones, ...
+  Place p;
+  const uint32_t heads = (uint32_t)a.units, split = blockIdx.x / heads, head = blockIdx.x - split * heads;
+  place_head(a, p, head);
+  p.keys = seen_keys(a, p);
   const int64_t rows = (int64_t)a.queries * a.group;
-  const int first = p.split * a.share * 4;       // a split is `share` groups of four tiles
+  const int64_t slot0 = ((int64_t)head * a.splits + split) * rows;
+  const int first = (int)split * a.share * 4;    // a split is `share` groups of four tiles
   if (a.splits > 1 && first * A::kKeys >= p.keys) {        // past this entry's length
-    if (threadIdx.x < rows) a.stats[p.pair * rows + threadIdx.x] = float2{-__builtin_inff(), 0.0f};
+    if (threadIdx.x < rows) a.stats[slot0 + threadIdx.x] = float2{-__builtin_inff(), 0.0f};
     return;
   }
   const int wave = wave_id();
@@ -682,7 +680,7 @@ __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
       for (int i = 0; i < 4; ++i) s += *reinterpret_cast<const f32x4*>(park + (i * 32 + r) * kPart + d);
       const float total = all_sum[r];
       if (a.splits > 1) {
-        const int64_t slot = p.pair * rows + r;
+        const int64_t slot = slot0 + r;
         *reinterpret_cast<f32x4*>(a.part + slot * DP + col) = s;
         if (col == 0) a.stats[slot] = float2{all_top[r], total};
       } else if (col < a.dim) {
@@ -697,15 +695,24 @@ __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
 
 // Joins the splits of a row, one wave per row: partial sums weighted by
 // 2^(their maximum - the largest), in split order.  Lane s holds split s's
-// maximum and sum (at most 64 splits).
+// maximum and sum (at most 64 splits).  A unit has `unit_rows` rows' slots a split.
 template <int DP>
-__global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
+__global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int unit_rows) {
   const int lane = threadIdx.x & 63;
-  const int64_t rows = (int64_t)a.queries * a.group;
-  const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();      // (batch, kv head, row)
-  if (at >= (int64_t)a.batch * a.kv_heads * rows) return;
-  const int64_t bh = at / rows, row = at - bh * rows;
-  const int64_t first = bh * a.splits * rows + row;
+  const int64_t rows = unit_rows;
+  const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();
+  const uint32_t unit = (uint32_t)(at / rows), in = (uint32_t)(at - unit * rows);
+  if (unit >= (uint32_t)a.units) return;
+  Place p;
+  int64_t row = in;
+  if (a.row_tiles == 0) {                        // few rows: a unit is a head
+    place_head(a, p, unit);
+  } else {
+    place_unit(a, p, unit);
+    row += (int64_t)p.row_tile * 128;
+    if (row >= (int64_t)a.queries * a.group) return;
+  }
+  const int64_t first = (int64_t)unit * a.splits * rows + in;
   float2 st = float2{0.0f, 0.0f};
   if (lane < a.splits) st = a.stats[first + lane * rows];
   float top = st.y != 0.0f ? st.x : -__builtin_inff();
@@ -734,9 +741,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
     }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t batch = bh / a.kv_heads, token = row / a.group;
-  const int64_t head = (bh - batch * a.kv_heads) * a.group + (row - token * a.group);
-  uint16_t* out = a.out + batch * a.o_batch + token * a.o_token + head * a.o_head;
+  uint16_t* out = output_row(a, p, row);
   if (DP == 128) {
     if (2 * lane < a.dim)
       *reinterpret_cast<uint32_t*>(out + 2 * lane) = bf16x2_rne(o[0] * inv, o[DP / 64 - 1] * inv);
@@ -745,30 +750,39 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
   }
 }
 
-// How a call is run.  `few`: at most 32 rows per kv head, the kernel whose waves
-// share the rows.  Its splits are of a fixed number of keys, so entries of
-// unequal lengths cost their own keys only: enough for four workgroups a
-// compute unit, each at least 256 keys.  The other kernel splits as many ways
-// as give every compute unit two workgroups, each split at least four tiles.
+// How a call is run.
+//   few: at most 32 rows per kv head, the kernel whose waves share the rows.  Its
+// splits are of a fixed number of keys, so entries of unequal lengths cost their
+// own keys only: enough for four workgroups a compute unit, each at least 256
+// keys.
+//   Otherwise units of 128 rows, whose keys are split where the units leave compute
+// units without work: up to 12 ways, each at least four tiles, towards two
+// workgroups a compute unit if that takes four ways or more, else one (4608 keys of
+// 24 heads: 96 units in 5 ways 54 us, in 2 ways 61, whole 89; 192 units in 2 ways
+// 96, whole 91: partial sums and their join cost about what they save).
 struct Plan {
   bool few;
+  int64_t row_tiles, units, slots;               // slots: rows of partial sums in the workspace
   int splits, share;
 };
 
 Plan plan_for(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys) {
-  const int64_t heads = batch * kv_heads > 0 ? batch * kv_heads : 1;
+  const int64_t heads = batch * kv_heads;
   if (rows <= 32) {
     const int64_t groups = (keys + 127) / 128;           // of four tiles of 32
     int64_t share = groups * heads / (4 * compute_units());
     if (share < 2) share = 2;
     if (share < (groups + 63) / 64) share = (groups + 63) / 64;
-    const int64_t splits = (groups + share - 1) / share;
-    return {true, (int)(splits < 1 ? 1 : splits), (int)share};
+    const int64_t splits = groups > 0 ? (groups + share - 1) / share : 1;
+    return {true, 0, heads, heads * splits * rows, (int)splits, (int)share};
   }
-  const int64_t groups = heads * ((rows + 127) / 128), tiles = (keys + 63) / 64;
-  int64_t s = 2 * compute_units() / groups;
-  if (s > tiles / 4) s = tiles / 4;
-  return {false, (int)(s < 1 ? 1 : s > 64 ? 64 : s), 0};
+  const int64_t row_tiles = (rows + 127) / 128, units = heads * row_tiles, tiles = (keys + 63) / 64;
+  int64_t splits = 2 * compute_units() / units;
+  if (splits < 4) splits = compute_units() / units;
+  if (splits > 12) splits = 12;
+  if (splits > tiles / 4) splits = tiles / 4;
+  if (splits < 1) splits = 1;
+  return {false, row_tiles, units, units * splits * 128, (int)splits, 0};
 }
 
 int padded_dim(int64_t dim) { return dim <= 64 ? 64 : 128; }
@@ -778,30 +792,28 @@ int padded_dim(int64_t dim) { return dim <= 64 ? 64 : 128; }
 size_t attention_workspace_bytes(int64_t batch, int64_t queries, int64_t keys, int64_t heads,
                                  int64_t kv_heads, int64_t dim) {
   if (batch == 0 || queries == 0) return 0;
-  const int64_t rows = queries * (heads / kv_heads);
-  const int splits = plan_for(batch, kv_heads, rows, keys).splits;
-  if (splits == 1) return 0;
-  return (size_t)(batch * kv_heads * splits * rows) * (padded_dim(dim) * 4 + 8);
+  const Plan plan = plan_for(batch, kv_heads, queries * (heads / kv_heads), keys);
+  return plan.splits == 1 ? 0 : (size_t)plan.slots * (padded_dim(dim) * 4 + 8);
 }
 
 hipError_t launch_attention(Attention a, void* workspace, size_t workspace_bytes,
                             hipStream_t stream) {
-  const int64_t rows = (int64_t)a.queries * a.group, bh = (int64_t)a.batch * a.kv_heads;
-  const Plan plan = plan_for(a.batch, a.kv_heads, rows, a.keys);
+  const int64_t rows = (int64_t)a.queries * a.group;
   const int dp = padded_dim(a.dim);
+  Plan plan = plan_for(a.batch, a.kv_heads, rows, a.keys);
+  if (plan.splits > 1 && (!workspace || workspace_bytes < (size_t)plan.slots * (dp * 4 + 8))) {
+    plan.share *= plan.splits;
+    plan.splits = 1;
+  }
+  a.row_tiles = plan.row_tiles;
+  a.units = plan.units;
   a.splits = plan.splits;
   a.share = plan.share;
-  const size_t need = (size_t)(bh * a.splits * rows) * (dp * 4 + 8);
-  if (a.splits > 1 && (!workspace || workspace_bytes < need)) {
-    a.share *= a.splits;
-    a.splits = 1;
-  }
-  if (a.splits > 1) {
+  if (plan.splits > 1) {
     a.part = static_cast<float*>(workspace);
-    a.stats = reinterpret_cast<float2*>(a.part + bh * a.splits * rows * dp);
+    a.stats = reinterpret_cast<float2*>(a.part + plan.slots * dp);
   }
-  a.row_tiles = plan.few ? 1 : (rows + 127) / 128;
-  const dim3 grid((unsigned)(bh * a.splits * a.row_tiles)), block(256);
+  const dim3 grid((unsigned)(plan.units * plan.splits)), block(256);
   if (plan.few)
     dp == 64 ? attention_few_kernel<64><<<grid, block, 0, stream>>>(a)
              : attention_few_kernel<128><<<grid, block, 0, stream>>>(a);
@@ -809,10 +821,11 @@ hipError_t launch_attention(Attention a, void* workspace, size_t workspace_bytes
     dp == 64 ? attention_kernel<64><<<grid, block, 0, stream>>>(a)
              : attention_kernel<128><<<grid, block, 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  const dim3 join((unsigned)((bh * rows + 3) / 4));
-  dp == 64 ? attention_join_kernel<64><<<join, block, 0, stream>>>(a)
-           : attention_join_kernel<128><<<join, block, 0, stream>>>(a);
+  if (e != hipSuccess || plan.splits == 1) return e;
+  const int unit_rows = plan.few ? (int)rows : 128;
+  const dim3 join((unsigned)((plan.units * unit_rows + 3) / 4));
+  dp == 64 ? attention_join_kernel<64><<<join, block, 0, stream>>>(a, unit_rows)
+           : attention_join_kernel<128><<<join, block, 0, stream>>>(a, unit_rows);
   return hipGetLastError();
 }
 

@@ -120,11 +120,13 @@ struct Attention {
   int64_t mask_stride;
   int batch, queries, keys, kv_heads, group, dim;   // group: query heads per kv head
   float scale;
-  // filled in by the launch
-  int64_t row_tiles;
-  int splits, share;             // share: groups of four 32-key tiles a split has
-  float* part;                   // [batch][kv head][split][row][padded dim]
-  float2* stats;                 // [batch][kv head][split][row]: maximum, sum
+  // filled in by the launch: row tiles per kv head (0: few rows), work units (a row
+  // tile of a head, or a head), the splits of each over its keys, and of the few-row
+  // kernel the groups of four 32-key tiles a split has
+  int64_t row_tiles, units;
+  int splits, share;
+  float* part;                   // [unit][split][row][padded dim]
+  float2* stats;                 // [unit][split][row]: maximum, sum
 };
 // Workspace bytes launch_attention can use to split the keys (0: no split).
 size_t attention_workspace_bytes(int64_t batch, int64_t queries, int64_t keys, int64_t heads,
