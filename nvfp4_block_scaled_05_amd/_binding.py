@@ -27,13 +27,7 @@ _I64 = ctypes.c_int64
 _F = ctypes.c_float
 _INT = ctypes.c_int
 
-
-class DitHeads(ctypes.Structure):
-    """dit_heads: bf16 heads in memory, strides in elements."""
-    _fields_ = [("data", _P), ("batch_stride", _I64), ("token_stride", _I64), ("head_stride", _I64)]
-
-
-_HEADS = ctypes.POINTER(DitHeads)
+_HEADS = ctypes.c_char_p                # a dit_heads packed into bytes (read only by the call)
 SIGNATURES = {
     "nvfp4_abi_version": (ctypes.c_int, []),
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),

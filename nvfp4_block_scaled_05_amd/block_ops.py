@@ -7,30 +7,60 @@ allocated with torch.  Everything is forward only: no output carries a
 gradient.
 """
 
-import ctypes
 import math
+import struct
 from collections import namedtuple
 
 from . import _NO_WORKSPACE, _device, _epilogue, _matrix, _opt, _ptr, _stream, _tensor, _torch
-from ._binding import DitHeads, check, load
+from ._binding import Nvfp4Error, load
 
 NORMS = {"none": 0, "layer": 1, "rms": 2}
 ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
 ROTARY_SCALINGS = ("none", "linear", "ntk", "yarn")
 
 
-def _place(first, named):
-    """_device on a dict of tensors, for calls of a few microseconds: the common
-    case (all on the current GPU) is one integer comparison a tensor.  Returns
-    the device of ``first``, one of them."""
-    at = first.get_device()
+# These calls take a few microseconds on the GPU when they are small, and their
+# checks have to cost no more than that: what is common (everything given is right
+# and on the current device) is a comparison or two a tensor, and names and
+# messages are put together only for an error.
+
+_CURRENT_DEVICE = None
+_RAW_STREAM = None
+
+
+def _place(tensors, names):
+    """_device on some tensors (None skipped, the first given).  Returns the
+    index of their device, which is the current one."""
+    global _CURRENT_DEVICE
+    at = tensors[0].get_device()
     good = at >= 0
-    for t in named.values():
+    for t in tensors:
         if t is not None and t.get_device() != at:
             good = False
-    if not good or at != _torch().cuda.current_device():
-        return _device(**named)                      # raises, with the name
-    return first.device
+    if good:
+        if _CURRENT_DEVICE is None:
+            torch = _torch()
+            torch.cuda.current_device()                      # initialises the device API
+            _CURRENT_DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        good = _CURRENT_DEVICE() == at
+    if not good:
+        _device(**dict(zip(names.split(), tensors)))         # raises, with the name
+    return at
+
+
+def _stream_at(at):
+    """The current stream of device ``at``, the current one."""
+    global _RAW_STREAM
+    if _RAW_STREAM is None:
+        _RAW_STREAM = getattr(_torch()._C, "_cuda_getCurrentRawStream", False)
+    return _RAW_STREAM(at) if _RAW_STREAM else _stream()
+
+
+def _like(t, name, dtype, shape):
+    """_tensor for a torch.Size that is at hand; an error takes the long way."""
+    if (not isinstance(t, _torch().Tensor) or t.dtype != dtype or t.shape != shape
+            or not t.is_contiguous()):
+        _tensor(t, name, dtype, shape, 0)
 
 
 def _choice(value, choices, name):
@@ -43,20 +73,20 @@ def _rows3(t, name):
     """(batch, tokens, channels) of a [tokens, channels] or [batch, tokens, channels] tensor."""
     if not isinstance(t, _torch().Tensor) or t.dim() not in (2, 3):
         raise ValueError(f"{name}: expected a 2-D or 3-D torch.Tensor")
-    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+    return t.shape if t.dim() == 3 else (1, *t.shape)
 
 
-def _vector(t, name, batch, channels, dtype):
+def _vector(t, name, shape, dtype):
     """The stride of a [batch, channels] tensor whose rows are dense (a chunk of
     a wider one), after its checks."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != (batch, channels):
-        raise ValueError(f"{name}: expected a torch.Tensor of shape {(batch, channels)}")
+    if not isinstance(t, _torch().Tensor) or t.shape != shape:
+        raise ValueError(f"{name}: expected a torch.Tensor of shape {shape}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if channels > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the last dimension must be dense (got strides {tuple(t.stride())})")
-    return t.stride(0) if batch > 1 else 0
+    row, dense = t.stride()
+    if dense != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the last dimension must be dense (got strides {(row, dense)})")
+    return row if shape[0] > 1 else 0
 
 
 def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weight=None, bias=None,
@@ -86,7 +116,7 @@ def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weigh
     _tensor(x, "x", torch.float32 if fp32 else torch.bfloat16, min_numel=0)
     if channels <= 0 or channels % 8 or channels > 16384:
         raise ValueError(f"x: channels must be a positive multiple of 8 up to 16384, got {channels}")
-    norm_id = _choice("none" if norm is None else norm, NORMS, "norm")
+    norm_id = NORMS["none"] if norm is None else _choice(norm, NORMS, "norm")
     post_id = _choice(post_norm, NORMS, "post_norm")
     if y is None:
         for name, v in (("gate", gate), ("post_weight", post_weight), ("residual_out", residual_out)):
@@ -103,35 +133,45 @@ def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weigh
             raise ValueError("norm None needs y")
     if not (eps > 0 and math.isfinite(eps) and math.isfinite(residual_scale)):
         raise ValueError(f"eps must be positive, residual_scale finite; got {eps}, {residual_scale}")
-    _opt(y, "y", torch.bfloat16, x.shape, 0)
+    shape = x.shape
+    if y is not None:
+        _like(y, "y", torch.bfloat16, shape)
     mod = None                                # the type of the first vector; all have it
-    strides = [0, 0, 0]
-    for i, v in enumerate((gate, scale, shift)):
+    g_stride = sc_stride = sh_stride = 0
+    for v in (gate, scale, shift):
         if v is not None:
-            name = ("gate", "scale", "shift")[i]
-            if mod is None:
-                mod = getattr(v, "dtype", None)
-                if mod not in (torch.bfloat16, torch.float32):
-                    raise ValueError(f"{name}: dtype {mod}, expected bfloat16 or float32")
-            strides[i] = _vector(v, name, batch, channels, mod)
-    _opt(weight, "weight", torch.float32, (channels,))
-    _opt(bias, "bias", torch.float32, (channels,))
-    _opt(post_weight, "post_weight", torch.float32, (channels,))
-    _opt(amax, "amax", torch.float32)
-    _opt(out, "out", torch.bfloat16, x.shape, 0)
-    _opt(residual_out, "residual_out", x.dtype, x.shape, 0)
-    dev = _place(x, {"x": x, "y": y, "gate": gate, "scale": scale, "shift": shift, "weight": weight,
-                  "bias": bias, "post_weight": post_weight, "amax": amax, "out": out,
-                  "residual_out": residual_out})
+            mod = getattr(v, "dtype", None)
+            if mod not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"gate, scale, shift: dtype {mod}, expected bfloat16 or float32")
+            break
+    if gate is not None:
+        g_stride = _vector(gate, "gate", (batch, channels), mod)
+    if scale is not None:
+        sc_stride = _vector(scale, "scale", (batch, channels), mod)
+    if shift is not None:
+        sh_stride = _vector(shift, "shift", (batch, channels), mod)
+    for v, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight")):
+        if v is not None:
+            _tensor(v, name, torch.float32, (channels,))
+    if amax is not None:
+        _tensor(amax, "amax", torch.float32)
+    if out is not None:
+        _like(out, "out", torch.bfloat16, shape)
+    if residual_out is not None:
+        _like(residual_out, "residual_out", x.dtype, shape)
+    at = _place((x, y, gate, scale, shift, weight, bias, post_weight, amax, out, residual_out),
+                "x y gate scale shift weight bias post_weight amax out residual_out")
     if out is None and norm is not None:
-        out = torch.empty_like(x) if not fp32 else torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(x, dtype=torch.bfloat16) if fp32 else torch.empty_like(x)
     if residual_out is None and y is not None:
         residual_out = torch.empty_like(x)
-    check(load().dit_gated_norm(
-        x.data_ptr(), fp32, _ptr(y), _ptr(gate), strides[0], _ptr(scale), strides[1], _ptr(shift),
-        strides[2], mod is torch.float32, _ptr(weight), _ptr(bias), _ptr(post_weight), batch, tokens,
+    status = load().dit_gated_norm(
+        x.data_ptr(), fp32, _ptr(y), _ptr(gate), g_stride, _ptr(scale), sc_stride, _ptr(shift),
+        sh_stride, mod is torch.float32, _ptr(weight), _ptr(bias), _ptr(post_weight), batch, tokens,
         channels, norm_id, post_id, residual_scale, eps, _ptr(residual_out), _ptr(out),
-        _ptr(amax), _stream()), "dit_gated_norm")
+        _ptr(amax), _stream_at(at))
+    if status:
+        raise Nvfp4Error(status, "dit_gated_norm")
     return (x if y is None else residual_out), out
 
 
@@ -197,6 +237,10 @@ def rotary_plan(rotary_dim, base=10000.0, axes=None, scaling="none", factor=1.0,
                       0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0)
 
 
+#: the dit_heads of the C ABI, as bytes: data, then the batch, token and head strides
+_VIEW = struct.Struct("@Pqqq").pack
+
+
 def _heads(t, name, out=False):
     """(batch, tokens, heads, dim) and the C view of bf16 heads [tokens, heads,
     dim] or [batch, tokens, heads, dim]: dim dense, other strides multiples of
@@ -228,14 +272,15 @@ def _heads(t, name, out=False):
             if s < reach:
                 raise ValueError(f"{name}: elements overlap (strides {tuple(t.stride())})")
             reach = s * size
-    return (b, n, h, d), DitHeads(t.data_ptr(), sb, sn, sh)
+    return (b, n, h, d), _VIEW(t.data_ptr(), sb, sn, sh)
 
 
-def _new_heads(shape, shape4, dev):
-    """A new dense output of ``shape`` (``shape4`` with its batch) and its C view."""
-    t = _torch().empty(shape, dtype=_torch().bfloat16, device=dev)
+def _new_heads(like, shape4):
+    """A new dense output like ``like`` (``shape4`` its shape with a batch) and its C view."""
+    torch = _torch()
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
     _, n, h, d = shape4
-    return t, DitHeads(t.data_ptr(), n * h * d, h * d, d)
+    return t, _VIEW(t.data_ptr(), n * h * d, h * d, d)
 
 
 def _out_heads(out, like, name):
@@ -290,17 +335,18 @@ def rotary(q, positions, plan, k=None, layout="interleaved", q_weight=None, k_we
     _opt(k_weight, "k_weight", torch.float32, (dim,))
     qo = _out_heads(out, q, "out")
     ko = None if k is None else _out_heads(k_out, k, "k_out")
-    dev = _place(q, {"q": q, "k": k, "positions": positions, "turns": plan.turns, "axis": plan.axis,
-                  "q_weight": q_weight, "k_weight": k_weight, "out": out, "k_out": k_out})
+    at = _place((q, k, positions, plan.turns, plan.axis, q_weight, k_weight, out, k_out),
+                "q k positions turns axis q_weight k_weight out k_out")
     if out is None:
-        out, qo = _new_heads(q.shape, shape, dev)
+        out, qo = _new_heads(q, shape)
     if k is not None and k_out is None:
-        k_out, ko = _new_heads(k.shape, k_shape, dev)
-    ref = ctypes.byref
-    check(load().dit_rotary(
-        ref(qv), ref(qo), heads, kv and ref(kv), ko and ref(ko), kv_heads, positions.data_ptr(),
-        plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(), plan.magnitude, _ptr(q_weight),
-        _ptr(k_weight), eps, batch, tokens, dim, plan.rotary_dim, layout_id, _stream()), "dit_rotary")
+        k_out, ko = _new_heads(k, k_shape)
+    status = load().dit_rotary(
+        qv, qo, heads, kv, ko, kv_heads, positions.data_ptr(), plan.axes, plan.turns.data_ptr(),
+        plan.axis.data_ptr(), plan.magnitude, _ptr(q_weight), _ptr(k_weight), eps, batch, tokens,
+        dim, plan.rotary_dim, layout_id, _stream_at(at))
+    if status:
+        raise Nvfp4Error(status, "dit_rotary")
     return out if k is None else (out, k_out)
 
 
@@ -357,17 +403,22 @@ def cross_attention(q, k, v, kv_lengths=None, key_mask=None, scale=None, out=Non
         mask_stride = key_mask.stride(0) if batch > 1 else 0
     ov = _out_heads(out, q, "out")
     ws = None if workspace is _NO_WORKSPACE else _opt(workspace, "workspace", torch.uint8)
-    dev = _place(q, {"q": q, "k": k, "v": v, "kv_lengths": kv_lengths, "key_mask": key_mask,
-                  "out": out, "workspace": ws})
+    at = _place((q, k, v, kv_lengths, key_mask, out, ws), "q k v kv_lengths key_mask out workspace")
     if out is None:
-        out, ov = _new_heads(q.shape, (batch, queries, heads, dim), dev)
+        out, ov = _new_heads(q, (batch, queries, heads, dim))
+    lib = load()
+    ws_bytes = 0
     if workspace is _NO_WORKSPACE:
-        ws = cross_attention_workspace(batch, queries, keys, heads, kv_heads, dim, dev)
-    ref = ctypes.byref
-    check(load().dit_cross_attention(
-        ref(qv), ref(kv), ref(vv), _ptr(kv_lengths), _ptr(key_mask), mask_stride, batch, queries,
-        keys, heads, kv_heads, dim, scale, ref(ov), _ptr(ws), 0 if ws is None else ws.numel(),
-        _stream()), "dit_cross_attention")
+        ws_bytes = lib.dit_cross_attention_workspace_bytes(batch, queries, keys, heads, kv_heads, dim)
+        if ws_bytes:
+            ws = q.new_empty((ws_bytes,), dtype=torch.uint8)
+    elif ws is not None:
+        ws_bytes = ws.numel()
+    status = lib.dit_cross_attention(
+        qv, kv, vv, _ptr(kv_lengths), _ptr(key_mask), mask_stride, batch, queries, keys, heads,
+        kv_heads, dim, scale, ov, _ptr(ws), ws_bytes, _stream_at(at))
+    if status:
+        raise Nvfp4Error(status, "dit_cross_attention")
     return out
 
 
@@ -416,14 +467,16 @@ def lora_add(y, x, down, up, ids, scales=None, epilogue="none", y_amax=None, out
     _opt(y_amax, "y_amax", torch.float32)
     _opt(out, "out", torch.bfloat16, (rows, outer))
     ws = None if workspace is _NO_WORKSPACE else _tensor(workspace, "workspace", torch.uint8)
-    dev = _place(y, {"y": y, "x": x, "down": down, "up": up, "ids": ids, "scales": scales,
-                  "y_amax": y_amax, "out": out, "workspace": ws})
+    at = _place((y, x, down, up, ids, scales, y_amax, out, ws),
+                "y x down up ids scales y_amax out workspace")
     if out is None:
         out = y
+    lib = load()
     if ws is None:
-        ws = lora_workspace(rows, inner, rank, dev)
-    check(load().dit_lora_add(y.data_ptr(), x.data_ptr(), down.data_ptr(), up.data_ptr(),
+        ws = y.new_empty((lib.dit_lora_workspace_bytes(rows, inner, rank),), dtype=torch.uint8)
+    status = lib.dit_lora_add(y.data_ptr(), x.data_ptr(), down.data_ptr(), up.data_ptr(),
                               ids.data_ptr(), _ptr(scales), rows, inner, outer, rank, adapters, epi,
-                              out.data_ptr(), _ptr(y_amax), ws.data_ptr(), ws.numel(), _stream()),
-          "dit_lora_add")
+                              out.data_ptr(), _ptr(y_amax), ws.data_ptr(), ws.numel(), _stream_at(at))
+    if status:
+        raise Nvfp4Error(status, "dit_lora_add")
     return out

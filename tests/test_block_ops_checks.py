@@ -4,7 +4,6 @@ entry points report errors before touching a device (their pointers are fake and
 never dereferenced: every call fails a check first, the device check at the
 latest).  The rotary plan's frequencies are checked against their formulas."""
 
-import ctypes
 import math
 
 import pytest
@@ -12,7 +11,7 @@ import torch
 
 import nvfp4_block_scaled_05_amd as nv
 from nvfp4_block_scaled_05_amd import _binding
-from nvfp4_block_scaled_05_amd._binding import DitHeads
+from nvfp4_block_scaled_05_amd.block_ops import _VIEW
 
 OK, NULL, SHAPE, ALIGN, WORKSPACE, DEVICE, ARG = 0, -1, -2, -3, -4, -5, -6
 A = 1 << 20
@@ -219,7 +218,7 @@ def test_gated_norm_c(lib):
 
 
 def heads(data=A, b=8192, t=1024, h=64):
-    return ctypes.byref(DitHeads(data, b, t, h))
+    return _VIEW(data or 0, b, t, h)
 
 
 def test_rotary_c(lib):
