@@ -21,11 +21,14 @@ namespace nvfp4 {
 
 namespace {
 
-// Sum over the workgroup's `waves` waves.  `red` alternates between two halves
-// from one sum to the next, so one barrier a sum is enough.
-__device__ __forceinline__ float block_sum(float v, int waves, float (*red)[16], int& half) {
+// Sum over a row.  LANES > 0: the row is LANES neighbouring lanes.  LANES 0: it is
+// the whole workgroup of `waves` waves; `red` alternates between two halves from
+// one sum to the next, so one barrier a sum is enough.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, int waves, float (*red)[16], int& half) {
+  if constexpr (LANES == 64) return wave_sum(v);
+  if constexpr (LANES > 0) return group_sum<LANES>(v);
   v = wave_sum(v);
-  if (waves == 1) return v;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (lane == 0) red[half][wave] = v;
   __syncthreads();
@@ -42,13 +45,14 @@ template <> struct Raw<float> { f32x4 lo, hi; };
 __device__ __forceinline__ Raw<uint16_t> load8(const uint16_t* p) {
   return {*reinterpret_cast<const u32x4*>(p)};
 }
-// x, y, r and h pass through once: streaming loads and stores leave the caches to
-// the vectors over channels (85 us against 90 at 16896 x 3072).
-__device__ __forceinline__ Raw<uint16_t> stream8(const uint16_t* p) {
+// x, y, r and h pass through once: they are streamed past the caches, which stay
+// with the vectors over channels (85 us against 90 at 16896 x 3072).
+__device__ __forceinline__ Raw<uint16_t> take8(const uint16_t* p) {
   return {__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p))};
 }
-__device__ __forceinline__ Raw<float> stream8(const float* p) {
-  return {__builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p)), __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1)};
+__device__ __forceinline__ Raw<float> take8(const float* p) {
+  return {__builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p)),
+          __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1)};
 }
 __device__ __forceinline__ Raw<float> load8(const float* p) {
   return {reinterpret_cast<const f32x4*>(p)[0], reinterpret_cast<const f32x4*>(p)[1]};
@@ -72,12 +76,12 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
   return u32x4{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
                bf16x2_rne(f[6], f[7])};
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) {
+__device__ __forceinline__ void put8(uint16_t* p, const float (&f)[8]) {
   __builtin_nontemporal_store(pack8(f), reinterpret_cast<u32x4*>(p));
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  reinterpret_cast<f32x4*>(p)[0] = f32x4{f[0], f[1], f[2], f[3]};
-  reinterpret_cast<f32x4*>(p)[1] = f32x4{f[4], f[5], f[6], f[7]};
+__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
+  __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4*>(p));
+  __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f32x4*>(p) + 1);
 }
 
 // 8 entries of a modulation vector, stored as bf16 or fp32.
@@ -90,7 +94,7 @@ __device__ __forceinline__ void vector8(const void* base, bool fp32, int64_t at,
 
 // v := (v - mean) * rstd of the row, in place; `mine[i]`: chunk i of this
 // thread exists.
-template <int CH>
+template <int LANES, int CH>
 __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&mine)[CH], int kind,
                                           float inv_c, float eps, int waves, float (*red)[16],
                                           int& half) {
@@ -101,7 +105,7 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&mine)[
     for (int i = 0; i < CH; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += v[i][j];      // absent chunks hold zeros
-    mean = block_sum(s, waves, red, half) * inv_c;
+    mean = row_sum<LANES>(s, waves, red, half) * inv_c;
   }
   float q = 0.0f;
 #pragma unroll
@@ -111,16 +115,18 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&mine)[
       v[i][j] -= mean;
       q = mine[i] ? __builtin_fmaf(v[i][j], v[i][j], q) : q;
     }
-  const float rstd = __builtin_amdgcn_rsqf(block_sum(q, waves, red, half) * inv_c + eps);
+  const float rstd = __builtin_amdgcn_rsqf(row_sum<LANES>(q, waves, red, half) * inv_c + eps);
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
 }
 
-// CH: 8-channel chunks a thread holds; chunk i of thread t is t + i * blockDim.
-template <class XT, int CH>
-__global__ __launch_bounds__(1024) void gated_norm_kernel(GatedNorm a) {
+// Rows of up to 64 chunks of 8 channels are held by LANES neighbouring lanes, one
+// chunk each, and a workgroup of 256 threads takes 256 / LANES of them at a time;
+// longer ones (LANES 0) by the whole workgroup, CH chunks a thread.
+template <class XT, int CH, int LANES>
+__global__ __launch_bounds__(LANES > 0 ? 256 : 1024) void gated_norm_kernel(GatedNorm a) {
   __shared__ float red[2][16];
   int half = 0;
   const int waves = blockDim.x >> 6, chunks = a.channels >> 3;
@@ -128,26 +134,28 @@ __global__ __launch_bounds__(1024) void gated_norm_kernel(GatedNorm a) {
   int at[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
+    const int c = LANES > 0 ? threadIdx.x % (LANES > 0 ? LANES : 1) : threadIdx.x + i * blockDim.x;
     mine[i] = c < chunks;
     at[i] = mine[i] ? 8 * c : 0;
   }
   const XT* x = static_cast<const XT*>(a.x);
   XT* r_out = static_cast<XT*>(a.residual);
   u16x2 top = {0, 0};
-  int64_t row = blockIdx.x;
+  constexpr int kRows = LANES > 0 ? 256 / (LANES > 0 ? LANES : 1) : 1;    // at a time
+  int64_t row = (int64_t)blockIdx.x * kRows + (LANES > 0 ? threadIdx.x / (LANES > 0 ? LANES : 1) : 0);
+  const int64_t step = (int64_t)gridDim.x * kRows;
   Raw<XT> xr[CH];
   Raw<uint16_t> yr[CH];
   auto fetch = [&](int64_t of) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (!mine[i]) continue;
-      xr[i] = stream8(x + of * a.channels + at[i]);
-      if (a.y) yr[i] = stream8(a.y + of * a.channels + at[i]);
+      xr[i] = take8(x + of * a.channels + at[i]);
+      if (a.y) yr[i] = take8(a.y + of * a.channels + at[i]);
     }
   };
-  fetch(row);
-  for (;;) {
+  if (row < a.rows) fetch(row);
+  while (row < a.rows) {
     const int64_t batch = row / a.tokens;
     float v[CH][8], z[CH][8];
 #pragma unroll
@@ -158,11 +166,11 @@ __global__ __launch_bounds__(1024) void gated_norm_kernel(GatedNorm a) {
       widen(xr[i], v[i]);
       if (a.y) widen(yr[i], z[i]);
     }
-    const int64_t next = row + gridDim.x;
+    const int64_t next = row + step;
     if (next < a.rows) fetch(next);          // the next row's loads run under this row's sums
     if (a.y) {
       if (a.post_norm != DIT_NORM_NONE)
-        normalise<CH>(z, mine, a.post_norm, a.inv_c, a.eps, waves, red, half);
+        normalise<LANES, CH>(z, mine, a.post_norm, a.inv_c, a.eps, waves, red, half);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         if (!mine[i]) continue;
@@ -184,11 +192,11 @@ __global__ __launch_bounds__(1024) void gated_norm_kernel(GatedNorm a) {
     if (r_out) {
 #pragma unroll
       for (int i = 0; i < CH; ++i)
-        if (mine[i]) store8(r_out + row * a.channels + at[i], v[i]);
+        if (mine[i]) put8(r_out + row * a.channels + at[i], v[i]);
     }
     if (a.h) {
       if (a.norm != DIT_NORM_NONE)
-        normalise<CH>(v, mine, a.norm, a.inv_c, a.eps, waves, red, half);
+        normalise<LANES, CH>(v, mine, a.norm, a.inv_c, a.eps, waves, red, half);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         if (!mine[i]) continue;
@@ -218,7 +226,6 @@ __global__ __launch_bounds__(1024) void gated_norm_kernel(GatedNorm a) {
         top = max_u16x2(top, max8(p));
       }
     }
-    if (next >= a.rows) break;
     row = next;
   }
   if (a.amax) {
@@ -228,7 +235,7 @@ __global__ __launch_bounds__(1024) void gated_norm_kernel(GatedNorm a) {
     __syncthreads();
     if (threadIdx.x == 0) {
       uint32_t t = 0;
-      for (int w = 0; w < waves; ++w) t = max(t, wave_top[w]);
+      for (int w = 0; w < (int)(blockDim.x >> 6); ++w) t = max(t, wave_top[w]);
       raise_amax(a.amax, t);
     }
   }
@@ -236,9 +243,12 @@ __global__ __launch_bounds__(1024) void gated_norm_kernel(GatedNorm a) {
 
 __global__ void zero_amax_kernel(uint32_t* p) { *p = 0u; }
 
-template <class XT, int CH>
-hipError_t launch(const GatedNorm& a, int threads, int64_t grid, hipStream_t stream) {
-  gated_norm_kernel<XT, CH><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
+template <int CH, int LANES>
+hipError_t launch(const GatedNorm& a, bool x_fp32, int threads, int64_t grid, hipStream_t stream) {
+  if (x_fp32)
+    gated_norm_kernel<float, CH, LANES><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
+  else
+    gated_norm_kernel<uint16_t, CH, LANES><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -252,15 +262,24 @@ hipError_t launch_gated_norm(const GatedNorm& a, bool x_fp32, hipStream_t stream
   }
   if (a.rows == 0) return hipSuccess;
   const int chunks = a.channels / 8;
-  const int waves = chunks <= 1024 ? (chunks + 63) / 64 : 16;
+  // one chunk a lane up to 8192 channels: more waves with less to hold each load
+  // more at once (at 16896 x 3072 two chunks a lane take 103 us, one 85).  24 waves
+  // a compute unit (18: 94 us; 30, more than the registers hold: 116), rows spread
+  // evenly over the rounds.
+  const int lanes = chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : chunks <= 64 ? 64 : 0;
+  const int waves = lanes ? 4 : chunks <= 1024 ? (chunks + 63) / 64 : 16;
+  const int64_t turns = lanes ? (a.rows + 256 / lanes - 1) / (256 / lanes) : a.rows;
   const int64_t cap = (int64_t)compute_units() * (24 / waves);
-  const int64_t rounds = (a.rows + cap - 1) / cap;     // rows spread evenly over the rounds
-  const int64_t grid = (a.rows + rounds - 1) / rounds;
-  if (chunks <= 1024)
-    return x_fp32 ? launch<float, 1>(a, 64 * waves, grid, stream)
-                  : launch<uint16_t, 1>(a, 64 * waves, grid, stream);
-  return x_fp32 ? launch<float, 2>(a, 1024, grid, stream)
-                : launch<uint16_t, 2>(a, 1024, grid, stream);
+  const int64_t rounds = (turns + cap - 1) / cap;
+  const int64_t grid = (turns + rounds - 1) / rounds;
+  switch (lanes) {
+    case 8: return launch<1, 8>(a, x_fp32, 256, grid, stream);
+    case 16: return launch<1, 16>(a, x_fp32, 256, grid, stream);
+    case 32: return launch<1, 32>(a, x_fp32, 256, grid, stream);
+    case 64: return launch<1, 64>(a, x_fp32, 256, grid, stream);
+  }
+  return chunks <= 1024 ? launch<1, 0>(a, x_fp32, 64 * waves, grid, stream)
+                        : launch<2, 0>(a, x_fp32, 1024, grid, stream);
 }
 
 }  // namespace nvfp4

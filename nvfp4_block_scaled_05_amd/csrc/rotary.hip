@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kRotThreads = 256;
 constexpr int kRotEntries = 512;   // (cos, sin) pairs a workgroup keeps: 4 KB of LDS
-constexpr int kRotTokens = 4;      // and tokens (at 16896 tokens of 48 heads: 2: 100 us, 4: 95, 8: 103)
+constexpr int kRotTokens = 32;     // and tokens, at most
 
 __device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -92,7 +92,8 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
       const bool is_q = hh < a.q.heads;
       const RotaryHeads& v = is_q ? a.q : a.k;
       const int64_t at = place[tt][is_q ? 0 : 1] + (is_q ? hh : hh - a.q.heads) * v.in_head + 8 * chunk;
-      return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(v.in + at));
+      const u32x4* from = reinterpret_cast<const u32x4*>(v.in + at);
+      return a.streaming ? __builtin_nontemporal_load(from) : *from;
     };
     if (slot < items && mine) raw = fetch(t, head);
     for (int base = 0; base < items; base += kRotThreads / LANES) {
@@ -148,7 +149,11 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
       if (live) {
         const RotaryHeads& v = is_q ? a.q : a.k;
         const int64_t at = place[t_now][is_q ? 2 : 3] + (is_q ? head_now : head_now - a.q.heads) * v.out_head;
-        __builtin_nontemporal_store(out, reinterpret_cast<u32x4*>(v.out + at + 8 * chunk));
+        u32x4* to = reinterpret_cast<u32x4*>(v.out + at + 8 * chunk);
+        if (a.streaming)
+          __builtin_nontemporal_store(out, to);
+        else
+          *to = out;
       }
     }
     __syncthreads();                             // before the next tokens' table
@@ -174,20 +179,30 @@ hipError_t launch(const Rotary& a, int64_t grid, hipStream_t stream) {
 
 hipError_t launch_rotary(Rotary a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  // tokens a workgroup takes: as many as its table holds, fewer while that
-  // would leave compute units without a workgroup
-  const int64_t fill = (a.rows + 4 * compute_units() - 1) / (4 * compute_units());
-  int per = kRotEntries / (a.rotary_dim / 2);
+  // tokens a workgroup takes: four (at 16896 tokens of 48 heads of 128, 2 take 100
+  // us, 4 95, 8 103), more where a token's heads do not fill the workgroup four
+  // times over, as many as its table holds, and fewer while that would leave
+  // compute units without a workgroup
+  const int chunks = a.dim / 8, lanes = chunks <= 4 ? 4 : chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
+  const int heads = a.q.heads + a.k.heads;
+  int per = 4 * (kRotThreads / lanes) / heads;
+  if (per < 4) per = 4;
   if (per > kRotTokens) per = kRotTokens;
+  if (per > kRotEntries / (a.rotary_dim / 2)) per = kRotEntries / (a.rotary_dim / 2);
+  const int64_t fill = (a.rows + 4 * compute_units() - 1) / (4 * compute_units());
   if (per > fill) per = (int)fill;
   a.tokens_per_group = per;
+  // what the last-level cache cannot hold is streamed past the others (95 us
+  // against 107 at 16896 tokens; up to half of that no difference)
+  a.streaming = a.rows * heads * a.dim * 4 > ((int64_t)256 << 20);
   const int64_t groups = (a.rows + per - 1) / per;
   const int64_t grid = groups < (1 << 20) ? groups : (1 << 20);    // the kernel strides over the rest
-  const int chunks = a.dim / 8;
-  if (chunks <= 4) return launch<4>(a, grid, stream);
-  if (chunks <= 8) return launch<8>(a, grid, stream);
-  if (chunks <= 16) return launch<16>(a, grid, stream);
-  return launch<32>(a, grid, stream);
+  switch (lanes) {
+    case 4: return launch<4>(a, grid, stream);
+    case 8: return launch<8>(a, grid, stream);
+    case 16: return launch<16>(a, grid, stream);
+    default: return launch<32>(a, grid, stream);
+  }
 }
 
 }  // namespace nvfp4
