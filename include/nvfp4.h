@@ -424,7 +424,7 @@ typedef struct {
  *   weight, bias, post_weight  optional [channels] fp32, 16-byte aligned.
  *   batch, tokens >= 0; 0 < channels <= 16384, a multiple of 8.
  *   norm, post_norm a dit_norm; DIT_NORM_NONE leaves the value as it is.
- *   eps             > 0.
+ *   eps             > 0, at least 2^-126.
  *   residual        optional out, r in x's type.  It may be x itself.
  *   h_bf16          optional out, bf16 (residual or h_bf16 must be given).  It
  *                   may be y_bf16 itself.
@@ -432,7 +432,8 @@ typedef struct {
  *                   outputs, ready for nvfp4_quantize's amax_in (zeroed first,
  *                   on `stream`; 0 if there are no rows; not finite if an
  *                   output is NaN).
- * h is computed from r before r is rounded.  Deterministic.
+ * No other overlap of outputs with inputs or each other.  h is computed from r
+ * before r is rounded.  Deterministic.
  */
 int dit_gated_norm(const void* x, int x_fp32, const void* y_bf16, const void* gate,
                    int64_t gate_stride, const void* scale, int64_t scale_stride,
@@ -461,7 +462,7 @@ int dit_gated_norm(const void* x, int x_fp32, const void* y_bf16, const void* ga
  *   q_weight, k_weight  optional [dim] fp32: that tensor's norm.
  *   dim             a multiple of 8, at most 256; rotary_dim a multiple of 16,
  *                   0 < rotary_dim <= dim.  1 <= axes <= 16.  heads > 0.
- *   layout          a dit_rotary_layout.  eps > 0.
+ *   layout          a dit_rotary_layout.  magnitude, eps > 0, at least 2^-126.
  */
 int dit_rotary(const dit_heads* q, const dit_heads* q_out, int64_t heads, const dit_heads* k,
                const dit_heads* k_out, int64_t kv_heads, const int32_t* positions, int64_t axes,
@@ -495,8 +496,9 @@ size_t dit_cross_attention_workspace_bytes(int64_t batch, int64_t queries, int64
  *                   the length).  Keys and values out of sight are not read or
  *                   do not count, whatever they hold.
  *   heads a positive multiple of kv_heads; dim a multiple of 8, at most 128;
- *   batch, queries, keys >= 0; scale > 0.  k's and v's token strides are
- *   below 2^23 elements; batch * heads * queries below 2^31.
+ *   batch, queries, keys >= 0; scale > 0, at least 2^-126.  k's and v's token
+ *   strides are below 2^23 elements; batch * heads * queries below 2^31, and in
+ *   rows of 128 per kv head at most 2^23.
  *   workspace       optional, 256-byte aligned, contents on entry irrelevant,
  *                   owned by the call until it completes: with at least
  *                   dit_cross_attention_workspace_bytes bytes the keys of a
@@ -530,8 +532,8 @@ size_t dit_lora_workspace_bytes(int64_t rows, int64_t inner, int64_t rank);
  *   ids             [rows] int32: the adapter of each row, in any order (rows
  *                   of one request lying together are fastest).
  *   scales          optional [adapters] fp32.
- *   rows, outer >= 0; inner and outer multiples of 8; rank a multiple of 8, 8
- *   to 128; adapters > 0.  bf16 pointers 16-byte aligned.
+ *   0 <= rows < 2^26; inner and outer multiples of 8 below 2^28, inner > 0;
+ *   rank a multiple of 8, 8 to 128; adapters > 0.  bf16 pointers 16-byte aligned.
  *   epilogue        an nvfp4_epilogue.
  *   out_bf16        out [rows, outer]; may be y_bf16 itself (rows without an
  *                   adapter then stay as they are under NVFP4_EPI_NONE).

@@ -304,7 +304,8 @@ def rotary(q, positions, plan, k=None, layout="interleaved", q_weight=None, k_we
     positions: int32 [tokens] or [batch, tokens], with a last dimension of
     plan.axes when the plan has several axes.  layout: "interleaved" (pairs of
     neighbours) or "half" (j with j + rotary_dim / 2).  Elements from
-    plan.rotary_dim on are not rotated.  ``out`` / ``k_out`` may be q / k.
+    plan.rotary_dim on are not rotated.  ``out`` / ``k_out`` may be q / k; no
+    other overlap.
     Returns out, or (out, k_out) when k is given.
     """
     torch = _torch()
@@ -335,6 +336,12 @@ def rotary(q, positions, plan, k=None, layout="interleaved", q_weight=None, k_we
     _opt(k_weight, "k_weight", torch.float32, (dim,))
     qo = _out_heads(out, q, "out")
     ko = None if k is None else _out_heads(k_out, k, "k_out")
+    if k is not None and (out is not None or k_out is not None) and q.numel() and k.numel():
+        # in place is each tensor in its own place; q and k in one would race
+        here = None if out is None else out.data_ptr()
+        there = None if k_out is None else k_out.data_ptr()
+        if here == k.data_ptr() or there == q.data_ptr() or (here is not None and here == there):
+            raise ValueError("out may be q itself and k_out k itself, but not the other's")
     at = _place((q, k, positions, plan.turns, plan.axis, q_weight, k_weight, out, k_out),
                 "q k positions turns axis q_weight k_weight out k_out")
     if out is None:

@@ -87,13 +87,16 @@ bool bad_attention(int64_t batch, int64_t queries, int64_t keys, int64_t heads, 
 
 // Sizes dit_lora_add does not take (element offsets within a row are 32-bit).
 bool bad_lora(int64_t rows, int64_t inner, int64_t outer, int64_t rank, int64_t adapters) {
-  if (bad_dim(rows) || rows >= (1 << 27)) return true;
+  // a workgroup of up to 768 threads for 16 rows, counted in 32 bits
+  if (bad_dim(rows) || rows >= (1 << 26)) return true;
   if (inner <= 0 || inner % 8 != 0 || inner >= (1 << 28)) return true;
   if (outer < 0 || outer % 8 != 0 || outer >= (1 << 28)) return true;
   return rank <= 0 || rank % 8 != 0 || rank > 128 || adapters <= 0 || adapters >= kMaxDim;
 }
 
-bool finite_positive(float v) { return v > 0.0f && v <= FLT_MAX; }
+// Positive, finite and not subnormal (the kernels' reciprocal square root takes a
+// subnormal for zero).
+bool finite_positive(float v) { return v >= FLT_MIN && v <= FLT_MAX; }
 
 nvfp4::RotaryHeads rotary_heads(const dit_heads& in, const dit_heads& out, const float* weight,
                                 int64_t heads) {

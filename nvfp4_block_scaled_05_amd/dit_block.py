@@ -178,8 +178,8 @@ class DitCrossBlock:
 
     def encode(self, states, lengths=None):
         """Keys and values of encoder ``states`` [batch, states, width] (bf16);
-        ``lengths``: int32 [batch], the states of each prompt (the rest is
-        padding)."""
+        ``lengths``: int32 [batch], the states of each prompt.  The rest is
+        padding; it is quantized with the states, so it has to be finite."""
         kv = self._linear(self.to_kv, states.view(-1, states.shape[-1]))
         kv = kv.view(self.batch, self.states, 2, self.kv_heads, -1)
         k, self.v, self.lengths = kv[:, :, 0], kv[:, :, 1], lengths

@@ -293,3 +293,27 @@ def test_norm_none_rejects():
     raises("needs a norm", nv.gated_norm, x, x, norm=None, scale=bf16(2, 64))
     raises("needs a norm", nv.gated_norm, x, x, norm=None, amax=f32(1))
     raises("needs y", nv.gated_norm, x, norm=None)
+
+
+def test_rotary_refuses_one_place_for_two():
+    plan = nv.rotary_plan(32, device="cpu")
+    q, k, pos = bf16(2, 5, 3, 64), bf16(2, 5, 3, 64), i32(2, 5)
+    raises("not the other's", nv.rotary, q, pos, plan, k=q, out=q, k_out=q)
+    raises("not the other's", nv.rotary, q, pos, plan, k=k, out=k)
+    raises("not the other's", nv.rotary, q, pos, plan, k=k, k_out=q)
+    raises("not the other's", nv.rotary, q, pos, plan, k=k, out=(o := bf16(2, 5, 3, 64)), k_out=o)
+    raises("GPU tensor", nv.rotary, q, pos, plan, k=k, out=q, k_out=k)      # each in its own place
+
+
+def test_subnormal_eps_is_refused(lib):
+    sub = 1e-40
+    assert lib.dit_gated_norm(A, 0, A, None, 0, None, 0, None, 0, 0, None, None, None, 1, 1, 64, 1, 0, 1.0, sub,
+                              A, A, None, None) == ARG
+    assert lib.dit_rotary(heads(), heads(), 4, None, None, 0, A, 1, A, None, 1.0, A, None, sub, 1, 1, 64, 32, 0,
+                          None) == ARG
+
+
+def test_sizes_past_the_grid_are_refused(lib):
+    assert lib.dit_lora_add(A, A, A, A, A, None, 1 << 26, 64, 32, 16, 1, 0, A, None, A, 1 << 40, None) == SHAPE
+    assert lib.dit_cross_attention(heads(), heads(), heads(), None, None, 0, 1 << 12, 33, 9, 1 << 13, 1 << 13, 64,
+                                   0.1, heads(), None, 0, None) == SHAPE
