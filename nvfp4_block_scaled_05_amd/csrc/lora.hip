@@ -8,10 +8,14 @@
 // workspace.  Bound: HBM -- x is read once by the first, y read and out written
 // once by the second; the adapters come from the caches.
 //
-// Rows of one request lie together, but any order is right: a tile of 16 rows
-// takes its distinct adapters one after another through the whole tile, and
-// each row keeps the result of its own (a select, so what another adapter holds
-// cannot reach it).
+// Rows of one request lie together, but any order is right: each distinct adapter
+// of a tile of 16 rows goes through the whole tile, and each row keeps the result
+// of its own (a select, so what another adapter holds cannot reach it).
+//
+// Measured at 4608 rows, 3072 to 9216, rank 32, five requests: 15 us and 48 us, the
+// second at 3.6 TB/s of y and out; at 48 rows of 12 requests, 3072 to 12288, rank
+// 16, with GELU and amax: 4.2 us and 8.7 us, bound by the latency of their chains
+// of loads (ids, adapter, product).
 #include "device_common.hpp"
 #include "kernels.hpp"
 
@@ -45,14 +49,15 @@ constexpr int kDownWaves = 12;
 
 // t[slice][row][16 * RT]: this slice's part of s_a * down_a x.  RT: 16-wide
 // tiles over the rank, MT: row tiles of the workgroup.  It has as many waves (up
-// to 12) as the slice has groups of steps, so that one round of loads takes it
-// through the slice; their sums are added in wave order.
+// to 12) as the slice has groups of steps, so that few rounds of loads take it
+// through the slice; their sums are added in wave order.  With gridDim.z > 1
+// workgroup z has the z-th distinct adapter of its tile, and that one's rows, alone.
 template <int RT, int MT>
 __global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(Lora a) {
   constexpr int U = group_steps(RT, MT);
   __shared__ float red[kDownWaves][MT * RT * 4][64];
   const int waves = blockDim.x >> 6;
-  if (a.amax && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.amax = 0u;
+  if (a.amax && blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x == 0) *a.amax = 0u;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int r = lane & 15, q = lane >> 4;
   const int64_t row0 = (int64_t)blockIdx.x * (kRowTile * MT);
@@ -65,11 +70,21 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(Lora a) {
   // row 4 (lane / 16) + e % 4; rows without an adapter stay zero
 #pragma unroll
   for (int e = 0; e < MT * RT * 4; ++e) red[wave][e][lane] = 0.0f;
-  uint64_t todo = __ballot(lane < kRowTile * MT && id >= 0);
+  const bool one = gridDim.z > 1;
+  uint32_t skip = blockIdx.z;
+  uint64_t todo = __ballot(lane < kRowTile * MT && id >= 0), mine = ~0ull;
   while (todo) {
     const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
     const uint64_t same = __ballot(lane < kRowTile * MT && id == cur);
     todo &= ~same;
+    if (one) {
+      if (skip > 0) {
+        --skip;
+        continue;
+      }
+      todo = 0;
+      mine = same;
+    }
     f32x4 acc[MT][RT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -118,12 +133,14 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(Lora a) {
         for (int i = 0; i < 4; ++i)
           if ((same >> (16 * m + 4 * q + i)) & 1) red[wave][(m * RT + c) * 4 + i][lane] = acc[m][c][i] * s;
   }
+  if (one && mine == ~0ull) return;              // the tile has fewer adapters
   __syncthreads();
   for (int e = wave; e < MT * RT * 4; e += waves) {
     float v = red[0][e][lane];
     for (int w = 1; w < waves; ++w) v += red[w][e][lane];
-    const int64_t to = row0 + 16 * (e / (4 * RT)) + 4 * q + e % 4;
-    if (to < a.rows) a.t[((int64_t)blockIdx.y * a.rows + to) * (16 * RT) + 16 * (e / 4 % RT) + r] = v;
+    const int in = 16 * (e / (4 * RT)) + 4 * q + e % 4;
+    const int64_t to = row0 + in;
+    if (to < a.rows && ((mine >> in) & 1)) a.t[((int64_t)blockIdx.y * a.rows + to) * (16 * RT) + 16 * (e / 4 % RT) + r] = v;
   }
 }
 
@@ -136,6 +153,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(Lora a) {
 template <int RT, int MT>
 __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
   constexpr int KS = (RT + 1) / 2;             // 32-deep steps over the rank
+  // column blocks that a tile of several adapters loads weights for at once: all of
+  // them where rows are few (8.7 us against 12.2 at 48 rows), one where the registers
+  // cost waves (48 against 51 us at 4608 rows)
+  constexpr int NB = MT > 1 ? 1 : KS <= 2 ? kColBlocks : kColBlocks / KS;
   const int lane = threadIdx.x & 63;
   const int r = lane & 15, q = lane >> 4;
   const int col_items = (a.outer + kColBlock * kColBlocks - 1) / (kColBlock * kColBlocks);
@@ -240,25 +261,37 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
           }
           finish(m, b, d);
         }
-    } else {
+    } else {                                   // one adapter after another through the tile
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int b = 0; b < kColBlocks; ++b) {
-          f32x4 d[2] = {f32x4{}, f32x4{}};
+        for (int b0 = 0; b0 < kColBlocks; b0 += NB) {
+          f32x4 d[NB][2];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) d[b][0] = d[b][1] = f32x4{};
           for (uint64_t left = __ballot(lane < 16 && id[m] >= 0); left;) {
             const int cur = __builtin_amdgcn_readlane(id[m], __builtin_ctzll(left));
             left &= ~__ballot(lane < 16 && id[m] == cur);
+            u32x4 uf[KS][NB][2];
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              f32x4 acc = f32x4{};
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-              for (int s = 0; s < KS; ++s)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(weights(cur, b, p, s)), tf[m][s], acc, 0, 0, 0);
-              if (id[m] == cur) d[p] = acc;
-            }
+              for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int s = 0; s < KS; ++s) uf[s][b][p] = weights(cur, b0 + b, p, s);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                f32x4 acc = f32x4{};
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                  acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(uf[s][b][p]), tf[m][s], acc, 0, 0, 0);
+                if (id[m] == cur) d[b][p] = acc;
+              }
           }
-          finish(m, b, d);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) finish(m, b0 + b, d[b]);
         }
     }
   }
@@ -297,7 +330,14 @@ hipError_t launch(const Lora& a, hipStream_t stream) {
   const int mt = RT <= 2 && 4 * two < 3 * one ? 2 : 1;
   const int groups = (a.slice + 32 * group_steps(RT, mt) - 1) / (32 * group_steps(RT, mt));
   const dim3 block(64 * (groups < kDownWaves ? groups : kDownWaves));
-  const dim3 down((unsigned)((tiles + mt - 1) / mt), a.slices);
+  // Few tiles: a workgroup for each adapter that a tile can have, those past its
+  // number leaving at once, so that no tile takes two one after another (15 us
+  // against 25 where 4 of 144 tiles have two adapters, 4.2 against 7.5 where 3
+  // tiles of 48 rows have four each).  Many: the tail of one such tile is small
+  // beside the rounds.
+  int64_t each = a.adapters < kRowTile * mt ? a.adapters : kRowTile * mt;
+  if ((tiles + mt - 1) / mt * a.slices * each > 4 * units) each = 1;
+  const dim3 down((unsigned)((tiles + mt - 1) / mt), a.slices, (unsigned)each);
   if (mt == 2)
     lora_down_kernel<RT, RT <= 2 ? 2 : 1><<<down, block, 0, stream>>>(a);
   else

@@ -81,6 +81,15 @@ def test_one_adapter_a_row():
     check(nv.lora_add(**d, out=torch.empty_like(d["y"])), d)
 
 
+@pytest.mark.parametrize("rows,inner,outer,rank,adapters", [
+    (4128, 136, 72, 16, 5),       # two row tiles a workgroup, one adapter each
+    (4128, 136, 72, 32, 40),      # two row tiles, their adapters one after another
+    (9000, 72, 40, 8, 3), (40, 1096, 264, 24, 16), (30, 1096, 264, 128, 17)])
+def test_adapters_mixed_in_every_tile(rows, inner, outer, rank, adapters):
+    d = make(7 * rows, rows, inner, outer, rank, adapters)
+    check(nv.lora_add(**d, out=torch.empty_like(d["y"])), d)
+
+
 @pytest.mark.parametrize("bad", [-1, -2 ** 31, 4, 2 ** 31 - 1])
 def test_rows_without_an_adapter(bad):
     d = make(4, 50, 128, 72, 8, 4, np.full(50, bad))
