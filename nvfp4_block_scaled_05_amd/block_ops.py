@@ -375,7 +375,8 @@ def cross_attention(q, k, v, kv_lengths=None, key_mask=None, scale=None, out=Non
     dim: a multiple of 8 up to 128.  kv_lengths: int32 [batch], the keys each
     entry sees; key_mask: bool or uint8 [batch, keys], the keys to see (both:
     their intersection).  What lies out of sight does not count, whatever it
-    holds; a query that sees no key gets zeros.  scale: dim ** -0.5 by default.
+    holds; a query that sees no key, or whose scores are all -infinity, gets
+    zeros.  scale: dim ** -0.5 by default.
 
     ``workspace``: a uint8 device tensor from ``cross_attention_workspace``
     (reused across calls on one stream), None not to split the keys, or left

@@ -1,6 +1,17 @@
 // dit_cross_attention: softmax(scale q k^T) v of query heads over the keys and
 // values of an encoder (or of any other length), with key heads shared by
 // groups of query heads, key lengths and a key mask.
+//
+// One pass over the keys: a wave computes the transposed scores S^T = K Q^T of 32
+// query rows and a tile of keys, so a lane holds scores of one query, keeps that
+// query's running maximum m and sum l of 2^(c s - m) (c = scale log2 e) and
+// accumulates O^T += V^T P^T, P = 2^(c s - m) in bf16: in this form P is already
+// where the second product takes it.  All else is binary32.  Query rows are
+// (token, head of the group) pairs, so the heads that share keys share their tiles.
+//
+// Two kernels: attention_kernel, bound by the matrix cores and the exponentials
+// beside them, and attention_few_kernel for up to 32 query rows a kv head, bound by
+// the stream of keys and values.  A third one joins key splits.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -13,6 +24,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+constexpr float kLowest = 3.40282347e38f;       // the largest finite binary32 value
 constexpr uint32_t kNoData = 0x80000000u;       // a lane offset past every tile: loads zeros
 
 // Where a 16-byte piece of a K / V row lies in its LDS row: pieces are permuted
@@ -80,7 +92,7 @@ struct Attend {
     half = lane >> 5;
     col = lane & 31;
     c = scale * 1.44269504f;
-    top = -__builtin_inff();
+    top = -kLowest;                             // finite: a score of -inf then weighs 0
     sum = 0.0f;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) o[b] = f32x16{};
@@ -234,15 +246,15 @@ struct Attend {
     f32x16 s[KB];
     u32x4 kf[KB][kSteps];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      s[kb] = f32x16{};
+    for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st) kf[kb][st] = k_frag(lds_k, kb, st, col, half);
-    }
+    for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+      for (int kb = 0; kb < KB; ++kb) kf[kb][st] = k_frag(lds_k, kb, st, col, half);
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st)
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
         s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf[kb][st]), q[st], s[kb], 0, 0, 0);
     u32x4 vf[kBlocks];
 #pragma unroll
@@ -368,35 +380,45 @@ __device__ __forceinline__ uint16_t* output_row(const Attention& a, const Place&
   return a.out + row_offset(a, p, row, a.o_batch, a.o_token, a.o_head);
 }
 
-// A lane's walk over rows: first, first + by, ... as (token, head in the group),
-// stepped without a division; rows past the last stay at the last token.
+// A lane's walk over rows: first, first + by, ... as an offset from the batch
+// entry's start, stepped without a product or a division.
 struct RowStep {
-  int token, head, by_token, by_head, group, last;
-  __device__ __forceinline__ RowStep(const Attention& a, const Place& p, int64_t first, int by) {
-    const uint32_t r = (uint32_t)first, g = (uint32_t)a.group;
+  int64_t at, step, wrap;
+  int row, by, head, by_head, group;
+  __device__ __forceinline__ RowStep(const Attention& a, const Place& p, int64_t first, int by_, int64_t token_stride,
+                                     int64_t head_stride) {
+    const uint32_t r = (uint32_t)first, g = (uint32_t)a.group, token = g == 1 ? r : r / g;
+    row = (int)r;
+    by = by_;
     group = a.group;
-    last = a.queries - 1;
-    token = (int)(g == 1 ? r : r / g);
-    head = (int)(r - (uint32_t)token * g);
-    by_token = by / group;
+    head = (int)(r - token * g);
+    const int by_token = by / group;
     by_head = by - by_token * group;
+    at = token * token_stride + (p.kvh * group + head) * head_stride;
+    step = by_token * token_stride + by_head * head_stride;
+    wrap = token_stride - group * head_stride;
   }
   __device__ __forceinline__ void next() {
-    token += by_token;
+    row += by;
     head += by_head;
-    if (head >= group) {
-      head -= group;
-      ++token;
-    }
-  }
-  __device__ __forceinline__ int64_t offset(const Attention& a, const Place& p, int64_t token_stride,
-                                            int64_t head_stride) const {
-    return (int64_t)min(token, last) * token_stride + (int64_t)(p.kvh * group + head) * head_stride;
+    at += step;
+    const bool over = head >= group;
+    head -= over ? group : 0;
+    at += over ? wrap : 0;
   }
 };
 
 // Many query rows: the four waves of a workgroup have 32 rows each and share the
-// tiles of 64 keys.
+// tiles of 64 keys, which the next turn's loads replace while this turn's are
+// used.  At 4608 queries and keys of 24 heads: 230 us, 1.01 PFLOP/s (the matrix
+// cores alone reach 1.68 on such data); a tile of 32 rows by 64 keys costs a SIMD
+// 1024 cycles of matrix products and about 950 of exponentials, sums and maxima, and
+// two waves a SIMD hide about half of the latter.  The rest is power: on zeros,
+// the same instructions take 189 us.  At 16384 queries of a pair of 512 and 77
+// keys: 178 us, 0.66 PFLOP/s and 2.3 TB/s.  Not faster: the exponentials of one
+// block of 32 keys under the scores of the next in one wave (235), 64 rows a wave
+// (registers spill), the loads spread between the products (they spill), query
+// rows fetched a unit ahead by workgroups that stay (they spill: 247 for 178).
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
   using A = Attend<DP, 2>;
@@ -418,12 +440,13 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
   const int piece = w.lane % kRowPieces;
   u32x4 qrow[32 / kRowsPerLoad];
   {
-    const int at = 8 * piece < a.dim ? 8 * piece : 0;
-    RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad);
+    // rows past the last read the first token's
+    const uint16_t* q = a.q + p.batch * a.q_batch + (8 * piece < a.dim ? 8 * piece : 0);
+    const int64_t none = (int64_t)p.kvh * a.group * a.q_head;
+    RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad, a.q_token, a.q_head);
 #pragma unroll
     for (int i = 0; i < 32 / kRowsPerLoad; ++i, step.next())
-      qrow[i] = *reinterpret_cast<const u32x4*>(a.q + p.batch * a.q_batch +
-                                                step.offset(a, p, a.q_token, a.q_head) + at);
+      qrow[i] = *reinterpret_cast<const u32x4*>(q + (step.row < rows ? step.at : none));
   }
   p.keys = seen_keys(a, p);
   TileLoader<DP, 2, 4> load;
@@ -503,15 +526,14 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
                                 8 * w.half) =
           u32x2{bf16x2_rne(w.o[b][4 * g] * inv, w.o[b][4 * g + 1] * inv),
                 bf16x2_rne(w.o[b][4 * g + 2] * inv, w.o[b][4 * g + 3] * inv)};
-  RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad);
+  uint16_t* out = a.out + p.batch * a.o_batch + 8 * piece;
+  RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad, a.o_token, a.o_head);
 #pragma unroll
   for (int i = 0; i < 32 / kRowsPerLoad; ++i, step.next()) {
     const int r = i * kRowsPerLoad + w.lane / kRowPieces;
     const u32x4 f =
         *reinterpret_cast<const u32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4));
-    if (row0 + r < rows && 8 * piece < a.dim)
-      *reinterpret_cast<u32x4*>(a.out + p.batch * a.o_batch + step.offset(a, p, a.o_token, a.o_head) +
-                                8 * piece) = f;
+    if (step.row < rows && 8 * piece < a.dim) *reinterpret_cast<u32x4*>(out + step.at) = f;
   }
 }
 
@@ -520,7 +542,10 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
 // waits for another; they are joined at the end.  What is left is the stream of
 // keys and values: K fragments go straight to registers (each element is used
 // by one lane once), V through LDS of the wave's own for the transposed reads,
-// both a tile ahead of their use.
+// both a tile ahead of their use.  One token of 8 entries of 1 to 8192 keys, 24
+// heads over 8: 41 us and 5 for the join, 129 MB at 3.2 TB/s (with the tiles shared
+// by the waves as above 48 in all); what lacks is the start of each workgroup and
+// the last ones, which find half a card to themselves.
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
   using A = Attend<DP, 1>;

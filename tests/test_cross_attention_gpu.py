@@ -151,6 +151,20 @@ def test_large_scores_and_scale(queries):
     check(nv.cross_attention(-q2, k2, v), -q2, k2, v)
 
 
+@pytest.mark.parametrize("queries", [3, 200])
+@pytest.mark.parametrize("hidden", [slice(0, 330), slice(128, 700), slice(0, 900)])
+def test_scores_of_minus_infinity_weigh_nothing(queries, hidden):
+    q, k, v = make(14, 1, queries, 900, 2, 1, 128)
+    q = q.abs() + 0.1
+    k[:, hidden] = float("-inf")
+    mask = torch.ones(1, 900, dtype=torch.bool, device="cuda")
+    mask[:, hidden] = False
+    for ws in ({}, {"workspace": None}):
+        got = nv.cross_attention(q, k, v, **ws)
+        check(got, q, k, v, mask=mask)
+        assert torch.equal(got, nv.cross_attention(q, k, v, key_mask=mask, **ws))
+
+
 def test_nan_stays_in_its_query_and_head():
     q, k, v = make(10, 1, 70, 200, 4, 2, 64)
     want = nv.cross_attention(q, k, v)
