@@ -12,9 +12,9 @@
 // of a tile of 16 rows goes through the whole tile, and each row keeps the result
 // of its own (a select, so what another adapter holds cannot reach it).
 //
-// Measured at 4608 rows, 3072 to 9216, rank 32, five requests: 15 us and 48 us, the
-// second at 3.6 TB/s of y and out; at 48 rows of 12 requests, 3072 to 12288, rank
-// 16, with GELU and amax: 4.2 us and 8.7 us, bound by the latency of their chains
+// Measured at 4608 rows, 3072 to 9216, rank 32, five requests: 15 us and 42 us, the
+// second at 4.0 TB/s of y and out; at 48 rows of 12 requests, 3072 to 12288, rank
+// 16, with GELU and amax: 4.2 us and 8.6 us, bound by the latency of their chains
 // of loads (ids, adapter, product).
 #include "device_common.hpp"
 #include "kernels.hpp"
@@ -147,15 +147,18 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(Lora a) {
 // out = epi(y + up_a t).  A wave takes MT row tiles and 128 columns at a time, the
 // column blocks of the rows side by side, so y and out are read and written in
 // long pieces (with a workgroup's waves on four row tiles of one column block
-// instead, sharing the adapter's weights in the cache: 58 us against 55).  The weight is the MFMA's first operand, so a lane holds columns
-// of one row; the weight rows of a pair of MFMA tiles are dealt so that the 4 + 4
-// columns a lane gets are 8 neighbours (16 bytes of y and out).
+// instead, sharing the adapter's weights in the cache: 5 % slower).  An access is
+// of 16 rows' 64 bytes, halves of cache lines that meet in the cache: streamed past
+// it, 4608 x 9216 take 49 us, not 42, and 16896 x 9216 in all 199, not 180.  The
+// weight is the MFMA's first operand, so a lane holds columns of one row; the
+// weight rows of a pair of MFMA tiles are dealt so that the 4 + 4 columns a lane
+// gets are 8 neighbours (16 bytes of y and out).
 template <int RT, int MT>
 __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
   constexpr int KS = (RT + 1) / 2;             // 32-deep steps over the rank
   // column blocks that a tile of several adapters loads weights for at once: all of
   // them where rows are few (8.7 us against 12.2 at 48 rows), one where the registers
-  // cost waves (48 against 51 us at 4608 rows)
+  // cost waves (42 us against 45 at 4608 rows)
   constexpr int NB = MT > 1 ? 1 : KS <= 2 ? kColBlocks : kColBlocks / KS;
   const int lane = threadIdx.x & 63;
   const int r = lane & 15, q = lane >> 4;
@@ -186,8 +189,8 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
 #pragma unroll
       for (int b = 0; b < kColBlocks; ++b) {
         const int col = col0 + kColBlock * b + 8 * q;
-        yv[m][b] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
-            a.y + min(row0 + 16 * m, a.rows - 1) * a.outer + (col < a.outer ? col : 0)));
+        yv[m][b] = *reinterpret_cast<const u32x4*>(a.y + min(row0 + 16 * m, a.rows - 1) * a.outer +
+                                                   (col < a.outer ? col : 0));
       }
     bf16x8 tf[MT][KS];
 #pragma unroll
@@ -231,7 +234,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
       const u32x4 v = u32x4{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
                             bf16x2_rne(f[6], f[7])};
       if (row < a.rows && col < a.outer) {
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(a.out + row * a.outer + col));
+        *reinterpret_cast<u32x4*>(a.out + row * a.outer + col) = v;
         top = max_u16x2(top, max8(v));
       }
     };
@@ -324,7 +327,7 @@ hipError_t launch(const Lora& a, hipStream_t stream) {
   const int64_t tiles = (a.rows + kRowTile - 1) / kRowTile;
   // a workgroup of 12 waves fills a compute unit: two row tiles each (every weight
   // fragment then serves both) where that saves rounds over the compute units: at
-  // 4608 rows of 3072, rank 32, 144 workgroups take 15 us, 288 take 20
+  // 4608 rows of 3072, rank 32, 144 workgroups take 15 us, 288 take 21
   const int64_t units = compute_units();
   const int64_t one = (tiles + units - 1) / units, two = ((tiles + 1) / 2 + units - 1) / units;
   const int mt = RT <= 2 && 4 * two < 3 * one ? 2 : 1;
@@ -344,7 +347,7 @@ hipError_t launch(const Lora& a, hipStream_t stream) {
     lora_down_kernel<RT, 1><<<down, block, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // two row tiles a wave (the adapter's weights then serve both: 48 us against 55
+  // two row tiles a wave (the adapter's weights then serve both: 42 us against 45
   // at 4608 x 9216, rank 32) where that still leaves every compute unit 16 waves
   const int64_t cols = (a.outer + kColBlock * kColBlocks - 1) / (kColBlock * kColBlocks);
   const int64_t cap = units * 64;
