@@ -232,6 +232,32 @@ struct Attend {
     }
     sum += (t[0] + t[1]) + (t[2] + t[3]);
   }
+  // The K fragments of a tile's first 32 keys, read and waited for in one asm block
+  // for the same reason.
+  static __device__ __forceinline__ void k_read(const uint32_t (&at)[kSteps], u32x4 (&f)[kSteps]) {
+    if constexpr (kSteps == 8)
+      asm volatile(
+          "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
+          "ds_read_b128 %4, %12\n\tds_read_b128 %5, %13\n\tds_read_b128 %6, %14\n\tds_read_b128 %7, %15\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(f[4]), "=&v"(f[5]), "=&v"(f[6]), "=&v"(f[7])
+          : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7])
+          : "memory");
+    else
+      asm volatile(
+          "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
+          : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+          : "memory");
+  }
+  // Where fragment st of K starts for this lane, in a tile at `lds`.
+  __device__ __forceinline__ void k_rows(uint8_t* lds, uint32_t (&at)[kSteps]) const {
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st)
+      at[st] = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds + col * kRowBytes +
+               (((2 * st + half) ^ k_swizzle<DP>(col)) << 4);
+  }
   // Where block b's rows of V start for this lane, in a tile at `lds`.
   __device__ __forceinline__ void v_rows(uint8_t* lds, uint32_t (&at)[kBlocks]) const {
     const int row4 = (lane & 15) >> 2, quad = lane & 3, side = (lane >> 4) & 1, key = 4 * half + row4;
@@ -540,17 +566,18 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
 // Few query rows (at most 32 per kv head: single tokens): a workgroup's four
 // waves have the same rows and every fourth tile of 32 keys each, so no wave
 // waits for another; they are joined at the end.  What is left is the stream of
-// keys and values: K fragments go straight to registers (each element is used
-// by one lane once), V through LDS of the wave's own for the transposed reads,
-// both a tile ahead of their use.  One token of 8 entries of 1 to 8192 keys, 24
-// heads over 8: 41 us and 5 for the join, 129 MB at 3.2 TB/s (with the tiles shared
-// by the waves as above 48 in all); what lacks is the start of each workgroup and
-// the last ones, which find half a card to themselves.
+// keys and values, whole rows at a time into LDS of the wave's own: the next tile's
+// K is on its way as soon as this one's fragments are read, its V as soon as this
+// one's products are.  One token of 8 entries of 1 to 8192 keys, 24 heads over 8: 36
+// us and 5 for the join, 129 MB at 3.6 TB/s (with K fragments straight to
+// registers, 32 bytes of 32 rows an access: 41 and 5; in tiles that the waves share,
+// as above, 48 in all).  What is left is the first loads' latency, with nothing to
+// hide it, and the end, when workgroups run out one by one.
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
   using A = Attend<DP, 1>;
-  __shared__ __attribute__((aligned(1024))) uint8_t even[4 * A::kTileBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t odd[4 * A::kTileBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t tile_k[4 * A::kTileBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t tile_v[4 * A::kTileBytes];
   // every head's first split, then the second ones, ...
   Place p;
   const uint32_t heads = (uint32_t)a.units, split = blockIdx.x / heads, head = blockIdx.x - split * heads;
@@ -567,19 +594,20 @@ __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
   A w;
   w.start(a.scale);
   const uint16_t* q = query_row(a, p, w.col < rows ? w.col : rows - 1);
-  constexpr int kLoads = A::kKeys * A::kPieces / 64;
-  uint32_t k_off[A::kSteps], v_off[kLoads];
 #pragma unroll
   for (int st = 0; st < A::kSteps; ++st) {
     const int at = 16 * st + 8 * w.half;
     u32x4 f = u32x4{0u, 0u, 0u, 0u};
     if (at < a.dim) f = *reinterpret_cast<const u32x4*>(q + at);
     w.q[st] = as_bf16x8(f);
-    k_off[st] = at < a.dim ? (uint32_t)(w.col * a.k_token * 2 + at * 2) : kNoData;
   }
+  constexpr int kLoads = A::kKeys * A::kPieces / 64;
+  uint32_t k_off[kLoads], v_off[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int n = i * 64 + w.lane, key = n / A::kPieces, vp = (n % A::kPieces) ^ v_swizzle<DP>(key);
+    const int n = i * 64 + w.lane, key = n / A::kPieces, piece = n % A::kPieces;
+    const int kp = piece ^ k_swizzle<DP>(key), vp = piece ^ v_swizzle<DP>(key);
+    k_off[i] = 8 * kp < a.dim ? (uint32_t)(key * a.k_token * 2 + kp * 16) : kNoData;
     v_off[i] = 8 * vp < a.dim ? (uint32_t)(key * a.v_token * 2 + vp * 16) : kNoData;
   }
   const int last = min(first + a.share * 4, (p.keys + A::kKeys - 1) / A::kKeys);
@@ -588,76 +616,61 @@ __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
       if ((seen = seen_from<32>(p, t * A::kKeys, w.lane)) != 0) break;
     return t;
   };
-  u32x4 kf[A::kSteps];
-  // keys out of sight load as zeros
-  auto load_k = [&](int t, uint64_t seen) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(p.k + (int64_t)t * A::kKeys * a.k_token), (short)0, (int)kNoData, kBufferWord3);
-    const uint32_t hide = ((uint32_t)(~seen >> w.col) & 1u) * kNoData;
-#pragma unroll
-    for (int st = 0; st < A::kSteps; ++st)
-      kf[st] = __builtin_amdgcn_raw_buffer_load_b128(r, k_off[st] | hide, 0, 0);
-  };
-  const int own = wave * A::kTileBytes;          // this wave's part of `even` and `odd`
-  uint32_t even_at[A::kBlocks], odd_at[A::kBlocks];
-  w.v_rows(even + own, even_at);
-  w.v_rows(odd + own, odd_at);
-  auto load_v = [&](int t, uint64_t seen, uint8_t* lds) {
-    const uint16_t* v = p.v + (int64_t)t * A::kKeys * a.v_token;
+  // the rows of a tile from `from` on, `by` offsets of the lane's pieces; keys out of
+  // sight load as zeros
+  const int own = wave * A::kTileBytes;          // this wave's part of `tile_k` and `tile_v`
+  auto load = [&](const uint16_t* from, const uint32_t (&by)[kLoads], uint64_t seen, uint8_t* lds) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int key = (i * 64 + w.lane) / A::kPieces;
-      tile_load(v, v_off[i] | (((uint32_t)(~seen >> key) & 1u) * kNoData), lds, own + i * 1024);
+      tile_load(from, by[i] | (((uint32_t)(~seen >> key) & 1u) * kNoData), lds, own + i * 1024);
     }
   };
+  auto load_k = [&](int t, uint64_t seen) { load(p.k + (int64_t)t * A::kKeys * a.k_token, k_off, seen, tile_k); };
+  auto load_v = [&](int t, uint64_t seen) { load(p.v + (int64_t)t * A::kKeys * a.v_token, v_off, seen, tile_v); };
+  uint32_t v_at[A::kBlocks];
+  w.v_rows(tile_v + own, v_at);
+  uint32_t k_at[A::kSteps];
+  w.k_rows(tile_k + own, k_at);
   uint64_t seen = 0, seen_next = 0;
   int t = next(first + wave - 4, seen);
-  constexpr int kAhead = A::kSteps + kLoads;     // loads of one tile: 16 or 8
-  static_assert(kAhead < 64, "vmcnt counts to 63");
-  // the scores take the K registers, which the next tile's loads then refill;
-  // lgkmcnt(0): the reads of the V buffer that is filled next are done;
-  // vmcnt(kAhead): all but the next tile's loads are
-#define ATTEND_TURN(cur, nxt)                                                                    \
-  {                                                                                              \
-    const int tn = next(t, seen_next);                                                           \
-    f32x16 s[1] = {f32x16{}};                                                                    \
-    _Pragma("unroll") for (int st = 0; st < A::kSteps; ++st) s[0] =                              \
-        __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf[st]), w.q[st], s[0], 0, 0, 0);      \
-    __builtin_amdgcn_s_waitcnt(0xC07F);                                                          \
-    if (tn < last) {                                                                             \
-      load_k(tn, seen_next);                                                                     \
-      load_v(tn, seen_next, nxt);                                                                \
-      __builtin_amdgcn_s_waitcnt(0x0F70 | (kAhead & 15) | ((kAhead >> 4) << 14));                \
-    } else {                                                                                     \
-      __builtin_amdgcn_s_waitcnt(0x0F70);                                                        \
-    }                                                                                            \
-    asm volatile("" ::: "memory");                                                               \
-    w.weigh(s, seen);                                                                            \
-    w.gather_in_flight(s, cur##_at);                                                             \
-    t = tn;                                                                                      \
-    seen = seen_next;                                                                            \
-  }
   if (t < last) {
     load_k(t, seen);
-    load_v(t, seen, even);
+    load_v(t, seen);
     // the query fragments are waited for here (they came first), not in the
     // loop, where the wait would cover the loads in flight
 #pragma unroll
     for (int st = 0; st < A::kSteps; ++st) asm volatile("" : "+v"(w.q[st]));
-    for (;;) {
-      ATTEND_TURN(even, odd)
-      if (t >= last) break;
-      ATTEND_TURN(odd, even)
-      if (t >= last) break;
-    }
+    static_assert(kLoads < 16, "the wait's count is 4 bits");
+    do {
+      const int tn = next(t, seen_next);
+      __builtin_amdgcn_s_waitcnt(0x0F70 | kLoads);         // vmcnt: K is in, V may be on its way
+      asm volatile("" ::: "memory");
+      u32x4 kf[A::kSteps];
+      w.k_read(k_at, kf);
+      if (tn < last) load_k(tn, seen_next);
+      f32x16 s[1] = {f32x16{}};
+#pragma unroll
+      for (int st = 0; st < A::kSteps; ++st)
+        s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf[st]), w.q[st], s[0], 0, 0, 0);
+      w.weigh(s, seen);
+      if (tn < last)
+        __builtin_amdgcn_s_waitcnt(0x0F70 | kLoads);       // V is in, the next K may be on its way
+      else
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+      asm volatile("" ::: "memory");
+      w.gather_in_flight(s, v_at);                         // its reads are done when it ends
+      if (tn < last) load_v(tn, seen_next);
+      t = tn;
+      seen = seen_next;
+    } while (t < last);
   }
-#undef ATTEND_TURN
 
   // the four waves' states meet in LDS, in wave order: first the maxima and sums,
   // then the outputs, half the columns at a time (32 rows x DP / 2 of each wave
-  // in binary32 are what `even` holds)
-  float* park = reinterpret_cast<float*>(even);
-  float(*park_top)[32] = reinterpret_cast<float(*)[32]>(odd);
+  // in binary32 are what `tile_k` holds)
+  float* park = reinterpret_cast<float*>(tile_k);
+  float(*park_top)[32] = reinterpret_cast<float(*)[32]>(tile_v);
   float(*park_sum)[32] = park_top + 4;
   float *all_top = park_top[8], *all_sum = park_top[9];
   const float l = halves_sum(w.sum);
