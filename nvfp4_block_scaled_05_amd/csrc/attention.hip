@@ -436,15 +436,16 @@ struct RowStep {
 
 // Many query rows: the four waves of a workgroup have 32 rows each and share the
 // tiles of 64 keys, which the next turn's loads replace while this turn's are
-// used.  At 4608 queries and keys of 24 heads: 230 us, 1.01 PFLOP/s (the matrix
+// used.  At 4608 queries and keys of 24 heads: 218 us, 1.06 PFLOP/s (the matrix
 // cores alone reach 1.68 on such data); a tile of 32 rows by 64 keys costs a SIMD
 // 1024 cycles of matrix products and about 950 of exponentials, sums and maxima, and
-// two waves a SIMD hide about half of the latter.  The rest is power: on zeros,
-// the same instructions take 189 us.  At 16384 queries of a pair of 512 and 77
-// keys: 178 us, 0.66 PFLOP/s and 2.3 TB/s.  Not faster: the exponentials of one
-// block of 32 keys under the scores of the next in one wave (235), 64 rows a wave
-// (registers spill), the loads spread between the products (they spill), query
-// rows fetched a unit ahead by workgroups that stay (they spill: 247 for 178).
+// two waves a SIMD hide about half of the latter.  The rest is power: on zeros the
+// same instructions take a fifth less.  At 2 x 16384 queries of 77 and 512 keys: 164
+// us, 0.72 PFLOP/s and 2.5 TB/s.  Not faster, in turn with the same kernel: the
+// exponentials of one block of 32 keys under the scores of the next in one wave (235
+// us for 226), 64 rows a wave and the loads spread between the products (registers
+// spill), query rows fetched a unit ahead by workgroups that stay (they spill: 247
+// us for 178).
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
   using A = Attend<DP, 2>;
@@ -466,13 +467,16 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
   const int piece = w.lane % kRowPieces;
   u32x4 qrow[32 / kRowsPerLoad];
   {
-    // rows past the last read the first token's
+    // Rows past the last read the first token's.  Queries and outputs pass through
+    // once and are streamed past the caches, which stay with the keys (164 us against
+    // 172 at 2 x 16384 queries of 77 and 512 keys, 36 against 37.5 at 4096 of 512).
     const uint16_t* q = a.q + p.batch * a.q_batch + (8 * piece < a.dim ? 8 * piece : 0);
     const int64_t none = (int64_t)p.kvh * a.group * a.q_head;
     RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad, a.q_token, a.q_head);
 #pragma unroll
     for (int i = 0; i < 32 / kRowsPerLoad; ++i, step.next())
-      qrow[i] = *reinterpret_cast<const u32x4*>(q + (step.row < rows ? step.at : none));
+      qrow[i] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4*>(q + (step.row < rows ? step.at : none)));
   }
   p.keys = seen_keys(a, p);
   TileLoader<DP, 2, 4> load;
@@ -559,7 +563,8 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
     const int r = i * kRowsPerLoad + w.lane / kRowPieces;
     const u32x4 f =
         *reinterpret_cast<const u32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4));
-    if (step.row < rows && 8 * piece < a.dim) *reinterpret_cast<u32x4*>(out + step.at) = f;
+    if (step.row < rows && 8 * piece < a.dim)
+      __builtin_nontemporal_store(f, reinterpret_cast<u32x4*>(out + step.at));
   }
 }
 

@@ -107,7 +107,6 @@ struct Rotary {
   int64_t rows, tokens;          // rows = batch * tokens
   int axes, dim, rotary_dim, layout, tokens_per_group;
   float magnitude, eps, inv_dim;
-  bool streaming;                // filled in by the launch, as tokens_per_group
 };
 hipError_t launch_rotary(Rotary a, hipStream_t stream);
 

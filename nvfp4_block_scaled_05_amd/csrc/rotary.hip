@@ -40,7 +40,7 @@ __device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
 // One head is held by LANES neighbouring lanes of 8 elements each (the ones
 // past dim / 8 idle), so a head's norm is a sum over LANES lanes and the half
 // layout's partner elements are one lane exchange away.
-template <int LANES, bool HALF, bool NORM>
+template <int LANES, bool HALF, bool NORM, bool STREAM>
 __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
   __shared__ float2 turn[kRotEntries];
   __shared__ int64_t place[kRotTokens][4];       // where each token's heads start: q, k, q out, k out
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
       const RotaryHeads& v = is_q ? a.q : a.k;
       const int64_t at = place[tt][is_q ? 0 : 1] + (is_q ? hh : hh - a.q.heads) * v.in_head + 8 * chunk;
       const u32x4* from = reinterpret_cast<const u32x4*>(v.in + at);
-      return a.streaming ? __builtin_nontemporal_load(from) : *from;
+      return STREAM ? __builtin_nontemporal_load(from) : *from;
     };
     if (slot < items && mine) raw = fetch(t, head);
     for (int base = 0; base < items; base += kRotThreads / LANES) {
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
         const RotaryHeads& v = is_q ? a.q : a.k;
         const int64_t at = place[t_now][is_q ? 2 : 3] + (is_q ? head_now : head_now - a.q.heads) * v.out_head;
         u32x4* to = reinterpret_cast<u32x4*>(v.out + at + 8 * chunk);
-        if (a.streaming)
+        if constexpr (STREAM)
           __builtin_nontemporal_store(out, to);
         else
           *to = out;
@@ -163,19 +163,27 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
   }
 }
 
-template <int LANES, bool HALF>
+template <int LANES, bool HALF, bool STREAM>
 hipError_t launch_norm(const Rotary& a, int64_t grid, hipStream_t stream) {
   if (a.q.weight || a.k.weight)
-    rotary_kernel<LANES, HALF, true><<<dim3((unsigned)grid), dim3(kRotThreads), 0, stream>>>(a);
+    rotary_kernel<LANES, HALF, true, STREAM><<<dim3((unsigned)grid), dim3(kRotThreads), 0, stream>>>(a);
   else
-    rotary_kernel<LANES, HALF, false><<<dim3((unsigned)grid), dim3(kRotThreads), 0, stream>>>(a);
+    rotary_kernel<LANES, HALF, false, STREAM><<<dim3((unsigned)grid), dim3(kRotThreads), 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <int LANES, bool STREAM>
+hipError_t launch_layout(const Rotary& a, int64_t grid, hipStream_t stream) {
+  return a.layout == DIT_ROTARY_HALF ? launch_norm<LANES, true, STREAM>(a, grid, stream)
+                                     : launch_norm<LANES, false, STREAM>(a, grid, stream);
 }
 
 template <int LANES>
 hipError_t launch(const Rotary& a, int64_t grid, hipStream_t stream) {
-  return a.layout == DIT_ROTARY_HALF ? launch_norm<LANES, true>(a, grid, stream)
-                                     : launch_norm<LANES, false>(a, grid, stream);
+  // what the last-level cache cannot hold is streamed past the others (16896 tokens
+  // of 48 heads of 128: 97 us against 100; 4608, which it holds: 33 against 31)
+  const bool streaming = a.rows * (a.q.heads + a.k.heads) * a.dim * 4 > ((int64_t)256 << 20);
+  return streaming ? launch_layout<LANES, true>(a, grid, stream) : launch_layout<LANES, false>(a, grid, stream);
 }
 
 }  // namespace
@@ -195,9 +203,6 @@ hipError_t launch_rotary(Rotary a, hipStream_t stream) {
   const int64_t fill = (a.rows + 4 * compute_units() - 1) / (4 * compute_units());
   if (per > fill) per = (int)fill;
   a.tokens_per_group = per;
-  // what the last-level cache cannot hold is streamed past the others (95 us
-  // against 107 at 16896 tokens; up to half of that no difference)
-  a.streaming = a.rows * heads * a.dim * 4 > ((int64_t)256 << 20);
   const int64_t groups = (a.rows + per - 1) / per;
   const int64_t grid = groups < (1 << 20) ? groups : (1 << 20);    // the kernel strides over the rest
   switch (lanes) {
