@@ -44,12 +44,13 @@ __device__ __forceinline__ int v_swizzle(int key) {
 // array `lds`; offsets from kNoData up are out of the resource's range and load
 // zeros.  (LDS positions are an array and one offset throughout: the compiler
 // then still knows which array an access is to, and does not make reads of one
-// wait for loads in flight into the other.)
+// wait for loads in flight into the other.)  STREAM: past the caches.
+template <bool STREAM>
 __device__ __forceinline__ void tile_load(const void* base, uint32_t offset, uint8_t* lds, int to) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<void*>(base), (short)0, (int)kNoData, kBufferWord3);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      r, (__attribute__((address_space(3))) void*)(lds + to), 16, offset, 0, 0, 0);
+      r, (__attribute__((address_space(3))) void*)(lds + to), 16, offset, 0, 0, STREAM ? 2 : 0);   // 2: nt
 }
 
 __device__ __forceinline__ s16x4 transposed4(const uint8_t* lds, int at) {
@@ -327,16 +328,16 @@ struct TileLoader {
                                         uint8_t* lds_k, uint8_t* lds_v) const {
     if (seen == A::kAll) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) tile_load(k, k_off[i], lds_k, at[i]);
+      for (int i = 0; i < kLoads; ++i) tile_load<false>(k, k_off[i], lds_k, at[i]);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) tile_load(v, v_off[i], lds_v, at[i]);
+      for (int i = 0; i < kLoads; ++i) tile_load<false>(v, v_off[i], lds_v, at[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
-        tile_load(k, k_off[i] | (((uint32_t)(~seen >> key[i]) & 1u) * kNoData), lds_k, at[i]);
+        tile_load<false>(k, k_off[i] | (((uint32_t)(~seen >> key[i]) & 1u) * kNoData), lds_k, at[i]);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
-        tile_load(v, v_off[i] | (((uint32_t)(~seen >> key[i]) & 1u) * kNoData), lds_v, at[i]);
+        tile_load<false>(v, v_off[i] | (((uint32_t)(~seen >> key[i]) & 1u) * kNoData), lds_v, at[i]);
     }
   }
 };
@@ -573,10 +574,12 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
 // waits for another; they are joined at the end.  What is left is the stream of
 // keys and values, whole rows at a time into LDS of the wave's own: the next tile's
 // K is on its way as soon as this one's fragments are read, its V as soon as this
-// one's products are.  One token of 8 entries of 1 to 8192 keys, 24 heads over 8: 36
-// us and 5 for the join, 129 MB at 3.6 TB/s (with K fragments straight to
-// registers, 32 bytes of 32 rows an access: 41 and 5; in tiles that the waves share,
-// as above, 48 in all).  What is left is the first loads' latency, with nothing to
+// one's products are.  They are read once and streamed past the caches (134 MB of
+// keys and values: 32 us against 37, 537 MB 90 against 100; only a cache that the
+// call before this one read whole is 5 % slower, 31 against 29).  One token of 8
+// entries of 1 to 8192 keys, 24 heads over 8: 32 us and 5 for the join, 129 MB at 4.0
+// TB/s (with K fragments straight to registers, 32 bytes of 32 rows an access: 41
+// and 5; in tiles that the waves share, as above, 48 in all).  What is left is the first loads' latency, with nothing to
 // hide it, and the end, when workgroups run out one by one.
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
@@ -628,7 +631,7 @@ __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int key = (i * 64 + w.lane) / A::kPieces;
-      tile_load(from, by[i] | (((uint32_t)(~seen >> key) & 1u) * kNoData), lds, own + i * 1024);
+      tile_load<true>(from, by[i] | (((uint32_t)(~seen >> key) & 1u) * kNoData), lds, own + i * 1024);
     }
   };
   auto load_k = [&](int t, uint64_t seen) { load(p.k + (int64_t)t * A::kKeys * a.k_token, k_off, seen, tile_k); };
