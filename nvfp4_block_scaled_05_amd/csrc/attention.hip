@@ -437,8 +437,8 @@ struct RowStep {
 
 // Many query rows: the four waves of a workgroup have 32 rows each and share the
 // tiles of 64 keys, which the next turn's loads replace while this turn's are
-// used.  At 4608 queries and keys of 24 heads: 218 us, 1.06 PFLOP/s (the matrix
-// cores alone reach 1.68 on such data); a tile of 32 rows by 64 keys costs a SIMD
+// used.  At 4096 queries and 4608 keys of 24 heads: 218 us, 1.06 PFLOP/s (the
+// matrix cores alone reach 1.68 on such data); a tile of 32 rows by 64 keys costs a SIMD
 // 1024 cycles of matrix products and about 950 of exponentials, sums and maxima, and
 // two waves a SIMD hide about half of the latter.  The rest is power: on zeros the
 // same instructions take a fifth less.  At 2 x 16384 queries of 77 and 512 keys: 164
@@ -534,20 +534,31 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
 #undef ATTEND_TURN
 
   const float l = halves_sum(w.sum);
-  if (a.splits > 1) {      // unnormalised partial sums, the maximum and the sum
-    const int64_t slot = ((int64_t)unit * a.splits + split) * 128 + wave * 32 + w.col;
-    float* out = a.part + slot * DP;
-#pragma unroll
-    for (int b = 0; b < A::kBlocks; ++b)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<f32x4*>(out + 32 * b + 8 * g + 4 * w.half) =
-            f32x4{w.o[b][4 * g], w.o[b][4 * g + 1], w.o[b][4 * g + 2], w.o[b][4 * g + 3]};
-    if (w.half == 0) a.stats[slot] = float2{w.top, l};
-    return;
-  }
   // through the wave's rows of LDS again, so that whole rows are stored
   __syncthreads();
+  if (a.splits > 1) {      // unnormalised partial sums, half a row at a time, the maximum and the sum
+    const int64_t slot = ((int64_t)unit * a.splits + split) * 128 + wave * 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int b = 0; b < A::kBlocks / 2; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x16& o = w.o[h * (A::kBlocks / 2) + b];
+          *reinterpret_cast<f32x4*>(own + w.col * A::kRowBytes +
+                                    (((8 * b + 2 * g + w.half) ^ k_swizzle<DP>(w.col)) << 4)) =
+              f32x4{o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]};
+        }
+#pragma unroll
+      for (int i = 0; i < 32 / kRowsPerLoad; ++i) {
+        const int r = i * kRowsPerLoad + w.lane / kRowPieces;
+        *reinterpret_cast<f32x4*>(a.part + (slot + r) * DP + h * (DP / 2) + 4 * piece) =
+            *reinterpret_cast<const f32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4));
+      }
+    }
+    if (w.half == 0) a.stats[slot + w.col] = float2{w.top, l};
+    return;
+  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // no key seen: zeros
 #pragma unroll
   for (int b = 0; b < A::kBlocks; ++b)
@@ -739,16 +750,17 @@ __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
   }
 }
 
-// Joins the splits of a row, one wave per row: partial sums weighted by
-// 2^(their maximum - the largest), in split order.  Lane s holds split s's
-// maximum and sum (at most 64 splits).  A unit has `unit_rows` rows' slots a split.
+// Joins the splits of a row, DP / 4 lanes a row: partial sums weighted by
+// 2^(their maximum - the largest), in split order.  Lane n of a row's holds the
+// maxima and sums of splits n, n + DP / 4, ... (64 in all).  A unit has
+// `unit_rows` rows' slots a split.
 template <int DP>
 __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int unit_rows) {
-  const int lane = threadIdx.x & 63;
-  const int64_t rows = unit_rows;
-  const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();
+  constexpr int G = DP / 4, kRows = 64 / G, kHeld = 64 / G;
+  const int lane = threadIdx.x & 63, sub = lane % G, base = lane - sub;
+  const int64_t rows = unit_rows, all = a.units * rows;
+  const int64_t n = ((int64_t)blockIdx.x * 4 + wave_id()) * kRows + lane / G, at = min(n, all - 1);
   const uint32_t unit = (uint32_t)(at / rows), in = (uint32_t)(at - unit * rows);
-  if (unit >= (uint32_t)a.units) return;
   Place p;
   int64_t row = in;
   if (a.row_tiles == 0) {                        // few rows: a unit is a head
@@ -756,45 +768,49 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int un
   } else {
     place_unit(a, p, unit);
     row += (int64_t)p.row_tile * 128;
-    if (row >= (int64_t)a.queries * a.group) return;
   }
+  const bool live = n < all && row < (int64_t)a.queries * a.group;
   const int64_t first = (int64_t)unit * a.splits * rows + in;
-  float2 st = float2{0.0f, 0.0f};
-  if (lane < a.splits) st = a.stats[first + lane * rows];
-  float top = st.y != 0.0f ? st.x : -__builtin_inff();
+  float2 st[kHeld];
+  float top = -__builtin_inff();
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off, 64));
-  const float weight = st.y != 0.0f ? __builtin_amdgcn_exp2f(st.x - top) : 0.0f;
-  const float part_sum = st.y != 0.0f ? st.y * weight : 0.0f;
-  float l = 0.0f, o[DP / 64] = {};
+  for (int j = 0; j < kHeld; ++j) {
+    const int s = j * G + sub;
+    st[j] = s < a.splits ? a.stats[first + s * rows] : float2{0.0f, 0.0f};
+    if (st[j].y != 0.0f) top = __builtin_fmaxf(top, st[j].x);
+  }
+#pragma unroll
+  for (int off = G / 2; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off, 64));
+  float weight[kHeld], l = 0.0f;                 // 0: saw no key, what it left is not used
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    weight[j] = st[j].y != 0.0f ? __builtin_amdgcn_exp2f(st[j].x - top) : 0.0f;
+    if (weight[j] != 0.0f) l = __builtin_fmaf(st[j].y, weight[j], l);
+  }
+#pragma unroll
+  for (int off = G / 2; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+  f32x4 o = f32x4{};
   constexpr int U = 8;                           // loads in flight
-  for (int s0 = 0; s0 < a.splits; s0 += U) {
-    float v[U][DP / 64];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float* from = a.part + (first + min(s0 + u, a.splits - 1) * rows) * DP + lane * (DP / 64);
+  for (int j = 0; j < kHeld; ++j)
+    for (int s0 = j * G; s0 < min(a.splits, (j + 1) * G); s0 += U) {
+      f32x4 v[U];
 #pragma unroll
-      for (int j = 0; j < DP / 64; ++j) v[u][j] = from[j];
+      for (int u = 0; u < U; ++u)
+        v[u] = *reinterpret_cast<const f32x4*>(a.part + (first + min(s0 + u, a.splits - 1) * rows) * DP + 4 * sub);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f = __shfl(weight[j], base + (s0 + u) % G, 64);
+        if (s0 + u < a.splits && f != 0.0f) o += v[u] * f;
+      }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float f = __shfl(weight, (s0 + u) & 63, 64), y = __shfl(part_sum, (s0 + u) & 63, 64);
-      // past the splits, or a split that saw no key (what it left is not read)
-      if (s0 + u >= a.splits || (f == 0.0f && y == 0.0f)) continue;
-      l += y;
-#pragma unroll
-      for (int j = 0; j < DP / 64; ++j) o[j] = __builtin_fmaf(v[u][j], f, o[j]);
-    }
-  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* out = output_row(a, p, row);
-  if (DP == 128) {
-    if (2 * lane < a.dim)
-      *reinterpret_cast<uint32_t*>(out + 2 * lane) = bf16x2_rne(o[0] * inv, o[DP / 64 - 1] * inv);
-  } else if (lane < a.dim) {
-    out[lane] = (uint16_t)bf16x2_rne(o[0] * inv, 0.0f);
-  }
+  if (live && 4 * sub < a.dim)
+    *reinterpret_cast<u32x2*>(output_row(a, p, row) + 4 * sub) =
+        u32x2{bf16x2_rne(o[0] * inv, o[1] * inv), bf16x2_rne(o[2] * inv, o[3] * inv)};
 }
+
+constexpr int64_t kMaxSplits = 64;               // what the join's lanes hold
 
 // How a call is run.
 //   few: at most 32 rows per kv head, the kernel whose waves share the rows.  Its
@@ -802,32 +818,52 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int un
 // own keys only: enough for four workgroups a compute unit, each at least 256
 // keys.
 //   Otherwise units of 128 rows, whose keys are split where the units leave compute
-// units without work: up to 12 ways, each at least four tiles, towards two
-// workgroups a compute unit if that takes four ways or more, else one (4608 keys of
-// 24 heads: 96 units in 5 ways 54 us, in 2 ways 61, whole 89; 192 units in 2 ways
-// 96, whole 91: partial sums and their join cost about what they save).
+// units without work and splitting costs less than it saves, by `split_cost`.
 struct Plan {
   bool few;
   int64_t row_tiles, units, slots;               // slots: rows of partial sums in the workspace
   int splits, share;
 };
 
-Plan plan_for(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys) {
+// Microseconds of `units` units of `tiles` 64-key tiles in s splits: a tile takes a
+// workgroup t1 alone on its compute unit, t2 beside another (1.17 and 1.65 at a
+// padded head size of 128, 0.85 and 1.15 at 64); splits add a launch, about 5, and
+// their partial sums' way to memory and back at 4.6 TB/s.  Measured, whole against
+// split, 24 heads of 128: 512 queries of 512 keys 13 against 20 (2 ways), of 2304 44
+// against 32 (4 ways), of 4608 85 against 48; 1024 queries of 2304 47 against 49, of
+// 4608 88 against 82.
+double split_cost(int64_t units, int64_t tiles, int dp, int64_t s, int64_t cus) {
+  const double t1 = dp == 64 ? 0.85 : 1.17, t2 = dp == 64 ? 1.15 : 1.65;
+  const int64_t full = units * s / (2 * cus), rest = units * s % (2 * cus);
+  const double rounds = full * t2 + (rest > cus ? t2 : rest > 0 ? t1 : 0.0);
+  const double cost = rounds * (double)((tiles + s - 1) / s);
+  return s == 1 ? cost : cost + 5.0 + (double)(units * s) * 128 * dp * 4 * 2 / 4.6e6;
+}
+
+Plan plan_for(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys, int dp) {
   const int64_t heads = batch * kv_heads;
   if (rows <= 32) {
     const int64_t groups = (keys + 127) / 128;           // of four tiles of 32
     int64_t share = groups * heads / (4 * compute_units());
     if (share < 2) share = 2;
-    if (share < (groups + 63) / 64) share = (groups + 63) / 64;
+    if (share < (groups + kMaxSplits - 1) / kMaxSplits) share = (groups + kMaxSplits - 1) / kMaxSplits;
     const int64_t splits = groups > 0 ? (groups + share - 1) / share : 1;
     return {true, 0, heads, heads * splits * rows, (int)splits, (int)share};
   }
   const int64_t row_tiles = (rows + 127) / 128, units = heads * row_tiles, tiles = (keys + 63) / 64;
-  int64_t splits = 2 * compute_units() / units;
-  if (splits < 4) splits = compute_units() / units;
-  if (splits > 12) splits = 12;
-  if (splits > tiles / 4) splits = tiles / 4;
-  if (splits < 1) splits = 1;
+  const int64_t cus = compute_units();
+  int64_t splits = 1;
+  if (units <= 2 * cus) {
+    double least = split_cost(units, tiles, dp, 1, cus);
+    for (int64_t s : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+      if (s > tiles || s > kMaxSplits) break;
+      const double cost = split_cost(units, tiles, dp, s, cus);
+      if (cost < least) {
+        least = cost;
+        splits = s;
+      }
+    }
+  }
   return {false, row_tiles, units, units * splits * 128, (int)splits, 0};
 }
 
@@ -838,15 +874,16 @@ int padded_dim(int64_t dim) { return dim <= 64 ? 64 : 128; }
 size_t attention_workspace_bytes(int64_t batch, int64_t queries, int64_t keys, int64_t heads,
                                  int64_t kv_heads, int64_t dim) {
   if (batch == 0 || queries == 0) return 0;
-  const Plan plan = plan_for(batch, kv_heads, queries * (heads / kv_heads), keys);
-  return plan.splits == 1 ? 0 : (size_t)plan.slots * (padded_dim(dim) * 4 + 8);
+  const int dp = padded_dim(dim);
+  const Plan plan = plan_for(batch, kv_heads, queries * (heads / kv_heads), keys, dp);
+  return plan.splits == 1 ? 0 : (size_t)plan.slots * (dp * 4 + 8);
 }
 
 hipError_t launch_attention(Attention a, void* workspace, size_t workspace_bytes,
                             hipStream_t stream) {
   const int64_t rows = (int64_t)a.queries * a.group;
   const int dp = padded_dim(a.dim);
-  Plan plan = plan_for(a.batch, a.kv_heads, rows, a.keys);
+  Plan plan = plan_for(a.batch, a.kv_heads, rows, a.keys, dp);
   if (plan.splits > 1 && (!workspace || workspace_bytes < (size_t)plan.slots * (dp * 4 + 8))) {
     plan.share *= plan.splits;
     plan.splits = 1;
@@ -869,7 +906,8 @@ hipError_t launch_attention(Attention a, void* workspace, size_t workspace_bytes
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.splits == 1) return e;
   const int unit_rows = plan.few ? (int)rows : 128;
-  const dim3 join((unsigned)((plan.units * unit_rows + 3) / 4));
+  const int per = 4 * 64 / (dp / 4);             // rows a workgroup of the join has
+  const dim3 join((unsigned)((plan.units * unit_rows + per - 1) / per));
   dp == 64 ? attention_join_kernel<64><<<join, block, 0, stream>>>(a, unit_rows)
            : attention_join_kernel<128><<<join, block, 0, stream>>>(a, unit_rows);
   return hipGetLastError();

@@ -211,6 +211,24 @@ def test_same_bits_every_time_and_workspace_reuse():
     check(nv.cross_attention(q, k, v, workspace=small), q, k, v)
 
 
+@pytest.mark.parametrize("dim", [40, 64, 96, 128])
+@pytest.mark.parametrize("queries,heads,kv", [(1, 3, 1), (11, 3, 1), (45, 3, 1), (150, 2, 2)])
+def test_many_splits(queries, heads, kv, dim):
+    # splits that see all, some and none of their keys; a workspace of NaNs
+    keys = 4100
+    q, k, v = make(dim + queries, 3, queries, keys, heads, kv, dim)
+    lengths = ints(keys, 1900, 70)
+    mask = torch.ones(3, keys, dtype=torch.bool, device="cuda")
+    mask[0, 512:2700] = False
+    mask[1, :1700] = False
+    ws = nv.cross_attention_workspace(3, queries, keys, heads, kv, dim)
+    assert ws is not None
+    for kw in ({}, {"kv_lengths": lengths}, {"kv_lengths": lengths, "key_mask": mask}):
+        ws.fill_(255)
+        got = nv.cross_attention(q, k, v, workspace=ws, **kw)
+        check(got, q, k, v, lengths=kw.get("kv_lengths"), mask=kw.get("key_mask"))
+
+
 def test_captured_and_on_two_streams():
     q, k, v = make(14, 2, 3, 2000, 4, 2, 64)
     lengths = ints(2000, 17)
