@@ -16,7 +16,7 @@
 // memory would add a pass for its making and its bytes to every call.
 //
 // Measured in place on 24 + 24 heads of 128 in 16896 rows of a fused projection,
-// with both norms, three axes: 95 us, 415 MB at 4.4 TB/s.
+// with both norms, three axes: 81 us, 415 MB at 5.1 TB/s.
 #include "device_common.hpp"
 #include "kernels.hpp"
 
@@ -43,6 +43,7 @@ __device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
 template <int LANES, bool HALF, bool NORM, bool STREAM>
 __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
   __shared__ float2 turn[kRotEntries];
+  __shared__ __attribute__((aligned(16))) float weight[NORM ? 2 : 1][NORM ? 8 * LANES : 1];
   __shared__ int64_t place[kRotTokens][4];       // where each token's heads start: q, k, q out, k out
   const int pairs = a.rotary_dim / 2;
   const int chunk = threadIdx.x % LANES, slot = threadIdx.x / LANES;
@@ -54,14 +55,20 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
   const int partner = chunk + (upper ? -half_chunks : half_chunks);
   const int partner_lane = (threadIdx.x & 63) - chunk + partner;
   float wq[8], wk[8], pq[8], pk[8];              // the norms' weights of this lane's and its partner's elements
-  if (NORM) {
+  if (NORM) {                                    // through LDS: loaded from memory by every lane, 97 us for 85
+    for (int d = threadIdx.x; d < a.dim; d += kRotThreads) {
+      weight[0][d] = a.q.weight ? a.q.weight[d] : 1.0f;
+      weight[1][d] = a.k.weight ? a.k.weight[d] : 1.0f;
+    }
+    __syncthreads();
+    const int own = mine ? 8 * chunk : 0, other = turned ? 8 * partner : 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      wq[j] = a.q.weight && mine ? a.q.weight[8 * chunk + j] : 1.0f;
-      wk[j] = a.k.weight && mine ? a.k.weight[8 * chunk + j] : 1.0f;
+      wq[j] = weight[0][own + j];
+      wk[j] = weight[1][own + j];
       if (HALF) {
-        pq[j] = a.q.weight && turned ? a.q.weight[8 * partner + j] : 1.0f;
-        pk[j] = a.k.weight && turned ? a.k.weight[8 * partner + j] : 1.0f;
+        pq[j] = weight[0][other + j];
+        pk[j] = weight[1][other + j];
       }
     }
   }
@@ -181,7 +188,7 @@ hipError_t launch_layout(const Rotary& a, int64_t grid, hipStream_t stream) {
 template <int LANES>
 hipError_t launch(const Rotary& a, int64_t grid, hipStream_t stream) {
   // what the last-level cache cannot hold is streamed past the others (16896 tokens
-  // of 48 heads of 128: 97 us against 100; 4608, which it holds: 33 against 31)
+  // of 48 heads of 128: 85 us against 91; 4608, which it holds: 26 against 23)
   const bool streaming = a.rows * (a.q.heads + a.k.heads) * a.dim * 4 > ((int64_t)256 << 20);
   return streaming ? launch_layout<LANES, true>(a, grid, stream) : launch_layout<LANES, false>(a, grid, stream);
 }
@@ -190,14 +197,15 @@ hipError_t launch(const Rotary& a, int64_t grid, hipStream_t stream) {
 
 hipError_t launch_rotary(Rotary a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  // tokens a workgroup takes: four (at 16896 tokens of 48 heads of 128, 2 take 100
-  // us, 4 95, 8 103), more where a token's heads do not fill the workgroup four
-  // times over, as many as its table holds, and fewer while that would leave
-  // compute units without a workgroup
+  // tokens a workgroup takes: two (at 16896 tokens of 48 heads of 128, 1 takes 85 us,
+  // 2 81, 4 85, 8 96), more where a token's heads do not fill the workgroup four
+  // times over (53396 tokens of 6 heads of 96: 41 us, filled twice 47), as many as
+  // its table holds, and fewer while that would leave compute units without a
+  // workgroup
   const int chunks = a.dim / 8, lanes = chunks <= 4 ? 4 : chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
   const int heads = a.q.heads + a.k.heads;
   int per = 4 * (kRotThreads / lanes) / heads;
-  if (per < 4) per = 4;
+  if (per < 2) per = 2;
   if (per > kRotTokens) per = kRotTokens;
   if (per > kRotEntries / (a.rotary_dim / 2)) per = kRotEntries / (a.rotary_dim / 2);
   const int64_t fill = (a.rows + 4 * compute_units() - 1) / (4 * compute_units());
