@@ -9,14 +9,14 @@
 //
 // Bound: HBM.  x and y are read once, r and h written once (8 bytes a channel
 // with a bf16 stream); the vectors over channels (gate, scale, shift, weights)
-// are re-read per row from the caches.  One workgroup owns a row at a time and
+// are re-read per row from the caches or held.  One workgroup owns a row at a time and
 // keeps it in registers between the statistics and the outputs, so each
 // statistic is over values already on chip; mean and variance are two sums, the
 // second of squared distances from the mean, so channels with a large common
 // offset lose nothing.  All of it is binary32; r and h are each rounded once.
 //
-// Measured at 16896 x 3072 (bf16, gate, norm, scale and shift): 85 us, 415 MB at
-// 4.9 TB/s, what a copy of that size reaches.
+// Measured at 16896 x 3072 (bf16, gate, norm, scale and shift): 77 us, 415 MB at
+// 5.4 TB/s; a copy of 1 GiB reaches 4.6.
 #include "device_common.hpp"
 #include "kernels.hpp"
 
@@ -49,7 +49,7 @@ __device__ __forceinline__ Raw<uint16_t> load8(const uint16_t* p) {
   return {*reinterpret_cast<const u32x4*>(p)};
 }
 // x, y, r and h pass through once: they are streamed past the caches, which stay
-// with the vectors over channels (85 us against 90 at 16896 x 3072).
+// with the vectors over channels (85 us against 90 at 16896 x 3072, before modulations were held).
 __device__ __forceinline__ Raw<uint16_t> take8(const uint16_t* p) {
   return {__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p))};
 }
@@ -87,14 +87,6 @@ __device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
   __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f32x4*>(p) + 1);
 }
 
-// 8 entries of a modulation vector, stored as bf16 or fp32.
-__device__ __forceinline__ void vector8(const void* base, bool fp32, int64_t at, float (&f)[8]) {
-  if (fp32)
-    widen(load8(static_cast<const float*>(base) + at), f);
-  else
-    widen(load8(static_cast<const uint16_t*>(base) + at), f);
-}
-
 // v := (v - mean) * rstd of the row, in place; `mine[i]`: chunk i of this
 // thread exists.
 template <int LANES, int CH>
@@ -128,7 +120,13 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&mine)[
 // Rows of up to 64 chunks of 8 channels are held by LANES neighbouring lanes, one
 // chunk each, and a workgroup of 256 threads takes 256 / LANES of them at a time;
 // longer ones (LANES 0) by the whole workgroup, CH chunks a thread.
-template <class XT, int CH, int LANES>
+//
+// HOLD: gate, scale and shift (of type MT) stay in registers for as long as the batch
+// entry lasts.  Loaded within the row they come after the next row's loads, and
+// waiting for them is waiting for those: 85 us against 77 at 16896 x 3072.  With norm
+// weights beside them, or two chunks a lane, the registers would cost more waves than
+// that is worth (3063 x 1536 with all of them: 16 us held, 13 not).
+template <class XT, class MT, bool HOLD, int CH, int LANES>
 __global__ __launch_bounds__(LANES > 0 ? 256 : 1024) void gated_norm_kernel(GatedNorm a) {
   __shared__ float red[2][16];
   int half = 0;
@@ -157,9 +155,23 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 1024) void gated_norm_kernel(Gate
       if (a.y) yr[i] = take8(a.y + of * a.channels + at[i]);
     }
   };
+  Raw<MT> gate[CH], scale[CH], shift[CH];
+  auto modulation = [&](const void* base, int64_t stride, int64_t batch, int i) {
+    return load8(static_cast<const MT*>(base) + batch * stride + at[i]);
+  };
+  int64_t entry = -1;                            // whose modulation is held
   if (row < a.rows) fetch(row);
   while (row < a.rows) {
     const int64_t batch = row / a.tokens;
+    if (HOLD && batch != entry) {
+      entry = batch;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        if (a.gate) gate[i] = modulation(a.gate, a.gate_stride, batch, i);
+        if (a.scale) scale[i] = modulation(a.scale, a.scale_stride, batch, i);
+        if (a.shift) shift[i] = modulation(a.shift, a.shift_stride, batch, i);
+      }
+    }
     float v[CH][8], z[CH][8];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -184,7 +196,7 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 1024) void gated_norm_kernel(Gate
           for (int j = 0; j < 8; ++j) z[i][j] *= f[j];
         }
         if (a.gate) {
-          vector8(a.gate, a.mod_fp32, batch * a.gate_stride + at[i], f);
+          widen(HOLD ? gate[i] : modulation(a.gate, a.gate_stride, batch, i), f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) z[i][j] *= f[j];
         }
@@ -215,12 +227,12 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 1024) void gated_norm_kernel(Gate
           for (int j = 0; j < 8; ++j) v[i][j] += f[j];
         }
         if (a.scale) {
-          vector8(a.scale, a.mod_fp32, batch * a.scale_stride + at[i], f);
+          widen(HOLD ? scale[i] : modulation(a.scale, a.scale_stride, batch, i), f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j], f[j], v[i][j]);
         }
         if (a.shift) {
-          vector8(a.shift, a.mod_fp32, batch * a.shift_stride + at[i], f);
+          widen(HOLD ? shift[i] : modulation(a.shift, a.shift_stride, batch, i), f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[i][j] += f[j];
         }
@@ -246,13 +258,24 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 1024) void gated_norm_kernel(Gate
 
 __global__ void zero_amax_kernel(uint32_t* p) { *p = 0u; }
 
+bool weighted(const GatedNorm& a) { return a.weight || a.bias || a.post_weight; }
+
+template <class XT, class MT, int CH, int LANES>
+hipError_t launch_hold(const GatedNorm& a, int threads, int64_t grid, hipStream_t stream) {
+  if (CH > 1 || weighted(a))
+    gated_norm_kernel<XT, MT, false, CH, LANES><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
+  else
+    gated_norm_kernel<XT, MT, CH == 1, CH, LANES><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <int CH, int LANES>
 hipError_t launch(const GatedNorm& a, bool x_fp32, int threads, int64_t grid, hipStream_t stream) {
   if (x_fp32)
-    gated_norm_kernel<float, CH, LANES><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
-  else
-    gated_norm_kernel<uint16_t, CH, LANES><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
-  return hipGetLastError();
+    return a.mod_fp32 ? launch_hold<float, float, CH, LANES>(a, threads, grid, stream)
+                      : launch_hold<float, uint16_t, CH, LANES>(a, threads, grid, stream);
+  return a.mod_fp32 ? launch_hold<uint16_t, float, CH, LANES>(a, threads, grid, stream)
+                    : launch_hold<uint16_t, uint16_t, CH, LANES>(a, threads, grid, stream);
 }
 
 }  // namespace
@@ -266,13 +289,14 @@ hipError_t launch_gated_norm(const GatedNorm& a, bool x_fp32, hipStream_t stream
   if (a.rows == 0) return hipSuccess;
   const int chunks = a.channels / 8;
   // one chunk a lane up to 8192 channels: more waves with less to hold each load
-  // more at once (at 16896 x 3072 two chunks a lane take 103 us, one 85).  24 waves
-  // a compute unit (18: 94 us; 30, more than the registers hold: 116), rows spread
-  // evenly over the rounds.
+  // more at once (at 16896 x 3072 two chunks a lane take 103 us, one 85, before
+  // modulations were held).  Waves a compute unit, rows spread evenly over the
+  // rounds: 20 with modulations held (16: 83 us, 20: 77, 24: 79, 30: 88), 24 else (18:
+  // 94, 24: 85; 30, more than the registers hold: 116).
   const int lanes = chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : chunks <= 64 ? 64 : 0;
   const int waves = lanes ? 4 : chunks <= 1024 ? (chunks + 63) / 64 : 16;
   const int64_t turns = lanes ? (a.rows + 256 / lanes - 1) / (256 / lanes) : a.rows;
-  const int64_t cap = (int64_t)compute_units() * (24 / waves);
+  const int64_t cap = (int64_t)compute_units() * ((weighted(a) || waves == 16 ? 24 : 20) / waves);
   const int64_t rounds = (turns + cap - 1) / cap;
   const int64_t grid = (turns + rounds - 1) / rounds;
   switch (lanes) {

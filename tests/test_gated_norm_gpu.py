@@ -99,6 +99,16 @@ def test_post_norm(shape, stream, post):
     check(d, r, h, **kw)
 
 
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("mod", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [(5, 977, 1024), (70, 61, 520), (3, 6000, 72), (900, 3, 264)], ids=str)
+def test_modulation_follows_the_batch_entry(shape, mod, weights):
+    # workgroups take several rows, of several entries
+    d = make(5, *shape, mod=mod, weights=weights)
+    r, h = nv.gated_norm(**d)
+    check(d, r, h)
+
+
 def test_common_offset_loses_nothing():
     # mean 1000, deviation 2: a variance as a difference of squares would be
     # off by 1000^2 / 2^2 * U32 = 1.5 % here
