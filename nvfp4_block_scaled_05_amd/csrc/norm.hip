@@ -49,7 +49,8 @@ __device__ __forceinline__ Raw<uint16_t> load8(const uint16_t* p) {
   return {*reinterpret_cast<const u32x4*>(p)};
 }
 // x, y, r and h pass through once: they are streamed past the caches, which stay
-// with the vectors over channels (85 us against 90 at 16896 x 3072, before modulations were held).
+// with the vectors over channels (85 us against 90 at 16896 x 3072, before
+// modulations were held).
 __device__ __forceinline__ Raw<uint16_t> take8(const uint16_t* p) {
   return {__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p))};
 }
