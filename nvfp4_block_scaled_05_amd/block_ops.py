@@ -107,7 +107,7 @@ def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weigh
     one-element float32 device tensor, set to max |h| for ``quantize``.
 
     Returns (r, h): r in x's type (x itself when there is no y), h in bf16.
-    ``residual_out`` may be x, ``out`` may be y; channels: a multiple of 8, at
+    ``residual_out`` may be x, ``out`` may be y, no other overlap; channels: a multiple of 8, at
     most 16384.
     """
     torch = _torch()
@@ -159,6 +159,8 @@ def gated_norm(x, y=None, gate=None, scale=None, shift=None, norm="layer", weigh
         _like(out, "out", torch.bfloat16, shape)
     if residual_out is not None:
         _like(residual_out, "residual_out", x.dtype, shape)
+        if out is not None and out.data_ptr() == residual_out.data_ptr() and x.numel():
+            raise ValueError("out and residual_out are the same buffer")
     at = _place((x, y, gate, scale, shift, weight, bias, post_weight, amax, out, residual_out),
                 "x y gate scale shift weight bias post_weight amax out residual_out")
     if out is None and norm is not None:

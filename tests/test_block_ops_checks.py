@@ -295,6 +295,15 @@ def test_norm_none_rejects():
     raises("needs y", nv.gated_norm, x, norm=None)
 
 
+def test_gated_norm_refuses_one_place_for_two():
+    x, y = bf16(2, 3, 64), bf16(2, 3, 64)
+    raises("same buffer", nv.gated_norm, x, y, out=y, residual_out=y)
+    raises("same buffer", nv.gated_norm, x, y, out=x, residual_out=x)
+    raises("GPU tensor", nv.gated_norm, x, y, out=y, residual_out=x)
+    empty = bf16(2, 0, 64)
+    raises("GPU tensor", nv.gated_norm, empty, empty, out=empty, residual_out=empty)
+
+
 def test_rotary_refuses_one_place_for_two():
     plan = nv.rotary_plan(32, device="cpu")
     q, k, pos = bf16(2, 5, 3, 64), bf16(2, 5, 3, 64), i32(2, 5)
