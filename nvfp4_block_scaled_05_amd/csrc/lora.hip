@@ -140,7 +140,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(Lora a) {
     for (int w = 1; w < waves; ++w) v += red[w][e][lane];
     const int in = 16 * (e / (4 * RT)) + 4 * q + e % 4;
     const int64_t to = row0 + in;
-    if (to < a.rows && ((mine >> in) & 1)) a.t[((int64_t)blockIdx.y * a.rows + to) * (16 * RT) + 16 * (e / 4 % RT) + r] = v;
+    if (to < a.rows && ((mine >> in) & 1))
+      a.t[((int64_t)blockIdx.y * a.rows + to) * (16 * RT) + 16 * (e / 4 % RT) + r] = v;
   }
 }
 

@@ -124,9 +124,9 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&mine)[
 //
 // HOLD: gate, scale and shift (of type MT) stay in registers for as long as the batch
 // entry lasts.  Loaded within the row they come after the next row's loads, and
-// waiting for them is waiting for those: 85 us against 77 at 16896 x 3072.  With norm
-// weights beside them, or two chunks a lane, the registers would cost more waves than
-// that is worth (3063 x 1536 with all of them: 16 us held, 13 not).
+// waiting for them is waiting for those: at 16896 x 3072 85 us against 77, with an
+// fp32 stream 151 against 123, with weights and a post-norm besides 175 against 141.
+// Two chunks a lane would take too many registers.
 template <class XT, class MT, bool HOLD, int CH, int LANES>
 __global__ __launch_bounds__(LANES > 0 ? 256 : 1024) void gated_norm_kernel(GatedNorm a) {
   __shared__ float red[2][16];
@@ -259,24 +259,23 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 1024) void gated_norm_kernel(Gate
 
 __global__ void zero_amax_kernel(uint32_t* p) { *p = 0u; }
 
-bool weighted(const GatedNorm& a) { return a.weight || a.bias || a.post_weight; }
-
 template <class XT, class MT, int CH, int LANES>
-hipError_t launch_hold(const GatedNorm& a, int threads, int64_t grid, hipStream_t stream) {
-  if (CH > 1 || weighted(a))
-    gated_norm_kernel<XT, MT, false, CH, LANES><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
-  else
+hipError_t launch_hold(const GatedNorm& a, bool hold, int threads, int64_t grid, hipStream_t stream) {
+  if (CH == 1 && hold)
     gated_norm_kernel<XT, MT, CH == 1, CH, LANES><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
+  else
+    gated_norm_kernel<XT, MT, false, CH, LANES><<<dim3((unsigned)grid), dim3(threads), 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <int CH, int LANES>
-hipError_t launch(const GatedNorm& a, bool x_fp32, int threads, int64_t grid, hipStream_t stream) {
+hipError_t launch(const GatedNorm& a, bool x_fp32, bool hold, int threads, int64_t grid,
+                  hipStream_t stream) {
   if (x_fp32)
-    return a.mod_fp32 ? launch_hold<float, float, CH, LANES>(a, threads, grid, stream)
-                      : launch_hold<float, uint16_t, CH, LANES>(a, threads, grid, stream);
-  return a.mod_fp32 ? launch_hold<uint16_t, float, CH, LANES>(a, threads, grid, stream)
-                    : launch_hold<uint16_t, uint16_t, CH, LANES>(a, threads, grid, stream);
+    return a.mod_fp32 ? launch_hold<float, float, CH, LANES>(a, hold, threads, grid, stream)
+                      : launch_hold<float, uint16_t, CH, LANES>(a, hold, threads, grid, stream);
+  return a.mod_fp32 ? launch_hold<uint16_t, float, CH, LANES>(a, hold, threads, grid, stream)
+                    : launch_hold<uint16_t, uint16_t, CH, LANES>(a, hold, threads, grid, stream);
 }
 
 }  // namespace
@@ -289,25 +288,29 @@ hipError_t launch_gated_norm(const GatedNorm& a, bool x_fp32, hipStream_t stream
   }
   if (a.rows == 0) return hipSuccess;
   const int chunks = a.channels / 8;
-  // one chunk a lane up to 8192 channels: more waves with less to hold each load
-  // more at once (at 16896 x 3072 two chunks a lane take 103 us, one 85, before
-  // modulations were held).  Waves a compute unit, rows spread evenly over the
-  // rounds: 20 with modulations held (16: 83 us, 20: 77, 24: 79, 30: 88), 24 else (18:
-  // 94, 24: 85; 30, more than the registers hold: 116).
+  // One chunk a lane up to 8192 channels: more waves with less to hold each load
+  // more at once (at 16896 x 3072 two chunks a lane took 103 us, one 85).  Rows are
+  // spread evenly over the rounds.  Up to two rounds of 24 waves a compute unit (18:
+  // 94 us, 30, more than the registers hold: 116), nothing held: the first loads count
+  // (3063 x 1536, fp32 stream, all vectors: 13.2 us, 14.0 held).  Past that,
+  // modulations held and 20 waves (at 16896 x 3072 16 waves take 83 us, 20 77, 24 79),
+  // of an fp32 stream 16 (123 us, 18: 141).
   const int lanes = chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : chunks <= 64 ? 64 : 0;
   const int waves = lanes ? 4 : chunks <= 1024 ? (chunks + 63) / 64 : 16;
   const int64_t turns = lanes ? (a.rows + 256 / lanes - 1) / (256 / lanes) : a.rows;
-  const int64_t cap = (int64_t)compute_units() * ((weighted(a) || waves == 16 ? 24 : 20) / waves);
+  const int64_t units = compute_units();
+  const bool hold = turns > 2 * units * (24 / waves) && chunks <= 1024;
+  const int64_t cap = units * ((!hold ? 24 : x_fp32 ? 16 : 20) / waves);
   const int64_t rounds = (turns + cap - 1) / cap;
   const int64_t grid = (turns + rounds - 1) / rounds;
   switch (lanes) {
-    case 8: return launch<1, 8>(a, x_fp32, 256, grid, stream);
-    case 16: return launch<1, 16>(a, x_fp32, 256, grid, stream);
-    case 32: return launch<1, 32>(a, x_fp32, 256, grid, stream);
-    case 64: return launch<1, 64>(a, x_fp32, 256, grid, stream);
+    case 8: return launch<1, 8>(a, x_fp32, hold, 256, grid, stream);
+    case 16: return launch<1, 16>(a, x_fp32, hold, 256, grid, stream);
+    case 32: return launch<1, 32>(a, x_fp32, hold, 256, grid, stream);
+    case 64: return launch<1, 64>(a, x_fp32, hold, 256, grid, stream);
   }
-  return chunks <= 1024 ? launch<1, 0>(a, x_fp32, 64 * waves, grid, stream)
-                        : launch<2, 0>(a, x_fp32, 1024, grid, stream);
+  return chunks <= 1024 ? launch<1, 0>(a, x_fp32, hold, 64 * waves, grid, stream)
+                        : launch<2, 0>(a, x_fp32, hold, 1024, grid, stream);
 }
 
 }  // namespace nvfp4
