@@ -14,8 +14,8 @@ projection takes its input from the caller.  DitCrossBlock is a whole block
 whose image tokens attend to a text encoder's states.
 """
 
-from . import (cross_attention, cross_attention_workspace, gated_norm, gemm, gemm_bf16,
-               gemm_workspace, layer_is_quantized, lora_add, lora_workspace, quantize,
+from . import (_device, _tensor, cross_attention, cross_attention_workspace, gated_norm, gemm,
+               gemm_bf16, gemm_workspace, layer_is_quantized, lora_add, lora_workspace, quantize,
                quantize_workspace, quantize_weight, rotary)
 
 #: layer name -> (input, weight, epilogue)
@@ -152,7 +152,9 @@ class DitCrossBlock:
         self.h, self.r = bf16(batch, tokens, hidden), bf16(batch, tokens, hidden)
         self.result = bf16(batch, tokens, hidden)
         self.attended = bf16(batch, tokens, heads, dim)
-        self.k = self.v = self.lengths = None
+        self.k = self.v = None
+        # the block's own, so that a captured call finds the last prompt's lengths in it
+        self.lengths = torch.full((batch,), states, dtype=torch.int32, device=dev)
         self.attn_ws = cross_attention_workspace(batch, tokens, states, heads, kv_heads, dim, dev)
         self.amax = torch.zeros((1,), dtype=torch.float32, device=dev)
         self.quant_ws = quantize_workspace(dev)
@@ -178,13 +180,23 @@ class DitCrossBlock:
 
     def encode(self, states, lengths=None):
         """Keys and values of encoder ``states`` [batch, states, width] (bf16);
-        ``lengths``: int32 [batch], the states of each prompt.  The rest is
-        padding; it is quantized with the states, so it has to be finite."""
+        ``lengths``: int32 [batch], the states of each prompt, None for all of
+        them.  The rest is padding; it is quantized with the states, so it has to
+        be finite.  All of it, the lengths too, is copied into the block's buffers:
+        a captured call that is replayed after another prompt follows that one."""
+        import torch
+        if lengths is not None:
+            _tensor(lengths, "lengths", torch.int32, (self.batch,))
+            _device(states=states, lengths=lengths)
         kv = self._linear(self.to_kv, states.view(-1, states.shape[-1]))
         kv = kv.view(self.batch, self.states, 2, self.kv_heads, -1)
-        k, self.v, self.lengths = kv[:, :, 0], kv[:, :, 1], lengths
+        k, self.v = kv[:, :, 0], kv[:, :, 1]
         # text states carry no position: position 0 leaves their norm alone
         self.k = rotary(k, self.no_positions, self.plan, q_weight=self.k_norm, out=k)
+        if lengths is None:
+            self.lengths.fill_(self.states)
+        else:
+            self.lengths.copy_(lengths)
 
     def __call__(self, temb, x, positions, ids=None):
         """temb [batch, cond], x [batch, tokens, hidden], positions as ``rotary``

@@ -165,3 +165,58 @@ def test_graph_replays_equal_eager_and_follow_the_inputs():
         got = g.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("first", ["lengths", "none"])
+def test_replay_follows_another_prompt(first):
+    # captured under one prompt, replayed under others, whose lengths are tensors of their own
+    block, (temb, x, pos, ids), states, lengths = make()
+    rng = np.random.default_rng(9)
+    block.encode(states, lengths if first == "lengths" else None)
+    g = capture(lambda: block(temb, x, pos, ids))
+    prompts = [(normal(rng, (B, L, ENC)), n if n is None else torch.tensor(n, dtype=torch.int32, device="cuda"))
+               for n in ([3, L], None, [L, 1], [0, 20])]
+    seen = []
+    for s, n in prompts + [(states, lengths)]:
+        block.encode(s, n)
+        for _ in range(2):
+            want = block(temb, x, pos, ids).clone()
+            torch.cuda.synchronize()
+            block.result.fill_(7.0)
+            got = g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+        seen.append(want)
+        # as with a block that never saw another prompt
+        fresh = make()[0]
+        fresh.encode(s, n)
+        assert torch.equal(fresh(temb, x, pos, ids), want)
+    assert all(not torch.equal(a, b) for i, a in enumerate(seen) for b in seen[:i])
+
+
+def test_lengths_are_the_prompts():
+    block, (temb, x, pos, ids), states, lengths = make(False)
+    block.encode(states, lengths)
+    want = block(temb, x, pos).clone()
+    lengths.zero_()                                   # the caller's again after encode
+    assert torch.equal(block(temb, x, pos), want)
+    for bad in (lengths.long(), lengths[:1], lengths.cpu(), [L, 5]):
+        with pytest.raises(ValueError, match="lengths"):
+            block.encode(states, bad)
+    assert torch.equal(block(temb, x, pos), want)     # a refused call left the prompt alone
+
+
+def test_captured_encode_follows_states_and_lengths():
+    block, (temb, x, pos, ids), states, lengths = make()
+    g = capture(lambda: (block.encode(states, lengths), block(temb, x, pos, ids))[1])
+    rng = np.random.default_rng(10)
+    other = make()[0]
+    for n in ([1, 2], [L, 0], [17, L]):
+        states.copy_(normal(rng, (B, L, ENC)))
+        lengths.copy_(torch.tensor(n, dtype=torch.int32))
+        other.encode(states, lengths)
+        want = other(temb, x, pos, ids).clone()
+        torch.cuda.synchronize()
+        got = g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
