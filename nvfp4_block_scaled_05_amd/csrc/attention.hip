@@ -781,11 +781,14 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int un
   }
 #pragma unroll
   for (int off = G / 2; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off, 64));
-  float weight[kHeld], l = 0.0f;                 // 0: saw no key, what it left is not used
+  // -1: saw no key, what it left is not used.  A weight of 0 is used: a split of
+  // NaN scores has no maximum to count with, and one far below the others' may hold
+  // NaN or infinite values.
+  float weight[kHeld], l = 0.0f;
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
-    weight[j] = st[j].y != 0.0f ? __builtin_amdgcn_exp2f(st[j].x - top) : 0.0f;
-    if (weight[j] != 0.0f) l = __builtin_fmaf(st[j].y, weight[j], l);
+    weight[j] = st[j].y != 0.0f ? __builtin_amdgcn_exp2f(st[j].x - top) : -1.0f;
+    if (!(weight[j] < 0.0f)) l = __builtin_fmaf(st[j].y, weight[j], l);
   }
 #pragma unroll
   for (int off = G / 2; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
@@ -801,7 +804,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int un
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const float f = __shfl(weight[j], base + (s0 + u) % G, 64);
-        if (s0 + u < a.splits && f != 0.0f) o += v[u] * f;
+        if (s0 + u < a.splits && !(f < 0.0f)) o += v[u] * f;
       }
     }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;

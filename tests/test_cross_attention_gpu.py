@@ -252,3 +252,30 @@ def test_captured_and_on_two_streams():
             got[i] = nv.cross_attention(*sets[i])
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("queries", [1, 40])
+@pytest.mark.parametrize("what", ["key", "value", "infinity"])
+def test_nan_in_a_split_of_its_own_is_not_lost(what, queries):
+    # one visible key among 2000 hidden ones, so some split sees that key alone
+    q, k, v = make(15, 1, queries, 4100, 2, 1, 64)
+    q = q.abs() + 0.5
+    mask = torch.ones(1, 4100, dtype=torch.bool, device="cuda")
+    mask[0, 1000:3000] = False
+    mask[0, 2000] = True
+    ws = nv.cross_attention_workspace(1, queries, 4100, 2, 1, 64)
+    assert ws is not None
+    if what == "key":                        # a score that is no number: no weight is one
+        k[0, 2000] = float("nan")
+    else:                                    # a weight of 2^-1000 or less is 0, and 0 times these is NaN
+        k[0, 2000] = -500.0
+        v[0, 2000, 0, 7] = float("nan" if what == "value" else "inf")
+    for w in (ws, None):
+        got = nv.cross_attention(q, k, v, key_mask=mask, workspace=w)
+        gone = torch.isnan(got)
+        if what == "key":
+            assert gone.all()
+        else:
+            assert gone[..., 7].all()
+            gone[..., 7] = False
+            assert not gone.any()
