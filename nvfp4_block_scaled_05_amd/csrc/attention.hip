@@ -559,15 +559,17 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
     if (w.half == 0) a.stats[slot + w.col] = float2{w.top, l};
     return;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // no key seen: zeros
+  // no key seen, or scores of -infinity alone: zeros, whatever 0 times their values left
+  const uint32_t any = l == 0.0f ? 0u : ~0u;
+  const float inv = 1.0f / l;
 #pragma unroll
   for (int b = 0; b < A::kBlocks; ++b)
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       *reinterpret_cast<u32x2*>(own + w.col * A::kRowBytes + (((4 * b + g) ^ k_swizzle<DP>(w.col)) << 4) +
                                 8 * w.half) =
-          u32x2{bf16x2_rne(w.o[b][4 * g] * inv, w.o[b][4 * g + 1] * inv),
-                bf16x2_rne(w.o[b][4 * g + 2] * inv, w.o[b][4 * g + 3] * inv)};
+          u32x2{bf16x2_rne(w.o[b][4 * g] * inv, w.o[b][4 * g + 1] * inv) & any,
+                bf16x2_rne(w.o[b][4 * g + 2] * inv, w.o[b][4 * g + 3] * inv) & any};
   uint16_t* out = a.out + p.batch * a.o_batch + 8 * piece;
   RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad, a.o_token, a.o_head);
 #pragma unroll

@@ -279,3 +279,15 @@ def test_nan_in_a_split_of_its_own_is_not_lost(what, queries):
             assert gone[..., 7].all()
             gone[..., 7] = False
             assert not gone.any()
+
+
+@pytest.mark.parametrize("queries", [3, 200])
+def test_rows_of_minus_infinity_are_zeros_whatever_the_values(queries):
+    q, k, v = make(16, 1, queries, 900, 2, 1, 64)
+    q = q.abs() + 0.1
+    k[:] = float("-inf")
+    v[..., 5] = float("nan")
+    v[..., 6] = float("inf")
+    for ws in ({}, {"workspace": None}):
+        got = nv.cross_attention(q, k, v, **ws)
+        assert torch.equal(got, torch.zeros_like(got))
