@@ -191,8 +191,9 @@ class DitCrossBlock:
         kv = self._linear(self.to_kv, states.view(-1, states.shape[-1]))
         kv = kv.view(self.batch, self.states, 2, self.kv_heads, -1)
         k, self.v = kv[:, :, 0], kv[:, :, 1]
-        # text states carry no position: position 0 leaves their norm alone
-        self.k = rotary(k, self.no_positions, self.plan, q_weight=self.k_norm, out=k)
+        # text states carry no position: position 0, without the factor on rotated
+        # values that a YaRN plan has, leaves their norm alone
+        self.k = rotary(k, self.no_positions, self.plan._replace(magnitude=1.0), q_weight=self.k_norm, out=k)
         if lengths is None:
             self.lengths.fill_(self.states)
         else:

@@ -220,3 +220,18 @@ def test_captured_encode_follows_states_and_lengths():
         got = g.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_text_keys_carry_no_rotary_factor(monkeypatch):
+    # a YaRN plan over half of each head: its factor belongs to rotated elements,
+    # and the text keys are not rotated
+    plan = nv.rotary_plan(32, scaling="yarn", factor=32.0, original_length=4096)
+    assert plan.magnitude > 1.3
+    monkeypatch.setattr(nv, "rotary_plan", lambda *a, **k: plan)
+    block, _, states, lengths = make(False)
+    block.encode(states, lengths)
+    kv = nv.linear(states.view(-1, ENC), block.weights[KVP], KVP).view(B, L, 2, KV, DIM)
+    assert torch.equal(block.v, kv[:, :, 1])
+    # bounds as in the norm's own tests: 64 U32 of the row's largest term, and one rounding
+    want = ob.normalise(f64(kv[:, :, 0]), "rms", 1e-6) * f64(block.k_norm)
+    assert_within(block.k, want, UBF * np.abs(want) + 64 * U32 * np.abs(want).max(-1, keepdims=True), "keys")
