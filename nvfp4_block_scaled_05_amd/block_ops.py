@@ -185,11 +185,18 @@ RotaryPlan = namedtuple("RotaryPlan", ["turns", "axis", "rotary_dim", "axes", "m
 def _yarn_blend(pairs, dim, base, original_length, beta_fast, beta_slow):
     """How far each pair's frequency is interpolated (0: kept, 1: divided by the
     factor): none for pairs with more than beta_fast turns over the trained
-    length, fully below beta_slow turns, linear in the pair index between."""
+    length, fully below beta_slow turns, linear in the pair index between, from
+    whole pair to whole pair."""
     def index_of(turns):
         return dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
-    low = max(math.floor(index_of(beta_fast)), 0)
-    high = min(math.ceil(index_of(beta_slow)), dim - 1)
+    fast, slow = index_of(beta_fast), index_of(beta_slow)
+    # no pair between the two: the ramp's ends, clamped to the pairs, would change places
+    if fast >= pairs - 1:
+        return [0.0] * pairs
+    if slow <= 0:
+        return [1.0] * pairs
+    low = max(math.floor(fast), 0)
+    high = min(math.ceil(slow), dim - 1)
     width = high - low if high != low else 0.001
     return [min(max((j - low) / width, 0.0), 1.0) for j in range(pairs)]
 
@@ -205,9 +212,12 @@ def rotary_plan(rotary_dim, base=10000.0, axes=None, scaling="none", factor=1.0,
       "linear"  every frequency divided by the factor;
       "ntk"     the base raised to base * factor ** (d / (d - 2));
       "yarn"    by parts ("YaRN: Efficient Context Window Extension of Large
-                Language Models", section 3): frequencies below beta_slow turns
-                over original_length divided, above beta_fast kept, blended
-                between; rotated values scaled by 0.1 ln(factor) + 1.
+                Language Models"): frequencies below beta_slow turns over
+                original_length divided, above beta_fast kept, blended between;
+                rotated values scaled by 0.1 ln(factor) + 1.  The blend is linear
+                in the pair index between whole pairs, the form that released
+                checkpoints are trained and run with; the paper's section 3
+                states it linear in the turns.
     """
     torch = _torch()
     if rotary_dim <= 0 or rotary_dim % 16 or rotary_dim > 256:

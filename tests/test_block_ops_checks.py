@@ -326,3 +326,31 @@ def test_sizes_past_the_grid_are_refused(lib):
     assert lib.dit_lora_add(A, A, A, A, A, None, 1 << 26, 64, 32, 16, 1, 0, A, None, A, 1 << 40, None) == SHAPE
     assert lib.dit_cross_attention(heads(), heads(), heads(), None, None, 0, 1 << 12, 33, 9, 1 << 13, 1 << 13, 64,
                                    0.1, heads(), None, 0, None) == SHAPE
+
+
+def yarn_radians(dim, length, factor=32.0, **kw):
+    return (nv.rotary_plan(dim, scaling="yarn", factor=factor, original_length=length, device="cpu", **kw).turns
+            * 2 * math.pi).tolist()
+
+
+def test_yarn_blend_between_the_ends():
+    # 32 turns over 4096 positions fall to pair 64 ln(4096 / 64 pi) / (2 ln 10000) = 10.47, one turn
+    # to pair 22.5: kept up to 10, divided from 23 on, in between linear in the pair index
+    for j, f in enumerate(yarn_radians(64, 4096)):
+        plain, slow = 10000.0 ** (-j / 32), min(max((j - 10) / 13, 0.0), 1.0)
+        assert f == pytest.approx(plain * (1 - slow) + plain / 32 * slow, rel=1e-12), j
+
+
+@pytest.mark.parametrize("kw,length", [(dict(base=2.0), 4096), (dict(base=1.01), 300), ({}, 1 << 50),
+                                       (dict(axes=(16, 48)), 1 << 50)])
+def test_yarn_keeps_pairs_that_all_turn_often(kw, length):
+    # every pair turns more than 32 times over the trained length: none is divided
+    want = (nv.rotary_plan(64, device="cpu", **kw).turns * 2 * math.pi).tolist()
+    assert min(want) * length / (2 * math.pi) > 32
+    assert yarn_radians(64, length, **kw) == pytest.approx(want, rel=1e-12)
+
+
+@pytest.mark.parametrize("length", [1, 3, 6])
+def test_yarn_divides_pairs_that_all_turn_less_than_once(length):
+    want = (nv.rotary_plan(64, device="cpu").turns * 2 * math.pi / 32).tolist()
+    assert yarn_radians(64, length) == pytest.approx(want, rel=1e-12)
