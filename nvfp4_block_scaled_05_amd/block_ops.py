@@ -486,7 +486,7 @@ def lora_add(y, x, down, up, ids, scales=None, epilogue="none", y_amax=None, out
     epi = _epilogue(epilogue)
     _opt(y_amax, "y_amax", torch.float32)
     _opt(out, "out", torch.bfloat16, (rows, outer))
-    ws = None if workspace is _NO_WORKSPACE else _tensor(workspace, "workspace", torch.uint8)
+    ws = None if workspace is _NO_WORKSPACE else _tensor(workspace, "workspace", torch.uint8, min_numel=0)
     at = _place((y, x, down, up, ids, scales, y_amax, out, ws),
                 "y x down up ids scales y_amax out workspace")
     if out is None:

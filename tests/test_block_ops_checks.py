@@ -354,3 +354,14 @@ def test_yarn_keeps_pairs_that_all_turn_often(kw, length):
 def test_yarn_divides_pairs_that_all_turn_less_than_once(length):
     want = (nv.rotary_plan(64, device="cpu").turns * 2 * math.pi / 32).tolist()
     assert yarn_radians(64, length) == pytest.approx(want, rel=1e-12)
+
+
+def test_lora_takes_the_workspace_of_no_rows():
+    # what lora_workspace makes for no rows has no bytes; the call is a no-op, not an error
+    ws = nv.lora_workspace(0, 64, 16, device="cpu")
+    assert ws.numel() == 0
+    raises("GPU tensor", nv.lora_add, bf16(0, 32), bf16(0, 64), bf16(3, 16, 64), bf16(3, 32, 16), i32(0),
+           workspace=ws)
+    # for rows it is refused all the same, by its size
+    raises("GPU tensor", nv.lora_add, bf16(6, 32), bf16(6, 64), bf16(3, 16, 64), bf16(3, 32, 16), i32(6),
+           workspace=ws)

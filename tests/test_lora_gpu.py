@@ -152,3 +152,12 @@ def test_captured_and_workspace_reuse():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(amax, want_max)
+
+
+def test_no_rows_with_their_workspace():
+    d = make(8, 0, 64, 64, 8, 1)
+    ws = nv.lora_workspace(0, 64, 8)
+    amax = torch.ones(1, device="cuda")
+    assert nv.lora_add(**d, y_amax=amax, workspace=ws).shape == (0, 64) and amax.item() == 0
+    with pytest.raises(nv.Nvfp4Error):
+        nv.lora_add(**make(8, 5, 64, 64, 8, 1), workspace=ws)
