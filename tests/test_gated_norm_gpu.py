@@ -193,3 +193,38 @@ def test_captured_and_on_two_streams():
             got[i] = nv.gated_norm(**others[i])[1]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def held_rows(channels):
+    """More rows than the launch takes in two rounds of 24 waves a compute unit (256 a packed
+    workgroup's lanes, or one workgroup each), from where on modulations are held."""
+    chunks = channels // 8
+    lanes = next((n for n in (8, 16, 32, 64) if chunks <= n), 0)
+    waves = 4 if lanes else -(-chunks // 64)
+    units = torch.cuda.get_device_properties(0).multi_processor_count
+    return int(2.3 * units * (24 // waves)) * (256 // lanes if lanes else 1)
+
+
+@pytest.mark.parametrize("stream,mod", [("bf16", torch.bfloat16), ("bf16", torch.float32),
+                                        ("f32", torch.bfloat16), ("f32", torch.float32)])
+@pytest.mark.parametrize("entries", [3, 211])     # several rows of a workgroup in an entry; one at most
+@pytest.mark.parametrize("channels", [64, 120, 200, 264, 520, 1032, 3000, 6008, 8192])
+def test_held_modulations_follow_the_batch_entry(channels, entries, stream, mod):
+    tokens = held_rows(channels) // entries + 1
+    weights, use = channels % 16 == 8, "ygsh" if channels != 1032 else "ysh"
+    d = make(channels + entries, entries, tokens, channels, stream=stream, mod=mod, weights=weights, use=use,
+             post="rms" if weights else "none")
+    kw = dict(norm="layer" if channels % 3 else "rms", post_norm="rms" if weights else "none")
+    amax = torch.zeros(1, device="cuda")
+    r, h = nv.gated_norm(**d, **kw, amax=amax)
+    check(d, r, h, **kw)
+    assert amax.item() == h.abs().max().item()
+    # in place, entry after entry in calls that are too small to hold anything: the same bits
+    i = entries // 2
+    one = {k: v if v is None or v.dim() == 1 else v[i:i + 1, :300] if v.dim() == 3 else v[i:i + 1]
+           for k, v in d.items()}
+    one["x"], one["y"] = one["x"].contiguous(), one["y"].contiguous()
+    r1, h1 = nv.gated_norm(**one, **kw)
+    assert torch.equal(r1, r[i:i + 1, :300]) and torch.equal(h1, h[i:i + 1, :300])
+    r2, h2 = nv.gated_norm(**d, **kw, residual_out=d["x"], out=d["y"])
+    assert torch.equal(r2, r) and torch.equal(h2, h)
