@@ -152,3 +152,33 @@ def test_empty_and_captured():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("heads,kv,dim,rot", [(3, 2, 32, 32), (4, 1, 40, 32), (9, 3, 128, 96), (2, 1, 200, 112)])
+def test_tensors_past_the_last_level_cache(heads, kv, dim, rot, norm, layout):
+    # more than 256 MiB read and written: accesses that pass the caches by, here in place
+    # on views of a fused projection
+    rng = np.random.default_rng(dim)
+    tokens = (256 << 20) // (4 * dim * (heads + kv)) + 77
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    qkv = torch.randn((tokens, heads + 2 * kv, dim), generator=g, device="cuda").bfloat16()
+    q, k, v = qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:]
+    pos = torch.randint(-100, 70000, (tokens, 2), generator=g, device="cuda", dtype=torch.int32)
+    qw = normal(rng, (dim,), 0.2, 1.0, torch.float32) if norm else None
+    kw = normal(rng, (dim,), 0.2, 1.0, torch.float32) if norm else None
+    plan = nv.rotary_plan(rot, axes=(16, rot - 16))
+    args = dict(layout=layout, q_weight=qw, k_weight=kw)
+    before = v.clone()
+    # parts of it, which the cache holds: the kernel of the tests above
+    parts = [nv.rotary(a.contiguous(), p.contiguous(), plan, k=b.contiguous(), **args)
+             for a, b, p in zip(q.split(tokens // 3), k.split(tokens // 3), pos.split(tokens // 3))]
+    at = torch.cat([torch.arange(100), torch.arange(tokens - 100, tokens),
+                    torch.from_numpy(rng.integers(0, tokens, 300))]).cuda()
+    q0, k0 = q[at].unsqueeze(0), k[at].unsqueeze(0)
+    qo, ko = nv.rotary(q, pos, plan, k=k, out=q, k_out=k, **args)
+    check(qo[at].unsqueeze(0), q0, pos[at], plan, layout, qw)
+    check(ko[at].unsqueeze(0), k0, pos[at], plan, layout, kw)
+    assert torch.equal(qo, torch.cat([p[0] for p in parts])) and torch.equal(ko, torch.cat([p[1] for p in parts]))
+    assert torch.equal(v, before)
