@@ -161,3 +161,40 @@ def test_no_rows_with_their_workspace():
     assert nv.lora_add(**d, y_amax=amax, workspace=ws).shape == (0, 64) and amax.item() == 0
     with pytest.raises(nv.Nvfp4Error):
         nv.lora_add(**make(8, 5, 64, 64, 8, 1), workspace=ws)
+
+
+def rows_of(d, at):
+    """The same call on some of its rows."""
+    return dict(d, **{k: d[k][at].contiguous() for k in ("y", "x", "ids")})
+
+
+@pytest.mark.parametrize("kind", ["runs", "mixed"])
+@pytest.mark.parametrize("rank,epilogue", [(8, "none"), (16, "gelu"), (24, "gelu"), (32, "none")])
+def test_row_tiles_in_pairs(rank, epilogue, kind):
+    # 257 row tiles by enough columns that each compute unit has 32 pairs of a tile and
+    # 128 columns: two row tiles a wave in both kernels
+    units = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = 16 * units + 4
+    outer = 128 * (32 * units // (units + 1) + 1) + 8
+    rng = np.random.default_rng(rank)
+    if kind == "mixed":
+        ids = rng.integers(-1, 6, rows)
+    else:                           # runs that end inside a pair, idle pairs and tiles, ids of no adapter
+        cuts = np.sort(rng.choice(rows, 90, replace=False))
+        ids = rng.integers(-1, 5, 91)[np.searchsorted(cuts, np.arange(rows), side="right")]
+        ids[64:160] = -1
+        ids[192:208] = 9
+        ids[208:224] = 2
+    d = make(rank, rows, 72, outer, rank, 5, ids)
+    amax = torch.zeros(1, device="cuda")
+    got = nv.lora_add(**d, epilogue=epilogue, y_amax=amax, out=torch.empty_like(d["y"]))
+    at = np.concatenate([np.arange(0, 320, 3), np.arange(rows - 40, rows), rng.integers(0, rows, 60)])
+    at = torch.from_numpy(at).cuda()
+    check(got[at], rows_of(d, at), epilogue)
+    assert amax.item() == got.abs().max().item()
+    # rows in calls of their own, one row tile a wave: the same bits
+    for i in range(0, rows, 1000):
+        part = rows_of(d, torch.arange(i, min(i + 1000, rows), device="cuda"))
+        assert torch.equal(nv.lora_add(**part, epilogue=epilogue), got[i:i + 1000])
+    # in place
+    assert torch.equal(nv.lora_add(**d, epilogue=epilogue), got) and torch.equal(d["y"], got)
