@@ -291,3 +291,26 @@ def test_rows_of_minus_infinity_are_zeros_whatever_the_values(queries):
     for ws in ({}, {"workspace": None}):
         got = nv.cross_attention(q, k, v, **ws)
         assert torch.equal(got, torch.zeros_like(got))
+
+
+@pytest.mark.parametrize("dim", [64, 80, 128])
+@pytest.mark.parametrize("batch,queries,keys,heads,kv", [
+    (1, 300, 333, 11, 11), (3, 150, 333, 8, 4), (2, 129, 70, 27, 9),
+    (2, 1500, 130, 24, 24), (5, 601, 200, 12, 6)])         # and more units than workgroups run at once
+def test_heads_side_by_side_over_several_row_tiles(batch, queries, keys, heads, kv, dim):
+    # at least eight kv heads (one a chiplet, and some left over) with several row tiles each
+    rng = np.random.default_rng(dim + keys)
+    q, k, v = make(dim + queries, batch, queries, keys, heads, kv, dim)
+    lengths = torch.from_numpy(rng.integers(keys // 3, keys + 1, batch)).int().cuda()
+    lengths[0] = keys
+    mask = torch.from_numpy(rng.random((batch, keys)) < 0.8).cuda()
+    for kw in ({}, {"kv_lengths": lengths, "key_mask": mask}):
+        want = nv.cross_attention(q, k, v, workspace=None, **kw)
+        check(want, q, k, v, lengths=kw.get("kv_lengths"), mask=kw.get("key_mask"))
+        check(nv.cross_attention(q, k, v, **kw), q, k, v, lengths=kw.get("kv_lengths"), mask=kw.get("key_mask"))
+        # a head alone, where nothing lies side by side: the same bits
+        for b, h in ((0, 0), (batch - 1, heads - 1), (batch // 2, heads // 2)):
+            g = h // (heads // kv)
+            one = nv.cross_attention(q[b:b + 1, :, h:h + 1], k[b:b + 1, :, g:g + 1], v[b:b + 1, :, g:g + 1],
+                                     workspace=None, **{n: t[b:b + 1].contiguous() for n, t in kw.items()})
+            assert torch.equal(one, want[b:b + 1, :, h:h + 1])
