@@ -3,6 +3,8 @@ quantized linears, stage by stage against binary64 on the GPU's own inputs of
 each stage (so a code flipped at a rounding tie cannot propagate), captured in a
 HIP graph, and equal to the same calls made one by one."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -235,3 +237,35 @@ def test_text_keys_carry_no_rotary_factor(monkeypatch):
     # bounds as in the norm's own tests: 64 U32 of the row's largest term, and one rounding
     want = ob.normalise(f64(kv[:, :, 0]), "rms", 1e-6) * f64(block.k_norm)
     assert_within(block.k, want, UBF * np.abs(want) + 64 * U32 * np.abs(want).max(-1, keepdims=True), "keys")
+
+
+def adapted64(block, name, ids, x):
+    """A layer with adapters in binary64 on its NVFP4 operands and bf16 input, and the bound on
+    what precedes its epilogue: the product's output is rounded once, then the adapters are added
+    (their rank values rounded once more)."""
+    y, size = linear64(block, name)
+    depth = x.shape[1]
+    off = UBF * np.abs(y) + (depth + 8) * U32 * size
+    down, up, s = (f64(t) for t in block.lora[name])
+    i = ids.cpu().numpy()
+    full, more = ob.lora_add(y, f64(x), down, up, i, s)
+    rank = ob.lora_rank_size(f64(x), down, up, i, s)
+    off = (1 + UBF) * off + (UBF * rank + (depth + down.shape[1] + 32) * U32 * more) * 1.01
+    return full, off + 2 * U32 * np.abs(full)
+
+
+def test_mlp_with_adapters():
+    block, (temb, x, pos, ids), states, lengths = make()
+    block.encode(states, lengths)
+    block(temb, x, pos, ids)
+    h, u, d = block.h.view(-1, HID), block.out[UP], block.out[DOWN]
+    # both inputs are quantized with their producers' amax: the codes of their own
+    for name, z in ((UP, h), (DOWN, u)):
+        q = nv.quantize(z)
+        assert all(torch.equal(a, b) for a, b in zip(block.qbuf[name], q[:3]))
+    z, off = adapted64(block, UP, ids, h)
+    want = 0.5 * z * np.vectorize(math.erfc)(-z / math.sqrt(2))
+    off = 1.13 * off + 2e-5 * np.abs(want)            # GELU's slope and its approximation
+    assert_within(u, want, off + UBF * (np.abs(want) + off), "up")
+    y, off = adapted64(block, DOWN, ids, u)
+    assert_within(d, y, off + UBF * (np.abs(y) + off), "down")
