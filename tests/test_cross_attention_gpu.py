@@ -314,3 +314,13 @@ def test_heads_side_by_side_over_several_row_tiles(batch, queries, keys, heads, 
             one = nv.cross_attention(q[b:b + 1, :, h:h + 1], k[b:b + 1, :, g:g + 1], v[b:b + 1, :, g:g + 1],
                                      workspace=None, **{n: t[b:b + 1].contiguous() for n, t in kw.items()})
             assert torch.equal(one, want[b:b + 1, :, h:h + 1])
+
+
+@pytest.mark.parametrize("queries,heads,kv,dim", [(1, 40, 1, 64), (3, 40, 1, 128), (20, 7, 1, 128), (9, 66, 2, 40),
+                                                  (33, 13, 1, 64)])
+def test_many_heads_share_a_key_head(queries, heads, kv, dim):
+    # a group that is longer than a load's rows, shorter, and no divisor of them
+    q, k, v = make(heads, 2, queries, 300, heads, kv, dim)
+    wide = torch.from_numpy(np.random.default_rng(1).random((2, 390)) < 0.7).cuda()
+    for mask in (wide[:, 50:350], wide[:1, 7:307].expand(2, -1)):       # a part of a wider mask; one for all
+        check(nv.cross_attention(q, k, v, key_mask=mask), q, k, v, mask=mask)

@@ -228,3 +228,12 @@ def test_held_modulations_follow_the_batch_entry(channels, entries, stream, mod)
     assert torch.equal(r1, r[i:i + 1, :300]) and torch.equal(h1, h[i:i + 1, :300])
     r2, h2 = nv.gated_norm(**d, **kw, residual_out=d["x"], out=d["y"])
     assert torch.equal(r2, r) and torch.equal(h2, h)
+
+
+@pytest.mark.parametrize("tokens", [5, 2600])
+def test_one_modulation_for_all_entries(tokens):
+    d = make(21, 3, tokens, 1032)
+    for name in ("gate", "scale", "shift"):
+        d[name] = d[name][1:2].expand(3, -1)
+    r, h = nv.gated_norm(**d)
+    check(d, r, h)
