@@ -483,7 +483,8 @@ size_t dit_cross_attention_workspace_bytes(int64_t batch, int64_t queries, int64
  *   out[b, t, h] = sum_j w_j v[b, j, g],  w = softmax_j(scale q[b, t, h] . k[b, j, g])
  *
  * over the visible keys j of batch entry b, with g = h / (heads / kv_heads).  A
- * row without a visible key, or with scores of -infinity alone, is zeros.
+ * row without a visible key, or with scores of -infinity alone, is zeros; NaN and
+ * infinities in sight go through the formula.
  * Products and sums are binary32; the softmax weights are rounded to bf16 for
  * the product with v (a relative 2^-8 each, as the output's own rounding), their
  * sum is not.

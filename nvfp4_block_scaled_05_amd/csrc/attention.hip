@@ -366,8 +366,8 @@ __device__ __forceinline__ int seen_keys(const Attention& a, const Place& p) {
 // Work unit u: a row tile of a (batch, kv head).  Workgroups are dealt to the 8
 // XCDs in turn; eight heads run side by side, each on one XCD, whose L2 keeps its
 // keys, so entries of unequal lengths are spread over all of them.  (One
-// contiguous range of heads per XCD gives an XCD one batch entry: 237 us against
-// 190 for a CFG pair of 512 and 77 text states.)
+// contiguous range of heads per XCD gives an XCD one batch entry: 245 us against
+// 175 for a CFG pair of 512 and 77 text states.)
 __device__ __forceinline__ void place_unit(const Attention& a, Place& p, uint32_t u) {
   const uint32_t tiles = (uint32_t)a.row_tiles, heads = (uint32_t)a.batch * (uint32_t)a.kv_heads;
   const uint32_t full = heads / kXcds * kXcds;
@@ -437,16 +437,16 @@ struct RowStep {
 
 // Many query rows: the four waves of a workgroup have 32 rows each and share the
 // tiles of 64 keys, which the next turn's loads replace while this turn's are
-// used.  At 4096 queries and 4608 keys of 24 heads: 218 us, 1.06 PFLOP/s (the
-// matrix cores alone reach 1.68 on such data); a tile of 32 rows by 64 keys costs a SIMD
-// 1024 cycles of matrix products and about 950 of exponentials, sums and maxima, and
-// two waves a SIMD hide about half of the latter.  The rest is power: on zeros the
-// same instructions take a fifth less.  At 2 x 16384 queries of 77 and 512 keys: 164
-// us, 0.72 PFLOP/s and 2.5 TB/s.  Not faster, in turn with the same kernel: the
-// exponentials of one block of 32 keys under the scores of the next in one wave (235
-// us for 226), 64 rows a wave and the loads spread between the products (registers
-// spill), query rows fetched a unit ahead by workgroups that stay (they spill: 247
-// us for 178).
+// used.  At 4096 queries and 4608 keys of 24 heads: 218 to 260 us by box, at best 1.06
+// PFLOP/s (the matrix cores alone reach 1.68 on such data); a tile of 32 rows by 64
+// keys costs a SIMD 1024 cycles of matrix products and about 950 of exponentials, sums
+// and maxima, and two waves a SIMD hide about half of the latter.  The rest is power:
+// on zeros the same instructions take a fifth less.  At 2 x 16384 queries of 77 and 512
+// keys: 164 to 180 us, at best 0.72 PFLOP/s and 2.5 TB/s.  Not faster, in turn with the
+// same kernel: the exponentials of one block of 32 keys under the scores of the next in
+// one wave (235 us for 226), 64 rows a wave and the loads spread between the products
+// (registers spill), query rows fetched a unit ahead by workgroups that stay (they
+// spill: 247 us for 178).
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
   using A = Attend<DP, 2>;
@@ -469,8 +469,8 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
   u32x4 qrow[32 / kRowsPerLoad];
   {
     // Rows past the last read the first token's.  Queries and outputs pass through
-    // once and are streamed past the caches, which stay with the keys (164 us against
-    // 172 at 2 x 16384 queries of 77 and 512 keys, 36 against 37.5 at 4096 of 512).
+    // once and are streamed past the caches, which stay with the keys (175 us against
+    // 182 at 2 x 16384 queries of 77 and 512 keys, 43 against 47 at 4096 of 512).
     const uint16_t* q = a.q + p.batch * a.q_batch + (8 * piece < a.dim ? 8 * piece : 0);
     const int64_t none = (int64_t)p.kvh * a.group * a.q_head;
     RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad, a.q_token, a.q_head);
@@ -588,12 +588,16 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
 // keys and values, whole rows at a time into LDS of the wave's own: the next tile's
 // K is on its way as soon as this one's fragments are read, its V as soon as this
 // one's products are.  They are read once and streamed past the caches (134 MB of
-// keys and values: 32 us against 37, 537 MB 90 against 100; only a cache that the
-// call before this one read whole is 5 % slower, 31 against 29).  One token of 8
-// entries of 1 to 8192 keys, 24 heads over 8: 32 us and 5 for the join, 129 MB at 4.0
-// TB/s (with K fragments straight to registers, 32 bytes of 32 rows an access: 41
-// and 5; in tiles that the waves share, as above, 48 in all).  What is left is the first loads' latency, with nothing to
-// hide it, and the end, when workgroups run out one by one.
+// keys and values: 26 us against 29, 268 MB 45 against 51, 537 MB 87 against 98; only
+// what the call before left in the last-level cache is slower to read, 31 against
+// 27).  A key mask's bytes are loaded in the turn that looks for the next tile, behind
+// the tiles in flight, so their wait is for those too; the other waves run meanwhile:
+// a mask that keeps every key takes 46 us of 268 MB, 45 without, of 134 MB 27.7 and 26.
+// One token of 8 entries of 1 to 8192 keys, 24 heads over 8: 31 to 33 us and 5 for the
+// join, 129 MB at 4.0 TB/s (with K fragments straight to registers, 32 bytes of 32
+// rows an access: 41 and 5; in tiles that the waves share, as above, 48 in all).
+// What is left is the first loads' latency, with nothing to hide it, and the end, when
+// workgroups run out one by one.
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attention_few_kernel(Attention a) {
   using A = Attend<DP, 1>;
@@ -834,9 +838,9 @@ struct Plan {
 // workgroup t1 alone on its compute unit, t2 beside another (1.17 and 1.65 at a
 // padded head size of 128, 0.85 and 1.15 at 64); splits add a launch, about 5, and
 // their partial sums' way to memory and back at 4.6 TB/s.  Measured, whole against
-// split, 24 heads of 128: 512 queries of 512 keys 13 against 20 (2 ways), of 2304 44
-// against 32 (4 ways), of 4608 85 against 48; 1024 queries of 2304 47 against 49, of
-// 4608 88 against 82.
+// split, 24 heads of 128: 512 queries of 512 keys 14 against 21 (2 ways), of 2304 45
+// against 32 (4 ways), of 4608 84 against 47; 1024 queries of 2304 47 against 49 (2
+// ways), of 4608 89 against 80; 128 queries of 16384 keys 296 against 55 (16 ways).
 double split_cost(int64_t units, int64_t tiles, int dp, int64_t s, int64_t cus) {
   const double t1 = dp == 64 ? 0.85 : 1.17, t2 = dp == 64 ? 1.15 : 1.65;
   const int64_t full = units * s / (2 * cus), rest = units * s % (2 * cus);
@@ -872,6 +876,9 @@ Plan plan_for(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys, int d
   return {false, row_tiles, units, units * splits * 128, (int)splits, 0};
 }
 
+// Head sizes are padded to one of two: at 4096 queries and 4608 keys of 16 heads 64
+// takes 97 us, 128 150, and what lies between the time of 128 (72 to 96: 138 to 144,
+// 112 and 120: 155 to 159), though 80 has 0.63 of its products.
 int padded_dim(int64_t dim) { return dim <= 64 ? 64 : 128; }
 
 }  // namespace

@@ -12,8 +12,8 @@
 // of a tile of 16 rows goes through the whole tile, and each row keeps the result
 // of its own (a select, so what another adapter holds cannot reach it).
 //
-// Measured at 4608 rows, 3072 to 9216, rank 32, five requests: 15 us and 42 us, the
-// second at 4.0 TB/s of y and out; at 48 rows of 12 requests, 3072 to 12288, rank
+// Measured at 4608 rows, 3072 to 9216, rank 32, five requests: 16 us and 42 to 46 us,
+// the second at 3.7 to 4.0 TB/s of y and out; at 48 rows of 12 requests, 3072 to 12288, rank
 // 16, with GELU and amax: 4.2 us and 8.6 us, bound by the latency of their chains
 // of loads (ids, adapter, product).
 #include "device_common.hpp"
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(Lora a) {
 // long pieces (with a workgroup's waves on four row tiles of one column block
 // instead, sharing the adapter's weights in the cache: 5 % slower).  An access is
 // of 16 rows' 64 bytes, halves of cache lines that meet in the cache: streamed past
-// it, 4608 x 9216 take 49 us, not 42, and 16896 x 9216 in all 199, not 180.  The
+// it, 4608 x 9216 take 50 us, not 46, and 16896 x 9216 166, not 139.  The
 // weight is the MFMA's first operand, so a lane holds columns of one row; the
 // weight rows of a pair of MFMA tiles are dealt so that the 4 + 4 columns a lane
 // gets are 8 neighbours (16 bytes of y and out).
@@ -158,8 +158,9 @@ template <int RT, int MT>
 __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
   constexpr int KS = (RT + 1) / 2;             // 32-deep steps over the rank
   // column blocks that a tile of several adapters loads weights for at once: all of
-  // them where rows are few (8.7 us against 12.2 at 48 rows), one where the registers
-  // cost waves (42 us against 45 at 4608 rows)
+  // them where rows are few (8.5 us against 10.3 at 48 rows), one where the registers
+  // cost waves (46 us against 49 at 4608 rows, 139 against 152 at 16896).  Many rows of
+  // rank 33 to 64, which run one row tile, pay for it: 82 us against 75 at 4608.
   constexpr int NB = MT > 1 ? 1 : KS <= 2 ? kColBlocks : kColBlocks / KS;
   const int lane = threadIdx.x & 63;
   const int r = lane & 15, q = lane >> 4;
@@ -311,6 +312,9 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(Lora a) {
 
 __global__ void zero_lora_amax_kernel(uint32_t* p) { *p = 0u; }
 
+// Ranks are padded to one of these many 16-wide tiles; above two, both kernels run one
+// row tile at a time, so the adapters' weights come from the caches twice as often (4608
+// x 9216: rank 32 62 us, 40 88, 64 116, 128 180).
 int rank_tiles(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
 // Slices of `inner` in the first kernel, while the row tiles alone leave compute
@@ -328,15 +332,15 @@ hipError_t launch(const Lora& a, hipStream_t stream) {
   const int64_t tiles = (a.rows + kRowTile - 1) / kRowTile;
   // a workgroup of 12 waves fills a compute unit: two row tiles each (every weight
   // fragment then serves both) where that saves rounds over the compute units: at
-  // 4608 rows of 3072, rank 32, 144 workgroups take 15 us, 288 take 21
+  // 4608 rows of 3072, rank 32, 144 workgroups take 16 us, 288 take 22
   const int64_t units = compute_units();
   const int64_t one = (tiles + units - 1) / units, two = ((tiles + 1) / 2 + units - 1) / units;
   const int mt = RT <= 2 && 4 * two < 3 * one ? 2 : 1;
   const int groups = (a.slice + 32 * group_steps(RT, mt) - 1) / (32 * group_steps(RT, mt));
   const dim3 block(64 * (groups < kDownWaves ? groups : kDownWaves));
   // Few tiles: a workgroup for each adapter that a tile can have, those past its
-  // number leaving at once, so that no tile takes two one after another (15 us
-  // against 25 where 4 of 144 tiles have two adapters, 4.2 against 7.5 where 3
+  // number leaving at once, so that no tile takes two one after another (16 us
+  // against 26 where 4 of 144 tiles have two adapters, 4.0 against 8.5 where 3
   // tiles of 48 rows have four each).  Many: the tail of one such tile is small
   // beside the rounds.
   int64_t each = a.adapters < kRowTile * mt ? a.adapters : kRowTile * mt;
@@ -348,8 +352,8 @@ hipError_t launch(const Lora& a, hipStream_t stream) {
     lora_down_kernel<RT, 1><<<down, block, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // two row tiles a wave (the adapter's weights then serve both: 42 us against 45
-  // at 4608 x 9216, rank 32) where that still leaves every compute unit 16 waves
+  // two row tiles a wave (the adapter's weights then serve both: 46 us against 48
+  // at 4608 x 9216, rank 32, 139 against 161 at 16896 rows) where that still leaves every compute unit 16 waves
   const int64_t cols = (a.outer + kColBlock * kColBlocks - 1) / (kColBlock * kColBlocks);
   const int64_t cap = units * 64;
   const int up = RT <= 2 && tiles * cols >= 32 * units ? 2 : 1;

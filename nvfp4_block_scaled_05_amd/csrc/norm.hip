@@ -49,8 +49,9 @@ __device__ __forceinline__ Raw<uint16_t> load8(const uint16_t* p) {
   return {*reinterpret_cast<const u32x4*>(p)};
 }
 // x, y, r and h pass through once: they are streamed past the caches, which stay
-// with the vectors over channels (85 us against 90 at 16896 x 3072, before
-// modulations were held).
+// with the vectors over channels (76 us against 81 at 16896 x 3072, 135 against 147
+// at 6144 channels; with an fp32 stream it does not matter at 3072, 124 against 122,
+// and costs up to 8 % at 4608 and 5120).
 __device__ __forceinline__ Raw<uint16_t> take8(const uint16_t* p) {
   return {__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p))};
 }
@@ -124,8 +125,8 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&mine)[
 //
 // HOLD: gate, scale and shift (of type MT) stay in registers for as long as the batch
 // entry lasts.  Loaded within the row they come after the next row's loads, and
-// waiting for them is waiting for those: at 16896 x 3072 85 us against 77, with an
-// fp32 stream 151 against 123, with weights and a post-norm besides 175 against 141.
+// waiting for them is waiting for those: at 16896 x 3072 83 us against 76, with an
+// fp32 stream 156 against 124, with weights and a post-norm besides 188 against 145.
 // Two chunks a lane would take too many registers.
 template <class XT, class MT, bool HOLD, int CH, int LANES>
 __global__ __launch_bounds__(LANES > 0 ? 256 : 1024) void gated_norm_kernel(GatedNorm a) {
@@ -289,12 +290,18 @@ hipError_t launch_gated_norm(const GatedNorm& a, bool x_fp32, hipStream_t stream
   if (a.rows == 0) return hipSuccess;
   const int chunks = a.channels / 8;
   // One chunk a lane up to 8192 channels: more waves with less to hold each load
-  // more at once (at 16896 x 3072 two chunks a lane took 103 us, one 85).  Rows are
-  // spread evenly over the rounds.  Up to two rounds of 24 waves a compute unit (18:
-  // 94 us, 30, more than the registers hold: 116), nothing held: the first loads count
-  // (3063 x 1536, fp32 stream, all vectors: 13.2 us, 14.0 held).  Past that,
-  // modulations held and 20 waves (at 16896 x 3072 16 waves take 83 us, 20 77, 24 79),
-  // of an fp32 stream 16 (123 us, 18: 141).
+  // more at once (at 16896 x 3072, nothing held, two chunks a lane take 106 us, one
+  // 83).  Rows are spread evenly over the rounds.  Up to two rounds of 24 waves a
+  // compute unit nothing is held: the first loads count (3063 x 1536, fp32 stream, all
+  // vectors: 14.2 us, 15.3 held; at 16896 x 3072, nothing held, 18 waves take 89 us, 24
+  // 83, 30, more than the registers hold, 107).  Past that modulations are held, and a
+  // compute unit has the whole workgroups that 20 waves make, of an fp32 stream 16: at
+  // 3072 channels, 6 waves a workgroup, 3 and 2 (76 and 124 us; 2 and 4 of bf16 80 and
+  // 85, 3 of fp32 143).  From 5128 channels on (fp32: 4104) it is one workgroup, no
+  // slower than two held (16896 x 6144: 135 us against 149, fp32 241 both) and, but
+  // for 2 % of an fp32 stream, than nothing held (150, 237).  Above 8192 channels two
+  // chunks a lane and one workgroup of 16 waves: 4224 x 16384 110 us, 5.0 TB/s, 8448 x
+  // 8200, where one lane alone has a second chunk, 144 us, 3.9.
   const int lanes = chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : chunks <= 64 ? 64 : 0;
   const int waves = lanes ? 4 : chunks <= 1024 ? (chunks + 63) / 64 : 16;
   const int64_t turns = lanes ? (a.rows + 256 / lanes - 1) / (256 / lanes) : a.rows;

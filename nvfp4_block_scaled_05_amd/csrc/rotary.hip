@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(Rotary a) {
   const int partner = chunk + (upper ? -half_chunks : half_chunks);
   const int partner_lane = (threadIdx.x & 63) - chunk + partner;
   float wq[8], wk[8], pq[8], pk[8];              // the norms' weights of this lane's and its partner's elements
-  if (NORM) {                                    // through LDS: loaded from memory by every lane, 97 us for 85
+  if (NORM) {                                    // through LDS: loaded from memory by every lane, 106 us for 79
     for (int d = threadIdx.x; d < a.dim; d += kRotThreads) {
       weight[0][d] = a.q.weight ? a.q.weight[d] : 1.0f;
       weight[1][d] = a.k.weight ? a.k.weight[d] : 1.0f;
@@ -188,7 +188,7 @@ hipError_t launch_layout(const Rotary& a, int64_t grid, hipStream_t stream) {
 template <int LANES>
 hipError_t launch(const Rotary& a, int64_t grid, hipStream_t stream) {
   // what the last-level cache cannot hold is streamed past the others (16896 tokens
-  // of 48 heads of 128: 85 us against 91; 4608, which it holds: 26 against 23)
+  // of 48 heads of 128: 79 us against 86; 4608, which it holds: 27 against 22)
   const bool streaming = a.rows * (a.q.heads + a.k.heads) * a.dim * 4 > ((int64_t)256 << 20);
   return streaming ? launch_layout<LANES, true>(a, grid, stream) : launch_layout<LANES, false>(a, grid, stream);
 }
@@ -197,11 +197,12 @@ hipError_t launch(const Rotary& a, int64_t grid, hipStream_t stream) {
 
 hipError_t launch_rotary(Rotary a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  // tokens a workgroup takes: two (at 16896 tokens of 48 heads of 128, 1 takes 85 us,
-  // 2 81, 4 85, 8 96), more where a token's heads do not fill the workgroup four
-  // times over (53396 tokens of 6 heads of 96: 41 us, filled twice 47), as many as
-  // its table holds, and fewer while that would leave compute units without a
-  // workgroup
+  // tokens a workgroup takes: two (at 16896 tokens of 48 heads of 128, 1 takes 80 us,
+  // 2 79, 4 83, 8 95), more where a token's heads do not fill the workgroup four
+  // times over (53396 tokens of 6 heads of 96: 41 us, filled twice 49; without the
+  // norm 31, so what is above the 27 of their bytes is mostly its weights, fetched
+  // again by each workgroup), as many as its table holds, and fewer while that would
+  // leave compute units without a workgroup
   const int chunks = a.dim / 8, lanes = chunks <= 4 ? 4 : chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
   const int heads = a.q.heads + a.k.heads;
   int per = 4 * (kRotThreads / lanes) / heads;
