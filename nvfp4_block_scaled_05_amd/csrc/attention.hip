@@ -469,8 +469,8 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Attention a) {
   u32x4 qrow[32 / kRowsPerLoad];
   {
     // Rows past the last read the first token's.  Queries and outputs pass through
-    // once and are streamed past the caches, which stay with the keys (175 us against
-    // 182 at 2 x 16384 queries of 77 and 512 keys, 43 against 47 at 4096 of 512).
+    // once and are streamed past the caches, which stay with the keys (173 us against
+    // 180 at 2 x 16384 queries of 77 and 512 keys; no difference at 4096).
     const uint16_t* q = a.q + p.batch * a.q_batch + (8 * piece < a.dim ? 8 * piece : 0);
     const int64_t none = (int64_t)p.kvh * a.group * a.q_head;
     RowStep step(a, p, row0 + w.lane / kRowPieces, kRowsPerLoad, a.q_token, a.q_head);

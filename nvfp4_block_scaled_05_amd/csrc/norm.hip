@@ -301,7 +301,7 @@ hipError_t launch_gated_norm(const GatedNorm& a, bool x_fp32, hipStream_t stream
   // slower than two held (16896 x 6144: 135 us against 149, fp32 241 both) and, but
   // for 2 % of an fp32 stream, than nothing held (150, 237).  Above 8192 channels two
   // chunks a lane and one workgroup of 16 waves: 4224 x 16384 110 us, 5.0 TB/s, 8448 x
-  // 8200, where one lane alone has a second chunk, 144 us, 3.9.
+  // 8200, where one lane alone has a second chunk, 144 us, 3.8.
   const int lanes = chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : chunks <= 64 ? 64 : 0;
   const int waves = lanes ? 4 : chunks <= 1024 ? (chunks + 63) / 64 : 16;
   const int64_t turns = lanes ? (a.rows + 256 / lanes - 1) / (256 / lanes) : a.rows;

@@ -199,8 +199,8 @@ hipError_t launch_rotary(Rotary a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
   // tokens a workgroup takes: two (at 16896 tokens of 48 heads of 128, 1 takes 80 us,
   // 2 79, 4 83, 8 95), more where a token's heads do not fill the workgroup four
-  // times over (53396 tokens of 6 heads of 96: 41 us, filled twice 49; without the
-  // norm 31, so what is above the 27 of their bytes is mostly its weights, fetched
+  // times over (53396 tokens of 6 heads of 96: 41 to 45 us, filled twice 49 to 51;
+  // without the norm 31, so what is above the 27 of their bytes is mostly its weights, fetched
   // again by each workgroup), as many as its table holds, and fewer while that would
   // leave compute units without a workgroup
   const int chunks = a.dim / 8, lanes = chunks <= 4 ? 4 : chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
