@@ -437,7 +437,7 @@ struct RowStep {
 
 // Many query rows: the four waves of a workgroup have 32 rows each and share the
 // tiles of 64 keys, which the next turn's loads replace while this turn's are
-// used.  At 4096 queries and 4608 keys of 24 heads: 218 to 260 us by box, at best 1.06
+// used.  At 4096 queries and 4608 keys of 24 heads: 218 to 260 us by card, at best 1.06
 // PFLOP/s (the matrix cores alone reach 1.68 on such data); a tile of 32 rows by 64
 // keys costs a SIMD 1024 cycles of matrix products and about 950 of exponentials, sums
 // and maxima, and two waves a SIMD hide about half of the latter.  The rest is power:
