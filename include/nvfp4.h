@@ -551,6 +551,118 @@ int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const
                  int64_t outer, int64_t rank, int64_t adapters, int epilogue, void* out_bf16,
                  float* out_amax, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A key/value cache held in NVFP4, and the product for few rows that goes with
+ * it.  The conventions above hold.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * w4_gemm_weight_only -- few rows of bf16 activations, not quantized, times
+ * an NVFP4 weight:
+ *   Y[m,n] = bf16_rne( epi( sW * sum_k X[m,k] * W[n,k] * S[n,k/16] + bias[n] ) )
+ * fp32 accumulation, products exact before it.
+ *   x_bf16 [M, K], 16-byte aligned; w_codes [N, K/2], w_scales [N, K/16],
+ *   w_tensor_scale [1] as nvfp4_quantize wrote them (codes 8-byte aligned);
+ *   bias_bf16 optional [N]; y_bf16 [M, N], 8-byte aligned.
+ *   0 <= M < 2^22; 0 <= N < 2^27; 0 < K < 2^30, K % 16 == 0.
+ *   y_amax   optional device float, set to max |y| over the bf16 outputs (0 if
+ *            there are none; not finite if one is NaN).
+ * Made for up to 64 rows, over which the weight is read once; more rows read it
+ * once for each 64 (nvfp4_gemm is the one for those).  Deterministic.
+ */
+int w4_gemm_weight_only(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_scales,
+                           const float* w_tensor_scale, const void* bias_bf16, int64_t M, int64_t N,
+                           int64_t K, int epilogue, void* y_bf16, float* y_amax, void* stream);
+
+/*
+ * A cache: pages of tokens' keys and values, a page's tokens one after another
+ * for each head.
+ *   k_codes, v_codes    [pages, kv_heads, page_size, dim/2], 16-byte aligned.
+ *   k_scales, v_scales  [pages, kv_heads, page_size, dim/16], 2-byte aligned.
+ *   amax        device float [2]: the static amax of keys and of values, finite
+ *               and positive; they stay as they are while the cache is in use.
+ *   table       optional [batch, table_pages] int32: the pages of each entry's
+ *               positions in order; an entry outside [0, pages) is no page.
+ *               NULL (table_pages 0): entry b is page b.
+ *   page_size   a multiple of 16; with a table a power of two.
+ *   dim         a multiple of 16, at most 128.  0 < kv_heads <= 65536.
+ *   An entry's capacity, table_pages * page_size (page_size without a table),
+ *   is below 2^31 - 256; 0 < pages < 2^31.
+ * Every byte holds a value from the start if the scales are zeroed once.
+ */
+typedef struct {
+  void *k_codes, *k_scales, *v_codes, *v_scales;
+  const float* amax;
+  int64_t pages, page_size, kv_heads, dim;
+  const int32_t* table;
+  int64_t table_pages;
+} kv_cache;
+
+/*
+ * kv_cache_write -- quantize new tokens into the cache: token t of entry b
+ * becomes its position starts[b] + t, for t < counts[b].  The bytes are those of
+ * nvfp4_quantize on that head's row with the cache's amax.
+ *   k, v        [batch, tokens, kv_heads, dim] bf16.
+ *   starts      [batch] int32; counts optional [batch] int32 (NULL: all tokens).
+ *   dev_status  optional: 0, or NVFP4_ERR_NONFINITE if a written block holds an
+ *               infinity or NaN.  Such a block gets the scale byte 0x7F (NaN): it
+ *               reads back as NaN and makes the attention that sees it NaN.
+ * Positions outside the entry's capacity or on no page are dropped.  No two
+ * tokens of a call may have one place (two entries whose tables share the page
+ * that they write).  batch * tokens * kv_heads * dim / 16 is below 2^31.
+ */
+int kv_cache_write(const kv_cache* cache, const dit_heads* k, const dit_heads* v,
+                      int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
+                      int32_t* dev_status, void* stream);
+
+/*
+ * kv_cache_read -- the values that positions starts[b] + t, t < counts[b],
+ * hold, as nvfp4_dequantize gives them; zeros for other t, for positions outside
+ * the entry's capacity and for those on no page.
+ *   k_out, v_out  [batch, tokens, kv_heads, dim] bf16, written whole.
+ *   starts, counts  optional [batch] int32 (NULL: 0, all tokens).
+ */
+int kv_cache_read(const kv_cache* cache, const dit_heads* k_out, const dit_heads* v_out,
+                     int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
+                     void* stream);
+
+/* Workspace bytes with which kv_cache_attention spreads the keys of a call over
+ * the compute units; 0 if it would not (or for invalid sizes). */
+size_t kv_cache_attention_workspace_bytes(int64_t batch, int64_t queries, int64_t heads,
+                                             int64_t kv_heads, int64_t dim, int64_t capacity);
+
+/*
+ * kv_cache_attention -- attention over the cache:
+ *
+ *   out[b, t, h] = sum_j w_j v[b, j, g],  w = softmax_j(scale q[b, t, h] . k[b, j, g])
+ *
+ * over positions j < lengths[b], with g = h / (heads / kv_heads); with starts also
+ * j <= starts[b] + t (the causal order of queries that begin at that position).  A
+ * position on no page is not seen.  A row that sees nothing, or scores of -infinity
+ * alone, is zeros; NaN in sight goes through the formula, what is out of sight does
+ * not count, whatever it holds.
+ * Products and sums are binary32 over the values as they are held; the softmax
+ * weights are rounded to fp16 for the product with v (2^-11 relative), their sum is
+ * not.
+ *   q, out      [batch, queries, heads, dim] bf16; out overlaps no input.
+ *   lengths     [batch] int32 (taken within [0, capacity]); starts optional [batch]
+ *               int32.
+ *   heads       a positive multiple of kv_heads, at most 65536; batch * heads *
+ *               queries below 2^31, and in rows of 128 per kv head, each times the
+ *               capacity's tiles of 64 keys, below 2^31.  scale > 0, at least 2^-126.
+ *   workspace   optional, 256-byte aligned, contents on entry irrelevant, owned by
+ *               the call until it completes: with at least
+ *               kv_cache_attention_workspace_bytes bytes the keys of all entries
+ *               are dealt to the compute units in equal parts, whatever the lengths,
+ *               and joined by a second kernel in a fixed order; NULL or less: no
+ *               entry's keys are split.  Deterministic either way; the two differ in
+ *               the order of the additions.
+ */
+int kv_cache_attention(const kv_cache* cache, const dit_heads* q, const int32_t* lengths,
+                          const int32_t* starts, int64_t batch, int64_t queries, int64_t heads,
+                          float scale, const dit_heads* out, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,7 +22,9 @@ __all__ = ["Nvfp4Tensor", "Fp8Tensor", "Nvfp4Error", "load", "abi_version", "sta
            "gemm_quantized", "gemm_bf16", "layer_is_quantized", "quantize_weight", "linear",
            "fp8_quantize", "fp8_gemm", "fp8_gemm_workspace",
            "gated_norm", "RotaryPlan", "rotary_plan", "rotary",
-           "cross_attention", "cross_attention_workspace", "lora_add", "lora_workspace"]
+           "cross_attention", "cross_attention_workspace", "lora_add", "lora_workspace",
+           "gemm_weight_only", "KvCache", "kv_cache", "cache_write", "cache_read",
+           "cache_attention", "cache_attention_workspace"]
 
 
 _TORCH = None
@@ -303,6 +305,34 @@ def gemm_quantized(a, w, amax, bias=None, epilogue="none", out=None):
     return Nvfp4Tensor(codes, scales, ts, N)
 
 
+def gemm_weight_only(x, w, bias=None, epilogue="none", y_amax=None, out=None):
+    """Y = epi(sW * X @ W_hat^T + bias) in bf16: few rows of bf16 activations, not
+    quantized, times an NVFP4 weight (an ``Nvfp4Tensor``).
+
+    x: [rows, K].  Made for up to 64 rows (single tokens of many requests, the
+    rows of a timestep embedding), over which the weight is read once; ``gemm`` is
+    the one for many rows.  y_amax: optional one-element float32 device tensor, set
+    to max |Y| for ``quantize``.
+    """
+    torch = _torch()
+    M, K = _matrix(x, "x", torch.bfloat16)
+    N = _nvfp4(w, "w")
+    if w.cols != K:
+        raise ValueError(f"K mismatch: x has {K} columns, w {w.cols}")
+    epi = _epilogue(epilogue)
+    _opt(bias, "bias", torch.bfloat16, (N,))
+    _opt(y_amax, "y_amax", torch.float32)
+    _opt(out, "out", torch.bfloat16, (M, N))
+    dev = _device(x=x, **_parts(w, "w"), bias=bias, y_amax=y_amax, out=out)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _binding.check(load().w4_gemm_weight_only(_ptr(x), _ptr(w.codes), _ptr(w.scales),
+                                                 _ptr(w.tensor_scale), _ptr(bias), M, N, K, epi,
+                                                 _ptr(out), _ptr(y_amax), _stream()),
+                   "w4_gemm_weight_only")
+    return out
+
+
 def fp8_quantize(x, dev_status=None, out=None):
     """FP8 row-wise quantization of a 2-D bf16 tensor (one scale per row).
     Returns an ``Fp8Tensor``; ``out``: optional (codes, scales)."""
@@ -402,17 +432,24 @@ def quantize_weight(w):
     return quantize(w)
 
 
-def linear(x, weight, name, bias=None, epilogue="none", pattern=None, lora=None):
+def linear(x, weight, name, bias=None, epilogue="none", pattern=None, lora=None,
+           weight_only=False):
     """One linear layer as the patched model runs it: NVFP4 (quantize x, then
     the block-scaled GEMM against the pre-quantized ``weight``) when the layer
     predicate selects it, else the bf16 passthrough on the bf16 ``weight``.
+
+    ``weight_only``: an NVFP4 layer takes x as it is (``gemm_weight_only``, for few
+    rows) instead of quantizing it.
 
     ``lora``: optional (down, up, ids, scales), the adapters of the rows'
     requests (``lora_add``): added to the layer's output from the unquantized x,
     before the epilogue."""
     own = "none" if lora is not None else epilogue
     if layer_is_quantized(name, pattern):
-        y = gemm(quantize(x), weight, bias=bias, epilogue=own)
+        if weight_only:
+            y = gemm_weight_only(x, weight, bias=bias, epilogue=own)
+        else:
+            y = gemm(quantize(x), weight, bias=bias, epilogue=own)
     else:
         y = gemm_bf16(x, weight, bias=bias, epilogue=own)
     if lora is None:
@@ -424,3 +461,5 @@ def linear(x, weight, name, bias=None, epilogue="none", pattern=None, lora=None)
 # the operators between the linears use the checks above
 from .block_ops import (RotaryPlan, cross_attention, cross_attention_workspace,  # noqa: E402
                         gated_norm, lora_add, lora_workspace, rotary, rotary_plan)
+from .cache_ops import (KvCache, cache_attention, cache_attention_workspace,  # noqa: E402
+                        cache_read, cache_write, kv_cache)

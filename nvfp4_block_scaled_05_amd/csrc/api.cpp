@@ -94,6 +94,44 @@ bool bad_lora(int64_t rows, int64_t inner, int64_t outer, int64_t rank, int64_t 
   return rank <= 0 || rank % 8 != 0 || rank > 128 || adapters <= 0 || adapters >= kMaxDim;
 }
 
+// An kv_cache and how many entries it serves.
+bool bad_cache(const kv_cache& c, int64_t batch) {
+  if (c.pages <= 0 || bad_dim(c.pages) || c.page_size <= 0 || c.page_size % 16 != 0) return true;
+  if (c.kv_heads <= 0 || c.kv_heads > (1 << 16) || c.dim <= 0 || c.dim % 16 != 0 || c.dim > 128)
+    return true;
+  if (c.page_size > kMaxDim - 256 || c.table_pages < 0 || c.table_pages > kMaxDim) return true;
+  if (!c.table) return batch > c.pages;
+  return (c.page_size & (c.page_size - 1)) != 0 || c.table_pages * c.page_size >= kMaxDim - 256;
+}
+bool null_cache(const kv_cache& c) {
+  return !c.k_codes || !c.k_scales || !c.v_codes || !c.v_scales || !c.amax;
+}
+bool misaligned_cache(const kv_cache& c) {
+  return !aligned(c.k_codes, 16) || !aligned(c.v_codes, 16) || !aligned(c.k_scales, 2) ||
+         !aligned(c.v_scales, 2) || !aligned(c.amax, 4) || !aligned(c.table, 4);
+}
+nvfp4::Cache cache_of(const kv_cache& c) {
+  int shift = 0;
+  while (c.table && ((int64_t)1 << shift) < c.page_size) ++shift;
+  return {static_cast<uint8_t*>(c.k_codes), static_cast<uint8_t*>(c.k_scales),
+          static_cast<uint8_t*>(c.v_codes), static_cast<uint8_t*>(c.v_scales), c.amax, c.table,
+          c.pages, c.table ? c.table_pages : 0, c.table ? c.table_pages * c.page_size : c.page_size,
+          (int)c.page_size, shift, (int)c.kv_heads, (int)c.dim};
+}
+
+// Sizes kv_cache_attention does not take (rows, and the tiles of all units, are
+// counted in 32 bits).
+bool bad_cache_attention(int64_t batch, int64_t queries, int64_t heads, int64_t kv_heads,
+                         int64_t dim, int64_t capacity) {
+  if (bad_dim(batch) || bad_dim(queries) || capacity < 0 || capacity > kMaxDim - 256) return true;
+  if (heads <= 0 || heads > (1 << 16) || kv_heads <= 0 || kv_heads > heads || heads % kv_heads != 0)
+    return true;
+  if (dim <= 0 || dim % 16 != 0 || dim > 128) return true;
+  if (batch * heads >= kMaxDim || (queries > 0 && batch * heads >= kMaxDim / queries)) return true;
+  const int64_t units = batch * kv_heads * ((queries * (heads / kv_heads) + 127) / 128);
+  return units > (1 << 23) || (units > 0 && (capacity + 63) / 64 + 1 >= kMaxDim / units);
+}
+
 // Positive, finite and not subnormal (the kernels' reciprocal square root takes a
 // subnormal for zero).
 bool finite_positive(float v) { return v >= FLT_MIN && v <= FLT_MAX; }
@@ -530,6 +568,122 @@ int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const
   a.out = static_cast<uint16_t*>(out_bf16);
   a.amax = reinterpret_cast<uint32_t*>(out_amax);
   return hip_status(nvfp4::launch_lora(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int w4_gemm_weight_only(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_scales,
+                           const float* w_tensor_scale, const void* bias_bf16, int64_t M, int64_t N,
+                           int64_t K, int epilogue, void* y_bf16, float* y_amax, void* stream) {
+  if (bad_dim(M) || bad_dim(N) || bad_dim(K)) return NVFP4_ERR_SHAPE;
+  const bool empty = M == 0 || N == 0;
+  if (!empty && (!x_bf16 || !w_codes || !w_scales || !w_tensor_scale || !y_bf16))
+    return NVFP4_ERR_NULL;
+  if (K == 0 || K % 16 != 0 || K >= (1 << 30) || M >= (1 << 22) || N >= (1 << 27))
+    return NVFP4_ERR_SHAPE;
+  if (!aligned(x_bf16, 16) || !aligned(w_codes, 8) || !aligned(w_tensor_scale, 4) ||
+      !aligned(bias_bf16, 2) || !aligned(y_bf16, 8) || !aligned(y_amax, 4))
+    return NVFP4_ERR_ALIGN;
+  if (epilogue != NVFP4_EPI_NONE && epilogue != NVFP4_EPI_GELU) return NVFP4_ERR_ARG;
+  int st = check_device();
+  if (st != NVFP4_OK) return st;
+  const nvfp4::WeightOnly a{static_cast<const uint16_t*>(x_bf16), w_codes, w_scales, w_tensor_scale,
+                            static_cast<const uint16_t*>(bias_bf16), M, (int)N, (int)K, epilogue,
+                            static_cast<uint16_t*>(y_bf16), reinterpret_cast<uint32_t*>(y_amax)};
+  return hip_status(nvfp4::launch_weight_only(a, static_cast<hipStream_t>(stream)));
+}
+
+int kv_cache_write(const kv_cache* cache, const dit_heads* k, const dit_heads* v,
+                      int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
+                      int32_t* dev_status, void* stream) {
+  if (bad_dim(batch) || bad_dim(tokens)) return NVFP4_ERR_SHAPE;
+  const bool empty = batch == 0 || tokens == 0;
+  if (!cache || !k || !v) return NVFP4_ERR_NULL;
+  if (!empty && (null_cache(*cache) || !k->data || !v->data || !starts)) return NVFP4_ERR_NULL;
+  if (bad_cache(*cache, batch) || bad_heads(*k) || bad_heads(*v)) return NVFP4_ERR_SHAPE;
+  if (!empty && batch * cache->kv_heads >= kMaxDim / tokens / (cache->dim / 16)) return NVFP4_ERR_SHAPE;
+  if (misaligned_cache(*cache) || !aligned(k->data, 16) || !aligned(v->data, 16) ||
+      !aligned(starts, 4) || !aligned(counts, 4) || !aligned(dev_status, 4))
+    return NVFP4_ERR_ALIGN;
+  int st = check_device();
+  if (st != NVFP4_OK) return st;
+  nvfp4::CacheCopy a{};
+  a.c = cache_of(*cache);
+  a.k = static_cast<const uint16_t*>(k->data);
+  a.v = static_cast<const uint16_t*>(v->data);
+  a.k_batch = k->batch_stride, a.k_token = k->token_stride, a.k_head = k->head_stride;
+  a.v_batch = v->batch_stride, a.v_token = v->token_stride, a.v_head = v->head_stride;
+  a.starts = starts;
+  a.counts = counts;
+  a.status = dev_status;
+  a.batch = batch;
+  a.tokens = tokens;
+  return hip_status(nvfp4::launch_cache_copy(a, true, static_cast<hipStream_t>(stream)));
+}
+
+int kv_cache_read(const kv_cache* cache, const dit_heads* k_out, const dit_heads* v_out,
+                     int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
+                     void* stream) {
+  if (bad_dim(batch) || bad_dim(tokens)) return NVFP4_ERR_SHAPE;
+  const bool empty = batch == 0 || tokens == 0;
+  if (!cache || !k_out || !v_out) return NVFP4_ERR_NULL;
+  if (!empty && (null_cache(*cache) || !k_out->data || !v_out->data)) return NVFP4_ERR_NULL;
+  if (bad_cache(*cache, batch) || bad_heads(*k_out) || bad_heads(*v_out)) return NVFP4_ERR_SHAPE;
+  if (!empty && batch * cache->kv_heads >= kMaxDim / tokens / (cache->dim / 16)) return NVFP4_ERR_SHAPE;
+  if (misaligned_cache(*cache) || !aligned(k_out->data, 16) || !aligned(v_out->data, 16) ||
+      !aligned(starts, 4) || !aligned(counts, 4))
+    return NVFP4_ERR_ALIGN;
+  int st = check_device();
+  if (st != NVFP4_OK) return st;
+  nvfp4::CacheCopy a{};
+  a.c = cache_of(*cache);
+  a.k_out = static_cast<uint16_t*>(k_out->data);
+  a.v_out = static_cast<uint16_t*>(v_out->data);
+  a.k_batch = k_out->batch_stride, a.k_token = k_out->token_stride, a.k_head = k_out->head_stride;
+  a.v_batch = v_out->batch_stride, a.v_token = v_out->token_stride, a.v_head = v_out->head_stride;
+  a.starts = starts;
+  a.counts = counts;
+  a.batch = batch;
+  a.tokens = tokens;
+  return hip_status(nvfp4::launch_cache_copy(a, false, static_cast<hipStream_t>(stream)));
+}
+
+size_t kv_cache_attention_workspace_bytes(int64_t batch, int64_t queries, int64_t heads,
+                                             int64_t kv_heads, int64_t dim, int64_t capacity) {
+  if (bad_cache_attention(batch, queries, heads, kv_heads, dim, capacity)) return 0;
+  return nvfp4::cache_attention_workspace_bytes(batch, queries, heads, kv_heads, dim, capacity);
+}
+
+int kv_cache_attention(const kv_cache* cache, const dit_heads* q, const int32_t* lengths,
+                          const int32_t* starts, int64_t batch, int64_t queries, int64_t heads,
+                          float scale, const dit_heads* out, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (bad_dim(batch) || bad_dim(queries)) return NVFP4_ERR_SHAPE;
+  const bool empty = batch == 0 || queries == 0;
+  if (!cache || !q || !out) return NVFP4_ERR_NULL;
+  if (!empty && (null_cache(*cache) || !q->data || !out->data || !lengths)) return NVFP4_ERR_NULL;
+  if (bad_cache(*cache, batch) || bad_heads(*q) || bad_heads(*out)) return NVFP4_ERR_SHAPE;
+  nvfp4::CacheAttention a{};
+  a.c = cache_of(*cache);
+  if (bad_cache_attention(batch, queries, heads, cache->kv_heads, cache->dim, a.c.capacity))
+    return NVFP4_ERR_SHAPE;
+  if (misaligned_cache(*cache) || !aligned(q->data, 16) || !aligned(out->data, 16) ||
+      !aligned(lengths, 4) || !aligned(starts, 4) || !aligned(workspace, 256))
+    return NVFP4_ERR_ALIGN;
+  if (!finite_positive(scale)) return NVFP4_ERR_ARG;
+  int st = check_device();
+  if (st != NVFP4_OK) return st;
+  if (empty) return NVFP4_OK;
+  a.q = static_cast<const uint16_t*>(q->data);
+  a.out = static_cast<uint16_t*>(out->data);
+  a.q_batch = q->batch_stride, a.q_token = q->token_stride, a.q_head = q->head_stride;
+  a.o_batch = out->batch_stride, a.o_token = out->token_stride, a.o_head = out->head_stride;
+  a.lengths = lengths;
+  a.starts = starts;
+  a.batch = (int)batch;
+  a.queries = (int)queries;
+  a.group = (int)(heads / cache->kv_heads);
+  a.scale = scale;
+  return hip_status(nvfp4::launch_cache_attention(a, workspace, workspace ? workspace_bytes : 0,
+                                                  static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

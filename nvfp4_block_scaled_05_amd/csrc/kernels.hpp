@@ -151,4 +151,68 @@ struct Lora {
 size_t lora_workspace_bytes(int64_t rows, int64_t inner, int64_t rank);
 hipError_t launch_lora(Lora a, void* workspace, hipStream_t stream);
 
+// An NVFP4 key/value cache (kv_cache), checked.
+struct Cache {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;   // [pages][kv_heads][page_size][dim / 2 or / 16]
+  const float* amax;             // [2]: of keys, of values
+  const int32_t* table;          // [batch][table_pages], or null: entry b is page b
+  int64_t pages, table_pages;
+  int64_t capacity;              // positions of an entry
+  int page_size, page_shift;     // page_size = 1 << page_shift with a table
+  int kv_heads, dim;
+};
+// Division by a number that the launch knows (cache.hpp).
+struct Divisor {
+  uint32_t magic, shift;
+};
+struct CacheCopy {
+  Cache c;
+  const uint16_t *k, *v;         // what is written, or
+  uint16_t *k_out, *v_out;       // where what is read goes
+  int64_t k_batch, k_token, k_head, v_batch, v_token, v_head;
+  const int32_t *starts, *counts;     // [batch], or null: 0, all tokens
+  int32_t* status;
+  int64_t batch, tokens;
+  // filled in by the launch
+  uint32_t blocks, total;        // of a row, of the call (fewer than 2^31)
+  Divisor by_blocks, by_tokens, by_heads;
+};
+hipError_t launch_cache_copy(CacheCopy a, bool write, hipStream_t stream);
+
+struct CacheAttention {
+  Cache c;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t q_batch, q_token, q_head, o_batch, o_token, o_head;
+  const int32_t* lengths;        // [batch]: keys that an entry holds
+  const int32_t* starts;         // [batch]: position of its first query; null: no causal order
+  int batch, queries, group;     // group: query heads per kv head
+  float scale;
+  // filled in by the launch
+  int rows, row_tiles;           // query rows of a kv head, and their tiles
+  int slot_rows;                 // rows of a slot of partial sums
+  int workers, least;            // workgroups over the keys of all units, tiles each takes at least; 0: one a unit
+  float* part;                   // [slot][row][padded dim]
+  float2* stats;                 // [slot][row]: maximum, sum
+};
+// Workspace bytes with which launch_cache_attention spreads the keys over the compute
+// units (0: it does not).
+size_t cache_attention_workspace_bytes(int64_t batch, int64_t queries, int64_t heads, int64_t kv_heads,
+                                       int64_t dim, int64_t capacity);
+hipError_t launch_cache_attention(CacheAttention a, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+
+// Y = epi(s_w * X W_hat^T + bias), X bf16 as it is.
+struct WeightOnly {
+  const uint16_t* x;             // [M, K]
+  const uint8_t *codes, *scales; // [N, K / 2], [N, K / 16]
+  const float* tensor_scale;
+  const uint16_t* bias;          // [N] or null
+  int64_t M;
+  int N, K, epilogue;
+  uint16_t* y;
+  uint32_t* amax;                // or null
+};
+hipError_t launch_weight_only(WeightOnly a, hipStream_t stream);
+
 }  // namespace nvfp4
