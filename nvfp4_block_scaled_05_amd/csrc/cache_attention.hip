@@ -159,15 +159,18 @@ __device__ __forceinline__ float rows_sum(float v) {
 
 // ------------------------------------------------------------------- few query rows
 //
-// A wave has RT tiles of 16 query rows and steps of 32 keys, two 16-key blocks T.  With
-// 16x16x32 products S^T = K Q^T, O^T += V^T P^T, and lane = 16 g + m:
-//   K operand   key 16 T + 4 (m % 4) + m / 4, elements g D / 4 ...: one load a block
+// A wave has RT tiles of 16 query rows and steps of 32 keys, two 16-key blocks T, in a
+// ring of LDS of its own: kStages - 1 steps are on their way while one is used, straight
+// from memory to LDS, so the bytes in flight take no registers.  With 16x16x32 products
+// S^T = K Q^T, O^T += V^T P^T, and lane = 16 g + m:
+//   K operand   key 16 T + 4 (m % 4) + m / 4, elements g D / 4 ...
 //   scores      row m, keys 16 T + 4 r + g, r = 0..3
 //   P operand   the same, as it comes
-//   V operand   columns m D / 16 ..., of those keys: a load for each T, r, of four
-//               neighbouring rows; pairs of keys are zipped nibble by nibble before
-//               the conversion, which then gives pairs along the keys
+//   V operand   columns m D / 16 ..., of those keys; pairs of keys are zipped nibble by
+//               nibble before the conversion, which then gives pairs along the keys
 // so nothing is exchanged between lanes.
+constexpr int kStages = 4;
+
 template <int D>
 struct Codes;
 template <>
@@ -180,6 +183,17 @@ struct Codes<64> {
   u32x2 k[2];
   uint32_t ks[2], v[2][4], vs[2][4];
 };
+
+// Straight into LDS, past the caches: 16 or 4 bytes of each lane to `lds` + lane * BYTES.
+template <int BYTES>
+__device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* lds) {
+  auto* to = (__attribute__((address_space(3))) void*)lds;
+  auto* at = (__attribute__((address_space(1))) void*)const_cast<uint8_t*>(from);
+  if constexpr (BYTES == 16)
+    __builtin_amdgcn_global_load_lds(at, to, 16, 0, 2);                       // 2: nt
+  else
+    __builtin_amdgcn_global_load_lds(at, to, 4, 0, 2);
+}
 
 template <int D, bool EXACT, int RT>
 struct FewRows {
@@ -194,6 +208,10 @@ struct FewRows {
   int lane, g, m;
   int code_bytes, scale_bytes;                 // of a token's row
   bool live_k[2], live_v;                      // this lane's blocks are within the head size
+  // of a stage: K's rows of D / 2 bytes, V's, K's scales (128 bytes a 16-key block), V's
+  static constexpr int kV = 16 * D, kKs = 32 * D, kVs = kKs + 256, kStage = kKs + 512;
+  static constexpr int kLoads = (EXACT ? 2 * (D / 64) : 2 * (D / 16)) + 2;       // of a stage
+  uint32_t at_k, at_v, at_ks, at_vs[EXACT ? 1 : 4];                              // this lane's reads in a stage
 
   __device__ __forceinline__ void start(const CacheAttention& a) {
     lane = threadIdx.x & 63;
@@ -204,6 +222,15 @@ struct FewRows {
 #pragma unroll
     for (int i = 0; i < 2; ++i) live_k[i] = EXACT || (D / 64) * g + i < scale_bytes;
     live_v = EXACT || (D / 32) * m < code_bytes;
+    const int key = 4 * (m & 3) + (m >> 2);
+    // (16-byte pieces of K's rows are permuted by XOR, so that the reads of 8 lanes spread
+    // over the banks)
+    at_k = (uint32_t)(key * (D / 2) + (D == 128 && EXACT ? (g ^ (m & 3)) << 4 : (D / 8) * g));
+    at_v = (uint32_t)(kV + g * (D / 2) + (D / 32) * m);
+    at_ks = (uint32_t)(kKs + key * scale_bytes + min((D / 64) * g, scale_bytes - 1));
+    const int block = min(m >> (D == 128 ? 1 : 2), scale_bytes - 1);
+#pragma unroll
+    for (int r = 0; r < (EXACT ? 1 : 4); ++r) at_vs[r] = (uint32_t)(kVs + (4 * r + g) * scale_bytes + block);
   }
 
   // The rows of a unit from `row0` on; rows past the last are the last.
@@ -237,63 +264,118 @@ struct FewRows {
     }
   }
 
-  // The codes of one 16-key block T: keys past `room` are taken as that one.
-  __device__ __forceinline__ void load(const Cache& c, int64_t row, int room, int T, Codes<D>& x) const {
-    const uint8_t* kc = c.k_codes + row * code_bytes;
-    const uint8_t* ks = c.k_scales + row * scale_bytes;
-    const uint8_t* vc = c.v_codes + row * code_bytes;
-    const uint8_t* vs = c.v_scales + row * scale_bytes;
-    const int key = min(4 * (m & 3) + (m >> 2), room);
-    {
-      const uint8_t* at = kc + (uint32_t)(key * code_bytes + (D / 8) * g);
-      const uint8_t* sc = ks + (uint32_t)(key * scale_bytes + (D / 64) * g);
-      if constexpr (D == 128) {
-        if constexpr (EXACT) {
-          x.k[T] = *reinterpret_cast<const u32x4*>(at);
-          x.ks[T] = *reinterpret_cast<const uint16_t*>(sc);
-        } else {
-          u32x2 lo = {}, hi = {};
-          uint32_t s0 = 0, s1 = 0;
-          if (live_k[0]) {
-            lo = *reinterpret_cast<const u32x2*>(at);
-            s0 = sc[0];
-          }
-          if (live_k[1]) {
-            hi = *reinterpret_cast<const u32x2*>(at + 8);
-            s1 = sc[1];
-          }
-          x.k[T] = u32x4{lo.x, lo.y, hi.x, hi.y};
-          x.ks[T] = s0 | s1 << 8;
-        }
-      } else {
-        x.k[T] = u32x2{};
-        x.ks[T] = 0;
-        if (live_k[0]) {
-          x.k[T] = *reinterpret_cast<const u32x2*>(at);
-          x.ks[T] = sc[0];
-        }
-      }
-    }
+  // The 16-key blocks whose rows begin at row[0] and row[1] (of a head's tokens in pages),
+  // on their way to a stage.  Whole blocks: they lie in the page, whatever the length.
+  __device__ __forceinline__ void load(const Cache& c, const int64_t (&row)[2], uint8_t* stage) const {
+    const auto codes = [&](const uint8_t* base, uint8_t* to, bool swizzle) {
+      const uint8_t* first[2] = {base + row[0] * code_bytes, base + row[1] * code_bytes};
+      if constexpr (EXACT && D == 128) {
+        const int r = lane >> 2, piece = (lane & 3) ^ (swizzle ? (r >> 2) & 3 : 0);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = min(4 * r + g, room);
-      x.v[T][r] = x.vs[T][r] = 0;
-      if (live_v) {
-        const uint8_t* at = vc + (uint32_t)(t * code_bytes + (D / 32) * m);
-        if constexpr (D == 128)
-          x.v[T][r] = *reinterpret_cast<const uint32_t*>(at);
-        else
-          x.v[T][r] = *reinterpret_cast<const uint16_t*>(at);
-        x.vs[T][r] = vs[(uint32_t)(t * scale_bytes + (m >> (D == 128 ? 1 : 2)))];
+        for (int T = 0; T < 2; ++T) to_lds<16>(first[T] + (uint32_t)(r * 64 + piece * 16), to + T * 1024);
+      } else if constexpr (EXACT) {
+        to_lds<16>((lane < 32 ? first[0] : first[1]) + (uint32_t)((lane & 31) * 16), to);
+      } else {
+        constexpr int kWords = D / 8;          // of a row of D
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int n = i * 64 + lane, token = n / kWords, word = n % kWords;
+          to_lds<4>(first[i >= D / 32] + (uint32_t)((token & 15) * code_bytes + (4 * word < code_bytes ? 4 * word : 0)),
+                    to + i * 256);
+        }
       }
+    };
+    const auto scales = [&](const uint8_t* base, uint8_t* to) {
+      const uint8_t* first = base + (lane < 32 ? row[0] : row[1]) * scale_bytes;
+      const int word = lane & 31;
+      to_lds<4>(first + (uint32_t)(word < 4 * scale_bytes ? 4 * word : 0), to);
+    };
+    codes(c.k_codes, stage, true);
+    scales(c.k_scales, stage + kKs);
+    codes(c.v_codes, stage + kV, false);
+    scales(c.v_scales, stage + kVs);
+  }
+
+  // This lane's K, or V, of a stage, waited for (the compiler sees no LDS read here, and
+  // puts no wait of its own for all that is on its way before it).
+  __device__ __forceinline__ void read_k(uint32_t stage, Codes<D>& x) const {
+    const uint32_t k = stage + at_k, s = stage + at_ks;
+    if constexpr (EXACT && D == 128) {
+      asm volatile(
+          "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:1024\n\t"
+          "ds_read_u16 %2, %5\n\tds_read_u16 %3, %5 offset:128\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x.k[0]), "=&v"(x.k[1]), "=&v"(x.ks[0]), "=&v"(x.ks[1])
+          : "v"(k), "v"(s)
+          : "memory");
+    } else if constexpr (D == 128) {
+      uint32_t s0, s1;
+      asm volatile(
+          "ds_read_b128 %0, %6\n\tds_read_b128 %1, %6 offset:1024\n\t"
+          "ds_read_u8 %2, %7\n\tds_read_u8 %3, %7 offset:128\n\t"
+          "ds_read_u8 %4, %7 offset:1\n\tds_read_u8 %5, %7 offset:129\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x.k[0]), "=&v"(x.k[1]), "=&v"(x.ks[0]), "=&v"(x.ks[1]), "=&v"(s0), "=&v"(s1)
+          : "v"(k), "v"(s)
+          : "memory");
+      x.ks[0] = (live_k[0] ? x.ks[0] : 0u) | (live_k[1] ? s0 << 8 : 0u);
+      x.ks[1] = (live_k[0] ? x.ks[1] : 0u) | (live_k[1] ? s1 << 8 : 0u);
+    } else {
+      asm volatile(
+          "ds_read_b64 %0, %4\n\tds_read_b64 %1, %4 offset:512\n\t"
+          "ds_read_u8 %2, %5\n\tds_read_u8 %3, %5 offset:128\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x.k[0]), "=&v"(x.k[1]), "=&v"(x.ks[0]), "=&v"(x.ks[1])
+          : "v"(k), "v"(s)
+          : "memory");
+      if (!EXACT && !live_k[0]) x.ks[0] = x.ks[1] = 0;
+    }
+  }
+  __device__ __forceinline__ void read_v(uint32_t stage, Codes<D>& x) const {
+    const uint32_t v = stage + at_v;
+    uint32_t s[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r] = stage + (EXACT ? at_vs[0] + 4 * r * (D / 16) : at_vs[EXACT ? 0 : r]);
+    if constexpr (D == 128)
+      asm volatile(
+          "ds_read_b32 %0, %16\n\tds_read_b32 %1, %16 offset:256\n\t"
+          "ds_read_b32 %2, %16 offset:512\n\tds_read_b32 %3, %16 offset:768\n\t"
+          "ds_read_b32 %4, %16 offset:1024\n\tds_read_b32 %5, %16 offset:1280\n\t"
+          "ds_read_b32 %6, %16 offset:1536\n\tds_read_b32 %7, %16 offset:1792\n\t"
+          "ds_read_u8 %8, %17\n\tds_read_u8 %9, %18\n\tds_read_u8 %10, %19\n\tds_read_u8 %11, %20\n\t"
+          "ds_read_u8 %12, %17 offset:128\n\tds_read_u8 %13, %18 offset:128\n\t"
+          "ds_read_u8 %14, %19 offset:128\n\tds_read_u8 %15, %20 offset:128\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x.v[0][0]), "=&v"(x.v[0][1]), "=&v"(x.v[0][2]), "=&v"(x.v[0][3]), "=&v"(x.v[1][0]),
+            "=&v"(x.v[1][1]), "=&v"(x.v[1][2]), "=&v"(x.v[1][3]), "=&v"(x.vs[0][0]), "=&v"(x.vs[0][1]),
+            "=&v"(x.vs[0][2]), "=&v"(x.vs[0][3]), "=&v"(x.vs[1][0]), "=&v"(x.vs[1][1]), "=&v"(x.vs[1][2]),
+            "=&v"(x.vs[1][3])
+          : "v"(v), "v"(s[0]), "v"(s[1]), "v"(s[2]), "v"(s[3])
+          : "memory");
+    else
+      asm volatile(
+          "ds_read_u16 %0, %16\n\tds_read_u16 %1, %16 offset:128\n\t"
+          "ds_read_u16 %2, %16 offset:256\n\tds_read_u16 %3, %16 offset:384\n\t"
+          "ds_read_u16 %4, %16 offset:512\n\tds_read_u16 %5, %16 offset:640\n\t"
+          "ds_read_u16 %6, %16 offset:768\n\tds_read_u16 %7, %16 offset:896\n\t"
+          "ds_read_u8 %8, %17\n\tds_read_u8 %9, %18\n\tds_read_u8 %10, %19\n\tds_read_u8 %11, %20\n\t"
+          "ds_read_u8 %12, %17 offset:128\n\tds_read_u8 %13, %18 offset:128\n\t"
+          "ds_read_u8 %14, %19 offset:128\n\tds_read_u8 %15, %20 offset:128\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x.v[0][0]), "=&v"(x.v[0][1]), "=&v"(x.v[0][2]), "=&v"(x.v[0][3]), "=&v"(x.v[1][0]),
+            "=&v"(x.v[1][1]), "=&v"(x.v[1][2]), "=&v"(x.v[1][3]), "=&v"(x.vs[0][0]), "=&v"(x.vs[0][1]),
+            "=&v"(x.vs[0][2]), "=&v"(x.vs[0][3]), "=&v"(x.vs[1][0]), "=&v"(x.vs[1][1]), "=&v"(x.vs[1][2]),
+            "=&v"(x.vs[1][3])
+          : "v"(v), "v"(s[0]), "v"(s[1]), "v"(s[2]), "v"(s[3])
+          : "memory");
+    if (!EXACT && !live_v) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x.vs[i / 4][i % 4] = 0;
     }
   }
 
   // One step of 32 keys from `first` on.  `blocks`: bit T, the 16-key block lies on a
   // page (if not, its codes are those of some other and count nowhere).  `all`: every
   // row sees every key.
-  __device__ __forceinline__ void step(Codes<D>& x, int first, int blocks, bool all) {
+  __device__ __forceinline__ void step(uint32_t stage, int first, int blocks, bool all) {
     f32x4 s[RT][2];
+    Codes<D> x;
+    read_k(stage, x);
 #pragma unroll
     for (int T = 0; T < 2; ++T) {
       const f16x2 sc = e4m3_pair_to_f16x2<false>(x.ks[T]);
@@ -308,6 +390,7 @@ struct FewRows {
           s[rt][T] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[i], __builtin_bit_cast(f16x8, q[rt][i]), s[rt][T], 0, 0, 0);
       }
     }
+    read_v(stage, x);
     if (!all) hide(x, s, first, blocks);
     u32x4 p[RT];
 #pragma unroll
@@ -413,12 +496,15 @@ struct FewRows {
 };
 
 template <int D, bool EXACT, int RT>
-__global__ __launch_bounds__(256) void cache_few_kernel(CacheAttention a) {
+__global__ __launch_bounds__(256, RT == 4 ? 1 : 2) void cache_few_kernel(CacheAttention a) {
   constexpr int kKeys = 128;                   // of a tile: a step of 32 for each wave
   constexpr int kRow = D + 4;                  // of LDS, in floats
-  __shared__ float park[4][16][kRow];
-  __shared__ float park_top[4][16], park_sum[4][16];
   using F = FewRows<D, EXACT, RT>;
+  // the waves' rings, and where their states meet after it
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[4 * kStages * F::kStage];
+  __shared__ float park_top[4][16], park_sum[4][16];
+  static_assert(4 * kStages * F::kStage >= 4 * 16 * kRow * 4, "");
+  float(*park)[16][kRow] = reinterpret_cast<float(*)[16][kRow]>(ring);
   F w;
   w.start(a);
   const int wave = wave_id();
@@ -452,29 +538,42 @@ __global__ __launch_bounds__(256) void cache_few_kernel(CacheAttention a) {
     const int least = row_limit(a, b, 0, seen);
 
     const int last = min((int)upto * 4, (seen + 31) / 32);
-    auto load = [&](int t, Codes<D>& x) {
-      int blocks = 0;
+    uint8_t* own = ring + wave * (kStages * F::kStage);
+    const uint32_t own_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)own;
+    // bit T: the 16-key block T lies on a page (its codes are loaded from another if not)
+    auto load = [&](int t, int stage) {
+      int64_t row[2];
+      uint32_t blocks = 0;
 #pragma unroll
       for (int T = 0; T < 2; ++T) {
         const int key = min(32 * t + 16 * T, (seen - 1) & ~15);
         const int64_t page = cache_page(a.c, b, key);
-        blocks |= (page >= 0 ? 1 : 0) << T;
-        w.load(a.c, cache_rows(a.c, page < 0 ? 0 : page, (int)kvh) + cache_place(a.c, key), min(seen - 1 - key, 15), T, x);
+        blocks |= (page >= 0 ? 1u : 0u) << T;
+        row[T] = cache_rows(a.c, page < 0 ? 0 : page, (int)kvh) + cache_place(a.c, key);
       }
+      w.load(a.c, row, own + stage * F::kStage);
       return blocks;
     };
-    Codes<D> x0, x1;
-    int t = (int)from * 4 + wave, b0 = 0, b1 = 0;
-    if (t < last) b0 = load(t, x0);
-    while (t < last) {
-      if (t + 4 < last) b1 = load(t + 4, x1);
-      w.step(x0, 32 * t, b0, b0 == 3 && 32 * t + 32 <= least);
-      t += 4;
-      if (t >= last) break;
-      if (t + 4 < last) b0 = load(t + 4, x0);
-      w.step(x1, 32 * t, b1, b1 == 3 && 32 * t + 32 <= least);
-      t += 4;
+    int t = (int)from * 4 + wave;
+    uint32_t blocks = 0;                       // two bits a stage
+    static_assert(F::kLoads * (kStages - 1) < 64, "the wait's count is 6 bits");
+    constexpr int kWait = F::kLoads * (kStages - 1);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+      if (t + 4 * i < last) blocks |= load(t + 4 * i, i) << (2 * i);
+    for (int stage = 0; t < last; t += 4, stage = stage + 1 == kStages ? 0 : stage + 1) {
+      const int free = stage == 0 ? kStages - 1 : stage - 1;
+      if (t + 4 * (kStages - 1) < last) {
+        blocks = (blocks & ~(3u << (2 * free))) | load(t + 4 * (kStages - 1), free) << (2 * free);
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (kWait & 15) | (kWait >> 4) << 14);     // vmcnt: this step's are in
+      } else {
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+      }
+      asm volatile("" ::: "memory");
+      const int on = (int)(blocks >> (2 * stage)) & 3;
+      w.step(own_at + (uint32_t)(stage * F::kStage), 32 * t, on, on == 3 && 32 * t + 32 <= least);
     }
+    __syncthreads();                           // the rings are free
 
     // the four waves' states meet in LDS, in wave order
     const uint32_t slot = (2 * blockIdx.x + (at != begin)) * (uint32_t)a.rows;
@@ -531,61 +630,63 @@ __global__ __launch_bounds__(256) void cache_few_kernel(CacheAttention a) {
 }
 
 // Joins what the workgroups left of a unit whose tiles several of them had: partial
-// sums weighted by 2^(their maximum - the largest), a workgroup a row: groups of D / 4
-// lanes take every (256 / (D / 4))-th of them in order and meet in LDS.
-template <int D, int KEYS, int TILE_ROWS>
+// sums weighted by 2^(their maximum - the largest).  A row has N groups of D / 4 lanes,
+// each of which takes every N-th of its parts in order; they meet in LDS.
+template <int D, int KEYS, int TILE_ROWS, int N>
 __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttention a) {
-  constexpr int G = D / 4, N = 256 / G;
-  __shared__ f32x4 park[N][G];
-  __shared__ float2 park_stats[N];
+  constexpr int G = D / 4, R = 256 / G / N;    // rows of a workgroup
+  __shared__ f32x4 park[R][N][G];
+  __shared__ float2 park_stats[R][N];
   const uint32_t units = (uint32_t)(a.c.kv_heads * a.row_tiles);
-  const uint32_t rows = (uint32_t)min(a.rows, TILE_ROWS);             // of a unit, at most
-  const uint32_t u = blockIdx.x / rows, in = blockIdx.x - u * rows;
+  const uint32_t rows = (uint32_t)min(a.rows, TILE_ROWS), groups = (rows + R - 1) / R;     // of a unit, at most
+  const uint32_t u = blockIdx.x / groups;
+  const int sub = threadIdx.x % G, n = threadIdx.x / G % N, r = threadIdx.x / G / N;
+  const uint32_t in = (blockIdx.x - u * groups) * R + (uint32_t)r;
   const int b = (int)(u / units);
   const uint32_t of = u - (uint32_t)b * units, kvh = of / (uint32_t)a.row_tiles;
   const int row = (int)(of - kvh * (uint32_t)a.row_tiles) * TILE_ROWS + (int)in;
-  if (row >= a.rows) return;
   Work work;
   work.start<KEYS>(a);
   const uint32_t tiles = tiles_of<KEYS>(a, b);
   const uint32_t from = work.first_of<KEYS>(a, b) + of * tiles, last = from + tiles - 1;
   const uint32_t w0 = from / work.share, w1 = last / work.share;
   if (w0 == w1) return;                        // one workgroup had it all
-  const int sub = threadIdx.x % G, n = threadIdx.x / G;
-  // each group's own maximum first, then the whole row's
+  const bool live = in < rows && row < a.rows;
   float most = -__builtin_inff(), total = 0.0f;
   f32x4 s = {};
-  for (uint32_t w = w0 + n; w <= w1; w += N) {
-    const int64_t slot = (int64_t)(2 * w + (w * work.share < from ? 1 : 0)) * a.slot_rows + in;
-    const float2 st = a.stats[slot];
-    const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + slot * D + 4 * sub);
-    if (st.y != 0.0f) {
-      const float now = __builtin_fmaxf(most, st.x);
-      const float f0 = total == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(most - now), f1 = __builtin_amdgcn_exp2f(st.x - now);
-      // (what a NaN sum has left stays NaN)
-      total = total == 0.0f ? st.y * f1 : __builtin_fmaf(total, f0, st.y * f1);
-      s = s * f0 + v * f1;
-      most = now;
+  if (live)
+    for (uint32_t w = w0 + n; w <= w1; w += N) {
+      const int64_t slot = (int64_t)(2 * w + (w * work.share < from ? 1 : 0)) * a.slot_rows + in;
+      const float2 st = a.stats[slot];
+      const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + slot * D + 4 * sub);
+      if (st.y != 0.0f) {
+        const float now = __builtin_fmaxf(most, st.x);
+        const float f0 = total == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(most - now), f1 = __builtin_amdgcn_exp2f(st.x - now);
+        total = total == 0.0f ? st.y * f1 : __builtin_fmaf(total, f0, st.y * f1);
+        s = s * f0 + v * f1;
+        most = now;
+      }
     }
+  if (N > 1) {
+    park[r][n][sub] = s;
+    if (sub == 0) park_stats[r][n] = float2{most, total};
+    __syncthreads();
+    if (n != 0) return;
+    most = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (park_stats[r][i].y != 0.0f) most = __builtin_fmaxf(most, park_stats[r][i].x);
+    total = 0.0f;
+    s = f32x4{};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (park_stats[r][i].y != 0.0f) {
+        const float f = __builtin_amdgcn_exp2f(park_stats[r][i].x - most);
+        total = __builtin_fmaf(park_stats[r][i].y, f, total);
+        s += park[r][i][sub] * f;
+      }
   }
-  park[n][sub] = s;
-  if (sub == 0) park_stats[n] = float2{most, total};
-  __syncthreads();
-  if (n != 0) return;
-  most = -__builtin_inff();
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (park_stats[i].y != 0.0f) most = __builtin_fmaxf(most, park_stats[i].x);
-  total = 0.0f;
-  s = f32x4{};
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (park_stats[i].y != 0.0f) {
-      const float f = __builtin_amdgcn_exp2f(park_stats[i].x - most);
-      total = __builtin_fmaf(park_stats[i].y, f, total);
-      s += park[i][sub] * f;
-    }
-  if (4 * sub < a.c.dim) {
+  if (live && 4 * sub < a.c.dim) {
     const float inv = total == 0.0f ? 0.0f : stored_scale(a.c.amax[1]) / total;
     *reinterpret_cast<u32x2*>(a.out + row_at(a, b, (int)kvh, row, a.o_batch, a.o_token, a.o_head) + 4 * sub) =
         u32x2{bf16x2_rne(s[0] * inv, s[1] * inv), bf16x2_rne(s[2] * inv, s[3] * inv)};
@@ -597,84 +698,166 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttention a) {
 // The waves of a workgroup have 32 rows each and share tiles of 64 keys, decoded into
 // LDS in fp16: while a tile is used, the next one's blocks (a thread has kItems of
 // them) are decoded into the other buffers and the one after that is on its way.
-template <int DP, int WAVES>
+template <int DP, int WAVES, bool PAGED>
 struct ManyRows {
   using A = Attend<DP, 2, true>;
   static constexpr int kBlocksRow = DP / 16;
-  static constexpr int kHalf = 64 * kBlocksRow;             // blocks of K, and of V, of a tile
-  static constexpr int kItems = 2 * kHalf / (64 * WAVES);
-  static_assert(kItems > 0 && kHalf % 64 == 0, "an item is K's or V's for a whole wave");
+  static constexpr int kGroupKeys = 64 / kBlocksRow;        // keys whose blocks a wave has at once
+  static constexpr int kGroups = 64 / kGroupKeys / WAVES;   // of a tile, for each wave
+  static constexpr int kAll = kGroups * WAVES;
+  static_assert(kGroups > 0 && 16 % kGroupKeys == 0, "a group's keys lie on one page");
 
   struct Tile {
-    u32x2 codes[kItems];
-    uint32_t scale[kItems];
-    uint64_t seen;             // keys below the entry's length and on a page
+    u32x2 k[kGroups], v[kGroups];
+    uint32_t ks[kGroups], vs[kGroups];
+    bool none[kGroups];        // the group lies on no page
+  };
+  // What is out of the ordinary in a tile, a byte for each block of each key: 1, its
+  // values are NaN (they are zeros in LDS); 2, the key lies on no page.
+  struct Odd {
+    uint8_t of[64][kBlocksRow];
   };
 
-  int wave, lane;
+  int wave, key, blk;          // this lane's key of a group, its block of the head
+  bool live;                   // the block is within the head size
+  int row_blocks;
+  // of the unit: its head's first page, the blocks of a page, the entry's table
+  const uint8_t *kc, *ks, *vc, *vs;
+  const int32_t* table;
+  int64_t page_blocks;
+  int pages, shift, seen, last_group;
 
-  __device__ __forceinline__ int item(int i) const { return (i * WAVES + wave) * 64 + lane; }
-
-  // The pages of the keys of tile t, a lane each (-1: none).
-  __device__ __forceinline__ int pages(const CacheAttention& a, int64_t b, int seen, int t) const {
-    const int key = 64 * t + lane;
-    return (int)cache_page(a.c, b, min(key, seen - 1));
+  __device__ __forceinline__ void start(const CacheAttention& a) {
+    const int lane = threadIdx.x & 63;
+    wave = wave_id();
+    key = lane / kBlocksRow;
+    blk = lane % kBlocksRow;
+    row_blocks = a.c.dim >> 4;
+    live = blk < row_blocks;
   }
-  __device__ __forceinline__ void load(const CacheAttention& a, int kvh, int seen, int t, int page, Tile& x) const {
-    x.seen = __ballot(64 * t + lane < seen && page >= 0);
+  __device__ __forceinline__ void unit(const CacheAttention& a, int64_t b, int kvh, int seen_) {
+    page_blocks = (int64_t)a.c.kv_heads * a.c.page_size * row_blocks;
+    const int64_t at = (int64_t)kvh * a.c.page_size * row_blocks + (PAGED ? 0 : b * page_blocks);
+    kc = a.c.k_codes + 8 * at;
+    ks = a.c.k_scales + at;
+    vc = a.c.v_codes + 8 * at;
+    vs = a.c.v_scales + at;
+    table = PAGED ? a.c.table + b * a.c.table_pages : nullptr;
+    pages = (int)a.c.pages;
+    shift = a.c.page_shift;
+    seen = seen_;
+    last_group = (seen - 1) & ~(kGroupKeys - 1);
+  }
+
+  // Where group i of tile t begins; past the last key, the last one's group.
+  __device__ __forceinline__ int first(int t, int i) const {
+    return min(64 * t + (i * WAVES + wave) * kGroupKeys, last_group);
+  }
+  __device__ __forceinline__ void look_up(int t, int (&page)[kGroups]) const {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int n = item(i), of = n % kHalf, key = of / kBlocksRow, blk = of % kBlocksRow;
-      const bool value = n >= kHalf;
-      const int from = __shfl(page, key, 64), at = min(64 * t + key, seen - 1);
-      x.codes[i] = u32x2{0u, 0u};
-      x.scale[i] = 0u;
-      if (16 * blk < a.c.dim && from >= 0) {
-        const int64_t row = cache_rows(a.c, from, kvh) + cache_place(a.c, at);
-        const int64_t block = row * (a.c.dim >> 4) + blk;
-        x.codes[i] = *reinterpret_cast<const u32x2*>((value ? a.c.v_codes : a.c.k_codes) + 8 * block);
-        x.scale[i] = (value ? a.c.v_scales : a.c.k_scales)[block];
+    for (int i = 0; i < kGroups; ++i) page[i] = PAGED ? table[first(t, i) >> shift] : 0;
+  }
+  __device__ __forceinline__ void load(int t, const int (&page)[kGroups], Tile& x) const {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int f = first(t, i);
+      x.none[i] = PAGED && (uint32_t)page[i] >= (uint32_t)pages;
+      const int64_t block = PAGED ? (x.none[i] ? 0 : page[i]) * page_blocks + (f & ((1 << shift) - 1)) * row_blocks
+                                  : (int64_t)f * row_blocks;
+      // keys past the last are taken as the last
+      const uint32_t at = (uint32_t)(min(key, seen - 1 - f) * row_blocks + blk);
+      x.k[i] = x.v[i] = u32x2{0u, 0u};
+      x.ks[i] = x.vs[i] = 0u;
+      if (live) {
+        x.k[i] = *reinterpret_cast<const u32x2*>(kc + 8 * block + 8 * at);
+        x.v[i] = *reinterpret_cast<const u32x2*>(vc + 8 * block + 8 * at);
+        x.ks[i] = (ks + block)[at];
+        x.vs[i] = (vs + block)[at];
       }
     }
   }
-  // `nan`: for each wave, the value blocks of its items that are NaN.  They are written
-  // as zeros.
-  __device__ __forceinline__ void store(Tile& x, uint8_t* lds_k, uint8_t* lds_v, uint64_t (*nan)[WAVES]) const {
+  __device__ __forceinline__ void store(const Tile& x, uint8_t* lds_k, uint8_t* lds_v, Odd& odd) const {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int n = item(i), of = n % kHalf, key = of / kBlocksRow, blk = of % kBlocksRow;
-      const bool value = n >= kHalf;
-      bool is = false;
-      if (value) is = (x.scale[i] & 0x7Fu) == 0x7Fu;
-      const uint64_t bits = __ballot(is);
-      if (lane == 0) nan[i][wave] = bits;
-      const f16x2 s = e4m3_pair_to_f16x2<false>(is ? 0u : x.scale[i]);
-      uint8_t* to = (value ? lds_v : lds_k) + key * A::kRowBytes;
-      const int swizzle = value ? v_swizzle<DP>(key) : k_swizzle<DP>(key);
-      *reinterpret_cast<f16x8*>(to + (((2 * blk) ^ swizzle) << 4)) = decode8(x.codes[i].x, s.x);
-      *reinterpret_cast<f16x8*>(to + (((2 * blk + 1) ^ swizzle) << 4)) = decode8(x.codes[i].y, s.x);
+    for (int i = 0; i < kGroups; ++i) {
+      const int in = (i * WAVES + wave) * kGroupKeys + key;
+      const bool is = !x.none[i] && (x.vs[i] & 0x7Fu) == 0x7Fu;
+      odd.of[in][blk] = (uint8_t)((is ? 1 : 0) | (x.none[i] ? 2 : 0));
+      const _Float16 k = e4m3_pair_to_f16x2<false>(x.ks[i]).x, v = e4m3_pair_to_f16x2<false>(is || x.none[i] ? 0u : x.vs[i]).x;
+      uint8_t *to_k = lds_k + in * A::kRowBytes, *to_v = lds_v + in * A::kRowBytes;
+      *reinterpret_cast<f16x8*>(to_k + (((2 * blk) ^ k_swizzle<DP>(in)) << 4)) = decode8(x.k[i].x, k);
+      *reinterpret_cast<f16x8*>(to_k + (((2 * blk + 1) ^ k_swizzle<DP>(in)) << 4)) = decode8(x.k[i].y, k);
+      *reinterpret_cast<f16x8*>(to_v + (((2 * blk) ^ v_swizzle<DP>(in)) << 4)) = decode8(x.v[i].x, v);
+      *reinterpret_cast<f16x8*>(to_v + (((2 * blk + 1) ^ v_swizzle<DP>(in)) << 4)) = decode8(x.v[i].y, v);
     }
+  }
+  static __device__ __forceinline__ bool any_odd(const Odd& odd) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (DP == 128)
+      return __any(*reinterpret_cast<const uint64_t*>(odd.of[lane]) != 0);
+    else
+      return __any(*reinterpret_cast<const uint32_t*>(odd.of[lane]) != 0);
+  }
+  // Of the keys that this lane's row sees (`mine`): those on no page are taken out, the
+  // blocks whose values are NaN are returned.
+  static __device__ __forceinline__ uint32_t odd_seen(const Odd& odd, uint64_t& mine) {
+    uint32_t hit = 0;
+    for (int i = 0; i < 64; ++i) {
+      uint32_t blocks = 0;
+      for (int j = 0; j < kBlocksRow; ++j) {
+        if (odd.of[i][j] & 2) mine &= ~(1ull << i);
+        blocks |= (odd.of[i][j] & 1u) << j;
+      }
+      hit |= mine >> i & 1 ? blocks : 0u;
+    }
+    return hit;
+  }
+  // The scores of a tile in LDS, with the next tile decoded between the matrix
+  // instructions, whose time covers it; the first fragments of V are read.
+  __device__ __forceinline__ void scores(const A& w, const uint8_t* lds_k, const uint8_t* lds_v, f32x16 (&s)[2],
+                                         u32x4 (&vf)[A::kBlocks], const Tile& x, uint8_t* next_k, uint8_t* next_v,
+                                         Odd& next_odd) const {
+    u32x4 kf[2][A::kSteps];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) s[kb] = f32x16{};
+#pragma unroll
+    for (int st = 0; st < A::kSteps; ++st)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) kf[kb][st] = A::k_frag(lds_k, kb, st, w.col, w.half);
+#pragma unroll
+    for (int st = 0; st < A::kSteps; ++st)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) s[kb] = product32<true>(kf[kb][st], w.q[st], s[kb]);
+    store(x, next_k, next_v, next_odd);
+#pragma unroll
+    for (int b = 0; b < A::kBlocks; ++b) vf[b] = A::v_frag(lds_v, 0, b, w.lane);
+    __builtin_amdgcn_sched_group_barrier(0x100, A::kSteps, 0);                     // DS reads
+#pragma unroll
+    for (int i = 0; i < 2 * A::kSteps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                           // MFMA
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);                           // VALU
+      if (i % 2) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);                // DS write
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 };
 
-template <int DP, int WAVES>
+template <int DP, int WAVES, bool PAGED>
 __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttention a) {
-  using M = ManyRows<DP, WAVES>;
+  using M = ManyRows<DP, WAVES, PAGED>;
   using A = typename M::A;
   constexpr int kKeys = 64, kTileRows = 32 * WAVES;
   constexpr int kRowPieces = A::kPieces, kRowsPerLoad = 64 / kRowPieces;
   __shared__ __attribute__((aligned(1024))) uint8_t k0[A::kTileBytes], v0[A::kTileBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t k1[A::kTileBytes], v1[A::kTileBytes];
-  __shared__ uint64_t nan0[M::kItems][WAVES], nan1[M::kItems][WAVES];
+  __shared__ typename M::Odd odd0, odd1;
   __shared__ float row_down[kTileRows];
   static_assert(WAVES == 4, "a wave's 32 rows of LDS are half a buffer of the second pair");
   M part;
-  part.wave = wave_id();
-  part.lane = threadIdx.x & 63;
-  const int wave = part.wave, lane = part.lane;
+  part.start(a);
+  const int wave = part.wave;
   const float k_scale = stored_scale(a.c.amax[0]), v_scale = stored_scale(a.c.amax[1]);
   uint8_t* own = (wave < 2 ? k1 : v1) + (wave & 1) * (32 * A::kRowBytes);
-  const int piece = lane % kRowPieces;
 
   Work work;
   uint32_t at, end, first;
@@ -702,17 +885,36 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
     const bool whole = upto - from == tiles;
     const int kvh = (int)(of / (uint32_t)a.row_tiles), row0 = (int)(of - (uint32_t)(kvh * a.row_tiles)) * kTileRows + wave * 32;
 
-    A w;
-    w.start(a.scale);
+    // the queries and the first tile are on their way before anything is waited for
+    u32x4 qrow[32 / kRowsPerLoad];
     {
-      u32x4 qrow[32 / kRowsPerLoad];
+      const int lane = opaque_lane(), piece = lane % kRowPieces;
 #pragma unroll
       for (int i = 0; i < 32 / kRowsPerLoad; ++i) {
         const int row = min(row0 + i * kRowsPerLoad + lane / kRowPieces, a.rows - 1);
         qrow[i] = u32x4{};
         if (8 * piece < a.c.dim)
-          qrow[i] = *reinterpret_cast<const u32x4*>(a.q + row_at(a, b, kvh, row, a.q_batch, a.q_token, a.q_head) + 8 * piece);
+          qrow[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+              a.q + row_at(a, b, kvh, row, a.q_batch, a.q_token, a.q_head) + 8 * piece));
       }
+    }
+    // tiles that no row of the workgroup sees are left out
+    const int most = row_limit(a, b, min(row0 - wave * 32 + kTileRows, a.rows) - 1, seen);
+    const int last = min((int)upto, (most + kKeys - 1) / kKeys);
+    typename M::Tile x;
+    int page[M::kGroups];
+    uint32_t hit = 0;
+    int t = (int)from;
+    if (t < last) {
+      part.unit(a, b, kvh, seen);
+      part.look_up(t, page);
+      part.load(t, page, x);
+      part.look_up(t + 1, page);
+    }
+    A w;
+    w.start(a.scale);
+    {
+      const int lane = opaque_lane(), piece = lane % kRowPieces;
 #pragma unroll
       for (int i = 0; i < 32 / kRowsPerLoad; ++i) {
         const int r = i * kRowsPerLoad + lane / kRowPieces;
@@ -733,55 +935,52 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
     const int limit = row_limit(a, b, min(row0 + w.col, a.rows - 1), seen);
     // of the wave's rows, which are in the order of their tokens
     const int least = row_limit(a, b, min(row0, a.rows - 1), seen);
-    const int most = row_limit(a, b, min(row0 + 31, a.rows - 1), seen);
-
-    const int last = seen > 0 ? (int)upto : (int)from;
-    typename M::Tile x;
-    uint64_t sight = 0;
-    int page = -1;
-    int t = (int)from;
     if (t < last) {
-      part.load(a, kvh, seen, t, part.pages(a, b, seen, t), x);
-      if (t + 1 < last) page = part.pages(a, b, seen, t + 1);
-      part.store(x, k0, v0, nan0);
-      sight = x.seen;
-      if (t + 1 < last) {
-        part.load(a, kvh, seen, t + 1, page, x);
-        if (t + 2 < last) page = part.pages(a, b, seen, t + 2);
-      }
+      part.store(x, k0, v0, odd0);
+      if (t + 1 < last) part.load(t + 1, page, x);
+      part.look_up(t + 2, page);
     }
-    // one tile: the next is decoded into the other buffers, the one after is loaded
-#define CACHE_TURN(kc, vc, nc, kn, vn, nn)                                                             {                                                                                                      __builtin_amdgcn_s_waitcnt(0xC07F); /* lgkmcnt(0): own writes are in LDS, own reads done */          asm volatile("s_barrier" ::: "memory");                                                              uint64_t sight_next = 0;                                                                             if (t + 1 < last) {                                                                                    part.store(x, kn, vn, nn);                                                                           sight_next = x.seen;                                                                                 if (t + 2 < last) {                                                                                    part.load(a, kvh, seen, t + 2, page, x);                                                             if (t + 3 < last) page = part.pages(a, b, seen, t + 3);                                            }                                                                                                  }                                                                                                    if (64 * t < most) {                                                                                   uint64_t mine = sight;                                                                               if (64 * t + 64 > least) {                                                                             const int n = limit - 64 * t;                                                                        mine &= n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;                                         }                                                                                                    w.tile(kc, vc, mine);                                                                                spread_nan(w, nc, mine);                                                                           }                                                                                                    sight = sight_next;                                                                                  ++t;                                                                                               }
-    // NaN values go to the rows that see them
-    auto spread_nan = [&](A& w, uint64_t (&nan)[M::kItems][WAVES], uint64_t mine) {
-      const uint64_t* flat = &nan[0][0];
-      if (__any(lane < M::kItems * WAVES && flat[lane < M::kItems * WAVES ? lane : 0] != 0)) {
-        for (int i = 0; i < M::kItems; ++i)
-          for (int v = 0; v < WAVES; ++v) {
-            const int n = (i * WAVES + v) * 64 - M::kHalf;             // of the values
-            const uint64_t bits = nan[i][v];
-            if (n < 0 || bits == 0) continue;
-            for (int j = 0; j < 64 / M::kBlocksRow; ++j) {
-              const uint32_t blocks = (uint32_t)(bits >> (j * M::kBlocksRow)) & ((1u << M::kBlocksRow) - 1);
-              if (blocks == 0 || !(mine >> (n / M::kBlocksRow + j) & 1)) continue;
-#pragma unroll
-              for (int o = 0; o < A::kBlocks; ++o)
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (blocks >> (2 * o + e / 8) & 1) w.o[o][e] = __builtin_nanf("");
-            }
-          }
-      }
-    };
+    // one tile: the next is decoded into the other buffers, the one after is loaded, the
+    // pages of the one after that are looked up
+#define CACHE_TURN(kc, vc, oc, kn, vn, on)                                                       \
+  {                                                                                              \
+    __builtin_amdgcn_s_waitcnt(0xC07F); /* lgkmcnt(0): own writes are in LDS, own reads done */  \
+    asm volatile("s_barrier" ::: "memory");                                                      \
+    f32x16 s[2];                                                                                 \
+    u32x4 vf[A::kBlocks];                                                                        \
+    const bool odd = M::any_odd(oc);                                                             \
+    part.scores(w, kc, vc, s, vf, x, kn, vn, on); /* (after the last, what x held before) */     \
+    if (t + 2 < last) {                                                                          \
+      part.load(t + 2, page, x);                                                                 \
+      part.look_up(t + 3, page);                                                                 \
+    }                                                                                            \
+    uint64_t mine = ~0ull;                                                                       \
+    if (64 * t + 64 > least) {                                                                   \
+      const int n = limit - 64 * t;                                                              \
+      mine = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;                                  \
+    }                                                                                            \
+    if (odd) hit |= M::odd_seen(oc, mine);                                                       \
+    w.weigh(s, mine);                                                                            \
+    w.gather(s, vc, vf);                                                                         \
+    ++t;                                                                                         \
+  }
     while (t < last) {
-      CACHE_TURN(k0, v0, nan0, k1, v1, nan1)
+      CACHE_TURN(k0, v0, odd0, k1, v1, odd1)
       if (t >= last) break;
-      CACHE_TURN(k1, v1, nan1, k0, v0, nan0)
+      CACHE_TURN(k1, v1, odd1, k0, v0, odd0)
     }
 #undef CACHE_TURN
+    // NaN values, which are zeros in LDS, go to the rows that see them
+    if (__any(hit != 0)) {
+#pragma unroll
+      for (int o = 0; o < A::kBlocks; ++o)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w.o[o][e] += hit >> (2 * o + e / 8) & 1 ? __builtin_nanf("") : 0.0f;
+    }
 
     const float l = halves_sum(w.sum);
     __syncthreads();
+    const int lane = opaque_lane(), piece = lane % kRowPieces, col = lane & 31, half = lane >> 5;
     // through the wave's rows of LDS again, so that whole rows are stored
     if (!whole) {
       const int64_t slot = (int64_t)(2 * blockIdx.x + (at != begin)) * kTileRows + wave * 32;
@@ -792,7 +991,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const f32x16& v = w.o[h * (A::kBlocks / 2) + o];
-            *reinterpret_cast<f32x4*>(own + w.col * A::kRowBytes + (((8 * o + 2 * g + w.half) ^ k_swizzle<DP>(w.col)) << 4)) =
+            *reinterpret_cast<f32x4*>(own + col * A::kRowBytes + (((8 * o + 2 * g + half) ^ k_swizzle<DP>(col)) << 4)) =
                 f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
           }
 #pragma unroll
@@ -802,7 +1001,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
               *reinterpret_cast<const f32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4));
         }
       }
-      if (w.half == 0) a.stats[slot + w.col] = float2{w.top, l};
+      if (half == 0) a.stats[slot + col] = float2{w.top, l};
     } else {
       const uint32_t any = l == 0.0f ? 0u : ~0u;
       const float inv = v_scale / l;
@@ -810,7 +1009,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
       for (int o = 0; o < A::kBlocks; ++o)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<u32x2*>(own + w.col * A::kRowBytes + (((4 * o + g) ^ k_swizzle<DP>(w.col)) << 4) + 8 * w.half) =
+          *reinterpret_cast<u32x2*>(own + col * A::kRowBytes + (((4 * o + g) ^ k_swizzle<DP>(col)) << 4) + 8 * half) =
               u32x2{bf16x2_rne(w.o[o][4 * g] * inv, w.o[o][4 * g + 1] * inv) & any,
                     bf16x2_rne(w.o[o][4 * g + 2] * inv, w.o[o][4 * g + 3] * inv) & any};
 #pragma unroll
@@ -818,7 +1017,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
         const int r = i * kRowsPerLoad + lane / kRowPieces, row = row0 + r;
         const u32x4 f = *reinterpret_cast<const u32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4));
         if (row < a.rows && 8 * piece < a.c.dim)
-          *reinterpret_cast<u32x4*>(a.out + row_at(a, b, kvh, row, a.o_batch, a.o_token, a.o_head) + 8 * piece) = f;
+          __builtin_nontemporal_store(f, reinterpret_cast<u32x4*>(a.out + row_at(a, b, kvh, row, a.o_batch, a.o_token, a.o_head) + 8 * piece));
       }
     }
     __syncthreads();
@@ -858,7 +1057,7 @@ Plan plan_for(int64_t batch, int64_t queries, int64_t heads, int64_t kv_heads, i
     p.slot_rows = 128;
     const int64_t tiles = (capacity + 63) / 64;
     p.least = 4;
-    if (tiles > 4 && p.units < 4 * cus) p.workers = (int)(2 * cus);
+    if (tiles > 4 && p.units <= cus) p.workers = (int)(2 * cus);
   }
   return p;
 }
@@ -906,19 +1105,23 @@ hipError_t launch_cache_attention(CacheAttention a, void* workspace, size_t work
     else
       a.c.dim == 128 ? launch_few<128, true>(a, p.few, grid, stream) : launch_few<128, false>(a, p.few, grid, stream);
   } else if (dp == 64) {
-    cache_many_kernel<64, 4><<<grid, 256, 0, stream>>>(a);
+    a.c.table ? cache_many_kernel<64, 4, true><<<grid, 256, 0, stream>>>(a)
+              : cache_many_kernel<64, 4, false><<<grid, 256, 0, stream>>>(a);
   } else {
-    cache_many_kernel<128, 4><<<grid, 256, 0, stream>>>(a);
+    a.c.table ? cache_many_kernel<128, 4, true><<<grid, 256, 0, stream>>>(a)
+              : cache_many_kernel<128, 4, false><<<grid, 256, 0, stream>>>(a);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.workers) return e;
-  const dim3 join((unsigned)(p.units * std::min<int64_t>(p.rows, p.slot_rows)));
+  const int n = p.few ? (dp == 64 ? 16 : 8) : 1, per = 256 / (dp / 4) / n;        // rows a workgroup of the join has
+  const int64_t rows = std::min<int64_t>(p.rows, p.few ? 64 : 128);
+  const dim3 join((unsigned)(p.units * ((rows + per - 1) / per)));
   if (p.few)
-    dp == 64 ? cache_join_kernel<64, 128, 64><<<join, 256, 0, stream>>>(a)
-             : cache_join_kernel<128, 128, 64><<<join, 256, 0, stream>>>(a);
+    dp == 64 ? cache_join_kernel<64, 128, 64, 16><<<join, 256, 0, stream>>>(a)
+             : cache_join_kernel<128, 128, 64, 8><<<join, 256, 0, stream>>>(a);
   else
-    dp == 64 ? cache_join_kernel<64, 64, 128><<<join, 256, 0, stream>>>(a)
-             : cache_join_kernel<128, 64, 128><<<join, 256, 0, stream>>>(a);
+    dp == 64 ? cache_join_kernel<64, 64, 128, 1><<<join, 256, 0, stream>>>(a)
+             : cache_join_kernel<128, 64, 128, 1><<<join, 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
