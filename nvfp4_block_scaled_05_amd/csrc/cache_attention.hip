@@ -28,7 +28,8 @@ namespace {
 // A unit is a tile of a kv head's query rows of an entry; its keys are counted in tiles
 // of KEYS, at least one (an entry that sees nothing still has zeros to write).  All
 // units' tiles, entry after entry, are dealt to the workgroups in equal ranges, whatever
-// the lengths.
+// the lengths.  A unit's beginning costs about as much as kStart tiles, and counts as so
+// many before its first: with 16 entries of 1 to 8192 keys @@
 
 // The keys that some query of entry b sees.
 __device__ __forceinline__ int seen_by(const CacheAttention& a, int64_t b) {
@@ -37,64 +38,72 @@ __device__ __forceinline__ int seen_by(const CacheAttention& a, int64_t b) {
   return (int)n;
 }
 
-template <int KEYS>
-__device__ __forceinline__ uint32_t tiles_of(const CacheAttention& a, int64_t b) {
-  return (uint32_t)max((seen_by(a, b) + KEYS - 1) / KEYS, 1);
-}
-
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v, int lane) {     // inclusive
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const uint32_t o = __shfl_up(v, off, 64);
-    v += lane >= off ? o : 0u;
-  }
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {               // inclusive
+#define CACHE_SHIFTED(ctrl, rows) (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, false)
+  v += CACHE_SHIFTED(0x111, 0xF);    // from 1, 2, 4, 8 lanes below, within 16
+  v += CACHE_SHIFTED(0x112, 0xF);
+  v += CACHE_SHIFTED(0x114, 0xF);
+  v += CACHE_SHIFTED(0x118, 0xF);
+  v += CACHE_SHIFTED(0x142, 0xA);    // rows 1 and 3 take the row before, then 2 and 3 lane 31
+  v += CACHE_SHIFTED(0x143, 0xC);
+#undef CACHE_SHIFTED
   return v;
 }
 
+// The lengths of the first 64 entries are kept, a lane each: one wait for most calls.
+template <int KEYS>
 struct Work {
-  uint32_t total, share;         // tiles in all, of a workgroup
+  static constexpr uint32_t kStart = KEYS == 128 ? 2 : 3;
+  uint32_t total, share;         // what all units count, and a workgroup's part
+  uint32_t units;                // of an entry
+  int seen0;                     // keys that this lane's entry sees, and what a unit of it and
+  uint32_t upto0;                // one of each entry before it count
 
-  // Every wave reads all lengths.
-  template <int KEYS>
+  static __device__ __forceinline__ uint32_t tiles(int seen) { return (uint32_t)max((seen + KEYS - 1) / KEYS, 1); }
+  // What a unit counts.
+  static __device__ __forceinline__ uint32_t parts(int seen) { return tiles(seen) + kStart; }
+  __device__ __forceinline__ uint32_t scan_from(const CacheAttention& a, int b0) const {
+    const int b = b0 + (int)(threadIdx.x & 63);
+    return wave_scan(b < a.batch ? parts(seen_by(a, b)) : 0u);
+  }
+  static __device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+  }
+
   __device__ __forceinline__ void start(const CacheAttention& a) {
     const int lane = threadIdx.x & 63;
-    uint32_t sum = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64) {
-      const uint32_t n = b0 + lane < a.batch ? tiles_of<KEYS>(a, b0 + lane) : 0u;
-      sum += __builtin_amdgcn_readlane(wave_scan(n, lane), 63);
-    }
-    total = sum * (uint32_t)(a.c.kv_heads * a.row_tiles);
+    units = (uint32_t)(a.c.kv_heads * a.row_tiles);
+    seen0 = lane < a.batch ? seen_by(a, lane) : 0;
+    upto0 = wave_scan(lane < a.batch ? parts(seen0) : 0u);
+    uint32_t sum = lane_of(upto0, 63);
+    for (int b0 = 64; b0 < a.batch; b0 += 64) sum += lane_of(scan_from(a, b0), 63);
+    total = sum * units;
     share = max((total + (uint32_t)a.workers - 1) / (uint32_t)a.workers, (uint32_t)a.least);
   }
-  // The entry with tile `at` (below the total), and its first tile.
-  template <int KEYS>
-  __device__ __forceinline__ void entry_at(const CacheAttention& a, uint32_t at, int& entry, uint32_t& first) {
-    const int lane = threadIdx.x & 63;
-    const uint32_t units = (uint32_t)(a.c.kv_heads * a.row_tiles);
+  // The entry with part `at` (below the total), and its first part.
+  __device__ __forceinline__ void entry_at(const CacheAttention& a, uint32_t at, int& entry, uint32_t& first) const {
     uint32_t before = 0;
     for (int b0 = 0;; b0 += 64) {
-      const uint32_t n = b0 + lane < a.batch ? tiles_of<KEYS>(a, b0 + lane) * units : 0u;
-      const uint32_t upto = before + wave_scan(n, lane);
-      const uint32_t all = __builtin_amdgcn_readlane(upto, 63);
-      if (at < all) {
-        const int i = __popcll(__ballot(upto <= at));
+      const uint32_t upto = (before + (b0 == 0 ? upto0 : scan_from(a, b0))), all = lane_of(upto, 63);
+      if (at < all * units) {
+        const int i = __popcll(__ballot(upto * units <= at));
         entry = b0 + i;
-        first = i == 0 ? before : __builtin_amdgcn_readlane(upto, i - 1);
+        first = (i == 0 ? before : lane_of(upto, i - 1)) * units;
         return;
       }
       before = all;
     }
   }
-  // The first tile of entry b.
-  template <int KEYS>
-  __device__ __forceinline__ uint32_t first_of(const CacheAttention& a, int b) {
-    const int lane = threadIdx.x & 63;
+  // The first part of entry b.
+  __device__ __forceinline__ uint32_t first_of(const CacheAttention& a, int b) const {
     uint32_t sum = 0;
-    for (int b0 = 0; b0 < b; b0 += 64) {
-      const uint32_t n = b0 + lane < b ? tiles_of<KEYS>(a, b0 + lane) : 0u;
-      sum += __builtin_amdgcn_readlane(wave_scan(n, lane), 63);
-    }
-    return sum * (uint32_t)(a.c.kv_heads * a.row_tiles);
+    int b0 = 0;
+    for (; b0 + 64 <= b; b0 += 64) sum += lane_of(b0 == 0 ? upto0 : scan_from(a, b0), 63);
+    if (b > b0) sum += lane_of(b0 == 0 ? upto0 : scan_from(a, b0), b - b0 - 1);
+    return sum * units;
+  }
+  __device__ __forceinline__ int seen(const CacheAttention& a, int b) const {
+    return b < 64 ? (int)lane_of((uint32_t)seen0, b) : __builtin_amdgcn_readfirstlane(seen_by(a, b));
   }
 };
 
@@ -233,17 +242,26 @@ struct FewRows {
     for (int r = 0; r < (EXACT ? 1 : 4); ++r) at_vs[r] = (uint32_t)(kVs + (4 * r + g) * scale_bytes + block);
   }
 
-  // The rows of a unit from `row0` on; rows past the last are the last.
-  __device__ __forceinline__ void rows(const CacheAttention& a, int64_t b, int kvh, int row0, int seen, float k_scale) {
+  // The rows of a unit; rows past the last are the last.
+  __device__ __forceinline__ void load_rows(const CacheAttention& a, int64_t b, int kvh) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int row = min(row0 + 16 * rt + m, a.rows - 1);
+      const int row = min(16 * rt + m, a.rows - 1);
       const uint16_t* at = a.q + row_at(a, b, kvh, row, a.q_batch, a.q_token, a.q_head) + (D / 4) * g;
-      float most = 0.0f;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         q[rt][s] = u32x4{};
         if (live_k[s / 2]) q[rt][s] = *reinterpret_cast<const u32x4*>(at + 8 * s);
+      }
+    }
+  }
+  __device__ __forceinline__ void start_rows(const CacheAttention& a, int64_t b, int seen, float k_scale) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int row = min(16 * rt + m, a.rows - 1);
+      float most = 0.0f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
         // an integer maximum: NaN is the largest
         const float v = top_magnitude(q[rt][s]);
         most = __uint_as_float(max(__float_as_uint(most), __float_as_uint(v)));
@@ -510,61 +528,83 @@ __global__ __launch_bounds__(256, RT == 4 ? 1 : 2) void cache_few_kernel(CacheAt
   const int wave = wave_id();
   const float k_scale = stored_scale(a.c.amax[0]), v_scale = stored_scale(a.c.amax[1]);
 
-  Work work;
+  Work<kKeys> work;
   uint32_t at, end, first;
   int b;
   if (a.workers) {
-    work.start<kKeys>(a);
+    work.start(a);
     at = blockIdx.x * work.share;
     if (at >= work.total) return;
     end = min(at + work.share, work.total);
-    work.entry_at<kKeys>(a, at, b, first);
+    work.entry_at(a, at, b, first);
   } else {
     b = (int)(blockIdx.x / (uint32_t)a.c.kv_heads);
     first = 0;
-    at = (blockIdx.x - (uint32_t)(b * a.c.kv_heads)) * tiles_of<kKeys>(a, b);
+    at = (blockIdx.x - (uint32_t)(b * a.c.kv_heads)) * Work<kKeys>::parts(seen_by(a, b));
     end = at + 1;                              // of any size: the unit is taken whole
   }
   const uint32_t begin = at;
 
   while (at < end) {
-    const int seen = __builtin_amdgcn_readfirstlane(seen_by(a, b));
-    const uint32_t tiles = (uint32_t)max((seen + kKeys - 1) / kKeys, 1);
-    const uint32_t kvh = (at - first) / tiles, from = at - first - kvh * tiles;
-    const uint32_t upto = a.workers ? min(from + (end - at), tiles) : tiles;
+    const int seen = a.workers ? work.seen(a, b) : __builtin_amdgcn_readfirstlane(seen_by(a, b));
+    const uint32_t tiles = Work<kKeys>::tiles(seen), parts = tiles + Work<kKeys>::kStart;
+    const uint32_t kvh = (at - first) / parts, in = at - first - kvh * parts;
+    const uint32_t upto_part = a.workers ? min(in + (end - at), parts) : parts;
+    const uint32_t from = in - min(in, Work<kKeys>::kStart), upto = upto_part - min(upto_part, Work<kKeys>::kStart);
     const bool whole = upto - from == tiles;
-    w.rows(a, b, (int)kvh, 0, seen, k_scale);
+    const uint32_t done = at;
+    at += upto_part - in;
+    if (upto > 0) {
+    w.load_rows(a, b, (int)kvh);               // on their way while the pages are looked up
     // the least that a row sees; rows are in the order of their tokens
     const int least = row_limit(a, b, 0, seen);
 
     const int last = min((int)upto * 4, (seen + 31) / 32);
     uint8_t* own = ring + wave * (kStages * F::kStage);
     const uint32_t own_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)own;
-    // bit T: the 16-key block T lies on a page (its codes are loaded from another if not)
-    auto load = [&](int t, int stage) {
-      int64_t row[2];
+    // where the two 16-key blocks of step t lie; bit T: block T is on a page (its codes are
+    // loaded from another if not)
+    int64_t row[2];
+    int held = 0, held_from = -64;             // 64 entries of the table, a lane each
+    auto look_up = [&](int t) {
       uint32_t blocks = 0;
 #pragma unroll
       for (int T = 0; T < 2; ++T) {
         const int key = min(32 * t + 16 * T, (seen - 1) & ~15);
-        const int64_t page = cache_page(a.c, b, key);
+        int page = b;
+        if (a.c.table) {
+          const int n = key >> a.c.page_shift;
+          if (n >= held_from + 64) {
+            held_from = n;
+            held = a.c.table[b * a.c.table_pages + min((int64_t)n + w.lane, a.c.table_pages - 1)];
+          }
+          page = __builtin_amdgcn_readlane(held, n - held_from);
+          if (page >= a.c.pages) page = -1;
+        }
         blocks |= (page >= 0 ? 1u : 0u) << T;
         row[T] = cache_rows(a.c, page < 0 ? 0 : page, (int)kvh) + cache_place(a.c, key);
       }
-      w.load(a.c, row, own + stage * F::kStage);
       return blocks;
+    };
+    auto load = [&](int t, int stage) {
+      const uint32_t blocks = look_up(t);
+      w.load(a.c, row, own + stage * F::kStage);
+      return blocks << (2 * stage);
     };
     int t = (int)from * 4 + wave;
     uint32_t blocks = 0;                       // two bits a stage
+    if (t < last) blocks = look_up(t);
+    w.start_rows(a, b, seen, k_scale);
+    if (t < last) w.load(a.c, row, own);
     static_assert(F::kLoads * (kStages - 1) < 64, "the wait's count is 6 bits");
     constexpr int kWait = F::kLoads * (kStages - 1);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i)
-      if (t + 4 * i < last) blocks |= load(t + 4 * i, i) << (2 * i);
+    for (int i = 1; i < kStages - 1; ++i)
+      if (t + 4 * i < last) blocks |= load(t + 4 * i, i);
     for (int stage = 0; t < last; t += 4, stage = stage + 1 == kStages ? 0 : stage + 1) {
       const int free = stage == 0 ? kStages - 1 : stage - 1;
       if (t + 4 * (kStages - 1) < last) {
-        blocks = (blocks & ~(3u << (2 * free))) | load(t + 4 * (kStages - 1), free) << (2 * free);
+        blocks = (blocks & ~(3u << (2 * free))) | load(t + 4 * (kStages - 1), free);
         __builtin_amdgcn_s_waitcnt(0x0F70 | (kWait & 15) | (kWait >> 4) << 14);     // vmcnt: this step's are in
       } else {
         __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -576,7 +616,7 @@ __global__ __launch_bounds__(256, RT == 4 ? 1 : 2) void cache_few_kernel(CacheAt
     __syncthreads();                           // the rings are free
 
     // the four waves' states meet in LDS, in wave order
-    const uint32_t slot = (2 * blockIdx.x + (at != begin)) * (uint32_t)a.rows;
+    const uint32_t slot = (2 * blockIdx.x + (done != begin)) * (uint32_t)a.rows;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const float l = rows_sum(w.sum[rt]);
@@ -619,10 +659,10 @@ __global__ __launch_bounds__(256, RT == 4 ? 1 : 2) void cache_few_kernel(CacheAt
       }
       __syncthreads();
     }
-    at += upto - from;
+    }
     if (!a.workers) return;
     // the next unit is the entry's next head, or the next entry's first
-    if (at - first == tiles * (uint32_t)a.c.kv_heads) {
+    if (at - first == parts * (uint32_t)a.c.kv_heads) {
       first = at;
       ++b;
     }
@@ -645,27 +685,37 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttention a) {
   const int b = (int)(u / units);
   const uint32_t of = u - (uint32_t)b * units, kvh = of / (uint32_t)a.row_tiles;
   const int row = (int)(of - kvh * (uint32_t)a.row_tiles) * TILE_ROWS + (int)in;
-  Work work;
-  work.start<KEYS>(a);
-  const uint32_t tiles = tiles_of<KEYS>(a, b);
-  const uint32_t from = work.first_of<KEYS>(a, b) + of * tiles, last = from + tiles - 1;
-  const uint32_t w0 = from / work.share, w1 = last / work.share;
+  Work<KEYS> work;
+  work.start(a);
+  const uint32_t parts = Work<KEYS>::parts(work.seen(a, b));
+  const uint32_t from = work.first_of(a, b) + of * parts, last = from + parts - 1;
+  // the workgroups that have its first and its last tile
+  const uint32_t w0 = (from + Work<KEYS>::kStart) / work.share, w1 = last / work.share;
   if (w0 == w1) return;                        // one workgroup had it all
   const bool live = in < rows && row < a.rows;
   float most = -__builtin_inff(), total = 0.0f;
   f32x4 s = {};
   if (live)
-    for (uint32_t w = w0 + n; w <= w1; w += N) {
-      const int64_t slot = (int64_t)(2 * w + (w * work.share < from ? 1 : 0)) * a.slot_rows + in;
-      const float2 st = a.stats[slot];
-      const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + slot * D + 4 * sub);
-      if (st.y != 0.0f) {
-        const float now = __builtin_fmaxf(most, st.x);
-        const float f0 = total == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(most - now), f1 = __builtin_amdgcn_exp2f(st.x - now);
-        total = total == 0.0f ? st.y * f1 : __builtin_fmaf(total, f0, st.y * f1);
-        s = s * f0 + v * f1;
-        most = now;
+    for (uint32_t w = w0 + n; w <= w1; w += 4 * N) {
+      float2 st[4];                            // four parts are on their way at once
+      f32x4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t u = min(w + i * N, w1);
+        const int64_t slot = (int64_t)(2 * u + (u * work.share < from ? 1 : 0)) * a.slot_rows + in;
+        st[i] = w + i * N <= w1 ? a.stats[slot] : float2{0.0f, 0.0f};
+        v[i] = *reinterpret_cast<const f32x4*>(a.part + slot * D + 4 * sub);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (st[i].y != 0.0f) {
+          const float now = __builtin_fmaxf(most, st[i].x);
+          const float f0 = total == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(most - now);
+          const float f1 = __builtin_amdgcn_exp2f(st[i].x - now);
+          total = total == 0.0f ? st[i].y * f1 : __builtin_fmaf(total, f0, st[i].y * f1);
+          s = s * f0 + v[i] * f1;
+          most = now;
+        }
     }
   if (N > 1) {
     park[r][n][sub] = s;
@@ -859,30 +909,34 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
   const float k_scale = stored_scale(a.c.amax[0]), v_scale = stored_scale(a.c.amax[1]);
   uint8_t* own = (wave < 2 ? k1 : v1) + (wave & 1) * (32 * A::kRowBytes);
 
-  Work work;
+  Work<kKeys> work;
   uint32_t at, end, first;
   int b;
   const uint32_t units = (uint32_t)(a.c.kv_heads * a.row_tiles);
   if (a.workers) {
-    work.start<kKeys>(a);
+    work.start(a);
     at = blockIdx.x * work.share;
     if (at >= work.total) return;
     end = min(at + work.share, work.total);
-    work.entry_at<kKeys>(a, at, b, first);
+    work.entry_at(a, at, b, first);
   } else {
     b = (int)(blockIdx.x / units);
     first = 0;
-    at = (blockIdx.x - (uint32_t)b * units) * tiles_of<kKeys>(a, b);
+    at = (blockIdx.x - (uint32_t)b * units) * Work<kKeys>::parts(seen_by(a, b));
     end = at + 1;
   }
   const uint32_t begin = at;
 
   while (at < end) {
-    const int seen = __builtin_amdgcn_readfirstlane(seen_by(a, b));
-    const uint32_t tiles = (uint32_t)max((seen + kKeys - 1) / kKeys, 1);
-    const uint32_t of = (at - first) / tiles, from = at - first - of * tiles;
-    const uint32_t upto = a.workers ? min(from + (end - at), tiles) : tiles;
+    const int seen = a.workers ? work.seen(a, b) : __builtin_amdgcn_readfirstlane(seen_by(a, b));
+    const uint32_t tiles = Work<kKeys>::tiles(seen), parts = tiles + Work<kKeys>::kStart;
+    const uint32_t of = (at - first) / parts, in = at - first - of * parts;
+    const uint32_t upto_part = a.workers ? min(in + (end - at), parts) : parts;
+    const uint32_t from = in - min(in, Work<kKeys>::kStart), upto = upto_part - min(upto_part, Work<kKeys>::kStart);
     const bool whole = upto - from == tiles;
+    const uint32_t done = at;
+    at += upto_part - in;
+    if (upto > 0) {
     const int kvh = (int)(of / (uint32_t)a.row_tiles), row0 = (int)(of - (uint32_t)(kvh * a.row_tiles)) * kTileRows + wave * 32;
 
     // the queries and the first tile are on their way before anything is waited for
@@ -983,7 +1037,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
     const int lane = opaque_lane(), piece = lane % kRowPieces, col = lane & 31, half = lane >> 5;
     // through the wave's rows of LDS again, so that whole rows are stored
     if (!whole) {
-      const int64_t slot = (int64_t)(2 * blockIdx.x + (at != begin)) * kTileRows + wave * 32;
+      const int64_t slot = (int64_t)(2 * blockIdx.x + (done != begin)) * kTileRows + wave * 32;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -1021,9 +1075,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
       }
     }
     __syncthreads();
-    at += upto - from;
+    }
     if (!a.workers) return;
-    if (at - first == tiles * units) {
+    if (at - first == parts * units) {
       first = at;
       ++b;
     }
