@@ -314,22 +314,41 @@ def gemm_weight_only(x, w, bias=None, epilogue="none", y_amax=None, out=None):
     the one for many rows.  y_amax: optional one-element float32 device tensor, set
     to max |Y| for ``quantize``.
     """
+    # what is common takes one look (block_ops); anything else the checks below
     torch = _torch()
-    M, K = _matrix(x, "x", torch.bfloat16)
-    N = _nvfp4(w, "w")
-    if w.cols != K:
-        raise ValueError(f"K mismatch: x has {K} columns, w {w.cols}")
+    codes, scales, tensor_scale, cols = w if type(w) is Nvfp4Tensor else (None,) * 4
+    try:
+        M, K = x.shape
+        N, half = codes.shape
+        good = (x.dtype is torch.bfloat16 and codes.dtype is torch.uint8 and scales.dtype is torch.uint8
+                and x.is_contiguous() and codes.is_contiguous() and scales.is_contiguous()
+                and K == cols == 2 * half and K > 0 and K % 16 == 0 and scales.shape == (N, K // 16)
+                and tensor_scale.dtype is torch.float32 and tensor_scale.numel() > 0
+                and tensor_scale.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        M, K = _matrix(x, "x", torch.bfloat16)
+        N = _nvfp4(w, "w")
+        if w.cols != K:
+            raise ValueError(f"K mismatch: x has {K} columns, w {w.cols}")
+        codes, scales, tensor_scale, _ = w
     epi = _epilogue(epilogue)
-    _opt(bias, "bias", torch.bfloat16, (N,))
-    _opt(y_amax, "y_amax", torch.float32)
-    _opt(out, "out", torch.bfloat16, (M, N))
-    dev = _device(x=x, **_parts(w, "w"), bias=bias, y_amax=y_amax, out=out)
+    if bias is not None:
+        _tensor(bias, "bias", torch.bfloat16, (N,))
+    if y_amax is not None:
+        _tensor(y_amax, "y_amax", torch.float32)
+    if out is not None:
+        _tensor(out, "out", torch.bfloat16, (M, N))
+    at = _place((x, codes, scales, tensor_scale, bias, y_amax, out),
+                "x w.codes w.scales w.tensor_scale bias y_amax out")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    _binding.check(load().w4_gemm_weight_only(_ptr(x), _ptr(w.codes), _ptr(w.scales),
-                                                 _ptr(w.tensor_scale), _ptr(bias), M, N, K, epi,
-                                                 _ptr(out), _ptr(y_amax), _stream()),
-                   "w4_gemm_weight_only")
+        out = x.new_empty((M, N))
+    status = load().w4_gemm_weight_only(x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                        tensor_scale.data_ptr(), _ptr(bias), M, N, K, epi,
+                                        out.data_ptr(), _ptr(y_amax), _stream_at(at))
+    if status:
+        raise Nvfp4Error(status, "w4_gemm_weight_only")
     return out
 
 
@@ -459,7 +478,7 @@ def linear(x, weight, name, bias=None, epilogue="none", pattern=None, lora=None,
 
 
 # the operators between the linears use the checks above
-from .block_ops import (RotaryPlan, cross_attention, cross_attention_workspace,  # noqa: E402
+from .block_ops import (RotaryPlan, _place, _stream_at, cross_attention, cross_attention_workspace,  # noqa: E402
                         gated_norm, lora_add, lora_workspace, rotary, rotary_plan)
 from .cache_ops import (KvCache, cache_attention, cache_attention_workspace,  # noqa: E402
                         cache_read, cache_write, kv_cache)

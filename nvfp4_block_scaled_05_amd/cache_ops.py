@@ -13,7 +13,7 @@ from collections import namedtuple
 
 from . import _NO_WORKSPACE, _opt, _ptr, _tensor, _torch
 from ._binding import Nvfp4Error, load
-from .block_ops import _heads, _new_heads, _out_heads, _place, _stream_at
+from .block_ops import _VIEW, _heads, _new_heads, _out_heads, _place, _stream_at
 
 #: codes uint8 [pages, kv_heads, page_size, dim / 2] and E4M3 scales uint8
 #: [pages, kv_heads, page_size, dim / 16] of keys and of values; amax float32 [2]
@@ -51,9 +51,8 @@ def kv_cache(pages, page_size, kv_heads, dim, k_amax=UNIT_AMAX, v_amax=UNIT_AMAX
                    torch.tensor([k_amax, v_amax], dtype=torch.float32, device=device))
 
 
-def _cache(cache, table, batch):
-    """(kv_heads, dim, capacity) and the C view of a cache whose table serves
-    ``batch`` entries (None: as many as it has)."""
+def _check_cache(cache):
+    """Raises ValueError for what is not a cache."""
     torch = _torch()
     if not isinstance(cache, KvCache):
         raise ValueError("cache: expected a KvCache (kv_cache)")
@@ -67,39 +66,59 @@ def _cache(cache, table, batch):
     scales = (pages, kv_heads, page_size, dim // 16)
     for name, t, want in (("k_codes", codes, shape), ("k_scales", cache.k_scales, scales),
                           ("v_codes", cache.v_codes, shape), ("v_scales", cache.v_scales, scales)):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.shape != want or not t.is_contiguous():
-            _tensor(t, f"cache.{name}", torch.uint8, want)
-    amax = cache.amax
-    if not isinstance(amax, torch.Tensor) or amax.dtype != torch.float32 or amax.shape != (2,):
-        _tensor(amax, "cache.amax", torch.float32, (2,))
+        _tensor(t, f"cache.{name}", torch.uint8, want)
+    _tensor(cache.amax, "cache.amax", torch.float32, (2,))
+
+
+def _cache(cache, table, batch):
+    """(batch, kv_heads, dim, capacity) and the C view of a cache whose table serves
+    ``batch`` entries (None: as many as it has)."""
+    torch = _torch()
+    u8 = torch.uint8
+    # what is common takes one look, as in block_ops
+    try:
+        kc, ks, vc, vs, amax = cache
+        shape = kc.shape
+        pages, kv_heads, page_size, half = shape
+        dim = 2 * half
+        good = (type(cache) is KvCache and kc.dtype is u8 and ks.dtype is u8 and vc.dtype is u8 and vs.dtype is u8
+                and amax.dtype is torch.float32 and kc.is_contiguous() and ks.is_contiguous()
+                and vc.is_contiguous() and vs.is_contiguous() and amax.is_contiguous() and vc.shape == shape
+                and ks.shape == vs.shape == (pages, kv_heads, page_size, half >> 3) and amax.shape == (2,)
+                and kc.numel() > 0 and not (page_size | dim) & 15 and dim <= 128)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _check_cache(cache)
     if table is None:
         if batch is None:
             batch = pages
         if batch > pages:
             raise ValueError(f"{batch} entries, but the cache has {pages} pages (no table is given)")
-        per, at, capacity = 0, None, page_size
+        per, at, capacity = 0, 0, page_size
     else:
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError("table: expected a 2-D torch.Tensor")
+        rows, per = table.shape
         if batch is None:
-            batch = table.shape[0]
-        per = table.shape[1]
-        _tensor(table, "table", torch.int32, (batch, per), 0)
+            batch = rows
+        if table.dtype is not torch.int32 or rows != batch or not table.is_contiguous():
+            _tensor(table, "table", torch.int32, (batch, per), 0)
         if page_size & (page_size - 1):
             raise ValueError(f"a table needs a page size that is a power of two, got {page_size}")
         if per == 0:
             raise ValueError("table: needs a page for each entry at least")
         at, capacity = table.data_ptr(), per * page_size
-    return batch, kv_heads, dim, capacity, _CACHE(
-        codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(),
-        amax.data_ptr(), pages, page_size, kv_heads, dim, at or 0, per)
+    return batch, kv_heads, dim, capacity, _CACHE(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
+                                                  amax.data_ptr(), pages, page_size, kv_heads, dim, at, per)
 
 
 def _entries(t, name, batch, optional=True):
     if t is None and optional:
         return
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != (batch,) or not t.is_contiguous():
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != batch
+            or not t.is_contiguous()):
         _tensor(t, name, torch.int32, (batch,), 0)
 
 
@@ -177,9 +196,9 @@ def cache_read(cache, tokens, starts=None, counts=None, table=None, out=None):
                 "cache.k_codes cache.k_scales cache.v_codes cache.v_scales cache.amax starts counts table "
                 "out_k out_v")
     if out is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+        k = cache.amax.new_empty(shape, dtype=torch.bfloat16)
         v, vv = _new_heads(k, shape)
-        kv = _heads(k, "k")[1]
+        kv = _VIEW(k.data_ptr(), tokens * kv_heads * dim, kv_heads * dim, dim)
     status = load().kv_cache_read(view, kv, vv, batch, tokens, _ptr(starts), _ptr(counts), _stream_at(at))
     if status:
         raise Nvfp4Error(status, "kv_cache_read")
