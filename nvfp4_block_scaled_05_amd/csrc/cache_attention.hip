@@ -127,7 +127,7 @@ __device__ __forceinline__ float stored_scale(float amax) {
   return s_dec;
 }
 
-// A row's power of two, from its largest magnitude: `up` brings it into [2^13, 2^14),
+// A row's power of two, from its largest magnitude (infinity and NaN stay what they are): `up` brings it into [2^13, 2^14),
 // `down` is 1 / up.  Rows below 2^-100 are taken as if they reached it.
 __device__ __forceinline__ void row_power(float top, float& up, float& down) {
   const int e = max((int)(__float_as_uint(top) >> 23), 27);
@@ -154,6 +154,19 @@ __device__ __forceinline__ u32x4 scaled_f16(u32x4 v, float up) {
 __device__ __forceinline__ float top_magnitude(u32x4 v) {
   const u16x2 m = max8(v);
   return bf16_bits_to_f32(m.x > m.y ? m.x : m.y);
+}
+
+// Largest over aligned groups of N = 8 or 16 lanes.
+template <int N>
+__device__ __forceinline__ float group_max(float v) {
+#define CACHE_LANES(ctrl) \
+  __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, 0xF, 0xF, false))
+  v = __builtin_fmaxf(v, CACHE_LANES(0xB1));                  // lane ^ 1
+  v = __builtin_fmaxf(v, CACHE_LANES(0x4E));                  // lane ^ 2
+  v = __builtin_fmaxf(v, CACHE_LANES(0x141));                 // mirrored within 8
+  if (N == 16) v = __builtin_fmaxf(v, CACHE_LANES(0x140));    // mirrored within 16
+#undef CACHE_LANES
+  return v;
 }
 
 // Largest over the four 16-lane rows of a wave, lane by lane.
@@ -262,15 +275,10 @@ struct FewRows {
       float most = 0.0f;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        // an integer maximum: NaN is the largest
-        const float v = top_magnitude(q[rt][s]);
-        most = __uint_as_float(max(__float_as_uint(most), __float_as_uint(v)));
+        most = __builtin_fmaxf(most, top_magnitude(q[rt][s]));
       }
-      uint32_t w = __float_as_uint(most);
-      w = max(w, (uint32_t)__shfl_xor((int)w, 16, 64));
-      w = max(w, (uint32_t)__shfl_xor((int)w, 32, 64));
       float up, down;
-      row_power(__uint_as_float(w), up, down);
+      row_power(rows_max(most), up, down);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) q[rt][s] = scaled_f16(q[rt][s], up);
       c[rt] = score_factor(a.scale, k_scale, down);
@@ -972,11 +980,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
 #pragma unroll
       for (int i = 0; i < 32 / kRowsPerLoad; ++i) {
         const int r = i * kRowsPerLoad + lane / kRowPieces;
-        uint32_t top = __float_as_uint(top_magnitude(qrow[i]));
-#pragma unroll
-        for (int off = 1; off < kRowPieces; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
         float up, down;
-        row_power(__uint_as_float(top), up, down);
+        row_power(group_max<kRowPieces>(top_magnitude(qrow[i])), up, down);
         *reinterpret_cast<u32x4*>(own + r * A::kRowBytes + ((piece ^ k_swizzle<DP>(r)) << 4)) = scaled_f16(qrow[i], up);
         if (piece == 0) row_down[wave * 32 + r] = down;
       }
