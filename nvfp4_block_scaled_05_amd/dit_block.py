@@ -14,8 +14,11 @@ projection takes its input from the caller.  DitCrossBlock is a whole block
 whose image tokens attend to a text encoder's states.
 """
 
-from . import (_device, _tensor, cross_attention, cross_attention_workspace, gated_norm, gemm,
-               gemm_bf16, gemm_workspace, layer_is_quantized, lora_add, lora_workspace, quantize,
+import math
+
+from . import (_device, _tensor, cache_attention, cache_attention_workspace, cache_write,
+               cross_attention, cross_attention_workspace, gated_norm, gemm, gemm_bf16,
+               gemm_workspace, kv_cache, layer_is_quantized, lora_add, lora_workspace, quantize,
                quantize_workspace, quantize_weight, rotary)
 
 #: layer name -> (input, weight, epilogue)
@@ -115,11 +118,19 @@ class DitCrossBlock:
     ``plan``: a rotary plan for the image positions (text states carry none).
     ``lora``: layer name -> (down, up, scales), the adapters of all requests;
     ``ids`` of a call says which one each token uses.
+    ``held``: "bf16", the prompts' keys and values as the projection and rotary leave
+    them, or "nvfp4", in a cache of 4-bit codes (``cache``, a page for each prompt):
+    9/32 of the memory, which every block of a model takes for every prompt over all
+    steps.  Keys are quantized under the bound that their norm gives,
+    sqrt(dim) max |k_norm|, values under the amax that the projection's epilogue
+    computes.
     """
 
     def __init__(self, weights, batch, tokens, states, heads, kv_heads, q_norm, k_norm, plan,
-                 lora=None):
+                 lora=None, held="bf16"):
         import torch
+        if held not in ("bf16", "nvfp4"):
+            raise ValueError(f"held must be 'bf16' or 'nvfp4', got {held!r}")
         dev = weights["w_q"].device
         self.batch, self.tokens, self.states = batch, tokens, states
         self.heads, self.kv_heads = heads, kv_heads
@@ -155,7 +166,15 @@ class DitCrossBlock:
         self.k = self.v = None
         # the block's own, so that a captured call finds the last prompt's lengths in it
         self.lengths = torch.full((batch,), states, dtype=torch.int32, device=dev)
-        self.attn_ws = cross_attention_workspace(batch, tokens, states, heads, kv_heads, dim, dev)
+        self.cache = None
+        if held == "nvfp4":
+            page = -(-states // 16) * 16
+            bound = math.sqrt(dim) * float(k_norm.abs().max()) or 1.0
+            self.cache = kv_cache(batch, page, kv_heads, dim, k_amax=bound, device=dev)
+            self.first = torch.zeros((batch,), dtype=torch.int32, device=dev)
+            self.attn_ws = cache_attention_workspace(batch, tokens, heads, kv_heads, dim, page, dev)
+        else:
+            self.attn_ws = cross_attention_workspace(batch, tokens, states, heads, kv_heads, dim, dev)
         self.amax = torch.zeros((1,), dtype=torch.float32, device=dev)
         self.quant_ws = quantize_workspace(dev)
         axes = (plan.axes,) if plan.axes > 1 else ()
@@ -188,12 +207,16 @@ class DitCrossBlock:
         if lengths is not None:
             _tensor(lengths, "lengths", torch.int32, (self.batch,))
             _device(states=states, lengths=lengths)
-        kv = self._linear(self.to_kv, states.view(-1, states.shape[-1]))
+        # the amax of keys and values together bounds the values'
+        amax = self.cache.amax[1:] if self.cache and self.quantized[self.to_kv] else None
+        kv = self._linear(self.to_kv, states.view(-1, states.shape[-1]), amax_out=amax)
         kv = kv.view(self.batch, self.states, 2, self.kv_heads, -1)
         k, self.v = kv[:, :, 0], kv[:, :, 1]
         # text states carry no position: position 0, without the factor on rotated
         # values that a YaRN plan has, leaves their norm alone
         self.k = rotary(k, self.no_positions, self.plan._replace(magnitude=1.0), q_weight=self.k_norm, out=k)
+        if self.cache:
+            cache_write(self.cache, self.k, self.v, self.first)
         if lengths is None:
             self.lengths.fill_(self.states)
         else:
@@ -212,8 +235,11 @@ class DitCrossBlock:
         q = self._linear(self.to_q, self.h.view(b * t, hidden), ids, amax_in=self._given(self.to_q))
         q = q.view(b, t, self.heads, -1)
         rotary(q, positions, self.plan, q_weight=self.q_norm, out=q)
-        cross_attention(q, self.k, self.v, kv_lengths=self.lengths, out=self.attended,
-                        workspace=self.attn_ws)
+        if self.cache:
+            cache_attention(q, self.cache, self.lengths, out=self.attended, workspace=self.attn_ws)
+        else:
+            cross_attention(q, self.k, self.v, kv_lengths=self.lengths, out=self.attended,
+                            workspace=self.attn_ws)
         o = self._linear(self.to_out, self.attended.view(b * t, -1), ids)
         gated_norm(x, o.view(b, t, hidden), gate=gate_a, scale=scale_m, shift=shift_m,
                    amax=self.amax, residual_out=self.r, out=self.h)

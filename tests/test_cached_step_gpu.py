@@ -1,0 +1,168 @@
+"""The cache's operators and the weight-only product run together: DitCrossBlock with
+its prompts held in 4 bits, and a small model's steps over a paged cache, token by token
+against the same tokens in one causal pass, eager and captured."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scaled_05_amd as nv
+import oracle.cache as oc
+from nvfp4_block_scaled_05_amd.dit_block import DitCrossBlock
+from nvfp4_block_scaled_05_amd.graph import capture
+from tests.block_util import f64, normal
+from tests.cache_util import check, ints, numbers_of
+from tests.gpu_util import bits_of
+
+pytestmark = pytest.mark.gpu
+
+B, T, L, HID, HEADS, KV, DIM, MLP, ENC = 2, 70, 33, 256, 4, 2, 64, 512, 128
+
+
+def block(held):
+    rng = np.random.default_rng(0)
+    w = {"w_mod": (6 * HID, HID), "w_q": (HEADS * DIM, HID), "w_kv": (2 * KV * DIM, ENC), "w_o": (HID, HEADS * DIM),
+         "w_up": (MLP, HID), "w_down": (HID, MLP)}
+    weights = {k: normal(rng, s, 0.05) for k, s in w.items()}
+    qn, kn = (normal(rng, (DIM,), 0.1, 1.0, torch.float32) for _ in range(2))
+    b = DitCrossBlock(weights, B, T, L, HEADS, KV, qn, kn, nv.rotary_plan(DIM, axes=(16, 24, 24)), held=held)
+    states = normal(rng, (B, L, ENC))
+    states[1, 5:] = 0
+    pos = torch.from_numpy(rng.integers(0, 64, (B, T, 3))).int().cuda()
+    return b, (normal(rng, (B, HID)), normal(rng, (B, T, HID)), pos), states, kn
+
+
+def test_block_holds_its_prompt_in_4_bits():
+    b, args, states, kn = block("nvfp4")
+    plain, _, _, _ = block("bf16")
+    lengths = ints(L, 5)
+    b.encode(states, lengths)
+    plain.encode(states, lengths)
+    # what is held: the keys and values of the other block, quantized
+    kv = plain.out["transformer_blocks.0.attn.add_kv_proj"].view(B, L, 2, KV, DIM)
+    assert b.cache.k_codes.shape == (B, KV, 48, DIM // 2)
+    assert b.cache.amax[0].item() == pytest.approx(math.sqrt(DIM) * kn.abs().max().item(), rel=1e-6)
+    assert plain.k.abs().max().item() <= b.cache.amax[0].item() * (1 + 2 ** -8)
+    assert plain.v.abs().max().item() <= b.cache.amax[1].item()
+    for x, codes, scales, amax in ((plain.k, b.cache.k_codes, b.cache.k_scales, b.cache.amax[0].item()),
+                                   (kv[:, :, 1], b.cache.v_codes, b.cache.v_scales, b.cache.amax[1].item())):
+        c, s, _ = oc.quantized_rows(bits_of(x.contiguous()), amax)
+        np.testing.assert_array_equal(codes[:, :, :L].cpu().numpy(), c.transpose(0, 2, 1, 3))
+        np.testing.assert_array_equal(scales[:, :, :L].cpu().numpy(), s.transpose(0, 2, 1, 3))
+    # and attended to
+    y = b(*args).clone()
+    q = b.out["transformer_blocks.0.attn.to_q"].view(B, T, HEADS, DIM)
+    k, v = numbers_of(b.cache)
+    check(b.attended, q, k, v, [L, 5])
+    assert y.shape == args[1].shape and bool(torch.isfinite(y).all())
+    # captured once, replayed after another prompt
+    g = capture(lambda: b(*args))
+    for seed in (1, 2):
+        other = normal(np.random.default_rng(seed), (B, L, ENC), 2.0)
+        b.encode(other, ints(3, 20))
+        got = g.replay().clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, b(*args))
+        q = b.out["transformer_blocks.0.attn.to_q"].view(B, T, HEADS, DIM)
+        k, v = numbers_of(b.cache)
+        check(b.attended, q, k, v, [3, 20])
+
+
+def test_block_refuses_other_ways_to_hold():
+    with pytest.raises(ValueError, match="held must be"):
+        block("fp8")
+
+
+class Steps:
+    """One layer of a model over a paged cache: projection, rotary with the key norm, the
+    cache, attention, projection and residual, all for `rows` tokens of `batch` entries."""
+
+    def __init__(self, rng, batch, pages, page, per):
+        self.hid, self.heads, self.kv, self.dim = 192, 6, 2, 64
+        n = (self.heads + 2 * self.kv) * self.dim
+        self.qkv = nv.quantize_weight(normal(rng, (n, self.hid), 0.08))
+        self.out = nv.quantize_weight(normal(rng, (self.hid, self.heads * self.dim), 0.05))
+        self.plan = nv.rotary_plan(self.dim)
+        self.norm = normal(rng, (self.dim,), 0.05, 1.0, torch.float32)
+        self.cache = nv.kv_cache(pages, page, self.kv, self.dim, k_amax=10.0, v_amax=4.0)
+        self.table = torch.from_numpy(rng.permutation(pages)[:batch * per].reshape(batch, per)).int().cuda()
+
+    def __call__(self, x, starts, positions, lengths):
+        b, t, _ = x.shape
+        p = nv.linear(x.view(b * t, -1), self.qkv, "blocks.0.qkv", weight_only=True)
+        p = p.view(b, t, self.heads + 2 * self.kv, self.dim)
+        q, k, v = p[:, :, :self.heads], p[:, :, self.heads:self.heads + self.kv], p[:, :, self.heads + self.kv:]
+        nv.rotary(q, positions, self.plan, k=k, q_weight=self.norm, k_weight=self.norm, out=q, k_out=k)
+        nv.cache_write(self.cache, k, v, starts, table=self.table)
+        a = nv.cache_attention(q, self.cache, lengths, starts=starts, table=self.table)
+        y = nv.linear(a.view(b * t, -1), self.out, "blocks.0.out", weight_only=True)
+        r, _ = nv.gated_norm(x, y.view(x.shape), norm=None)
+        return r, q, a
+
+
+def test_tokens_one_by_one_and_in_one_pass():
+    """Twelve tokens behind a prompt, each a step of its own, and the same tokens in one
+    causal pass: the attention of either over what its own cache holds by then."""
+    batch, page, per, prompt, new = 3, 16, 4, 29, 12
+    weights = np.random.default_rng(3)
+    one, many = (Steps(np.random.default_rng(7), batch, 14, page, per) for _ in range(2))
+    x = normal(weights, (batch, prompt + new, one.hid))
+    begin = [0, 0, 0]
+
+    def pos(first, n):
+        return (torch.arange(n, device="cuda", dtype=torch.int32) + first).expand(batch, n).contiguous()
+
+    for s in (one, many):
+        s(x[:, :prompt].contiguous(), ints(*begin), pos(0, prompt), ints(*[prompt] * batch))
+    for t in range(prompt, prompt + new):
+        n = [t + 1] * batch
+        r, q, a = one(x[:, t:t + 1].contiguous(), ints(*[t] * batch), pos(t, 1), ints(*n))
+        k, v = numbers_of(one.cache)
+        check(a, q, k, v, n, [t] * batch, one.table.cpu().numpy())
+        assert r.shape == (batch, 1, one.hid) and bool(torch.isfinite(r).all())
+    r, q, a = many(x[:, prompt:].contiguous(), ints(*[prompt] * batch), pos(prompt, new), ints(*[prompt + new] * batch))
+    k, v = numbers_of(many.cache)
+    check(a, q, k, v, [prompt + new] * batch, [prompt] * batch, many.table.cpu().numpy())
+
+
+def test_a_captured_step():
+    """One graph of a whole step, replayed token after token on tensors that grow in place,
+    beside the eager step on a cache of its own."""
+    batch, page, per = 2, 16, 3
+    eager, held = (Steps(np.random.default_rng(9), batch, 8, page, per) for _ in range(2))
+    rng = np.random.default_rng(10)
+    x = torch.zeros((batch, 1, eager.hid), dtype=torch.bfloat16, device="cuda")
+    starts, positions, lengths = ints(0, 0), ints(0, 0).view(batch, 1), ints(1, 1)
+    ws = nv.cache_attention_workspace(batch, 1, held.heads, held.kv, held.dim, page * per)
+    n = (held.heads + 2 * held.kv) * held.dim
+    p = torch.empty((batch, n), dtype=torch.bfloat16, device="cuda")
+    a = torch.empty((batch, 1, held.heads, held.dim), dtype=torch.bfloat16, device="cuda")
+    y, r = (torch.empty((batch, held.hid), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step():
+        nv.gemm_weight_only(x.view(batch, -1), held.qkv, out=p)
+        h = p.view(batch, 1, -1, held.dim)
+        q, k, v = h[:, :, :held.heads], h[:, :, held.heads:held.heads + held.kv], h[:, :, held.heads + held.kv:]
+        nv.rotary(q, positions, held.plan, k=k, q_weight=held.norm, k_weight=held.norm, out=q, k_out=k)
+        nv.cache_write(held.cache, k, v, starts, table=held.table)
+        nv.cache_attention(q, held.cache, lengths, starts=starts, table=held.table, out=a, workspace=ws)
+        nv.gemm_weight_only(a.view(batch, -1), held.out, out=y)
+        nv.gated_norm(x, y.view(x.shape), norm=None, residual_out=r.view(x.shape))
+
+    g = capture(step)
+    for t in held.cache[:4]:
+        t.zero_()
+    for t in range(20):
+        x.copy_(normal(rng, tuple(x.shape)))
+        at = [t, t + 7]
+        starts.copy_(ints(*at))
+        positions.copy_(ints(*at).view(batch, 1))
+        lengths.copy_(ints(t + 1, t + 8))
+        g.replay()
+        torch.cuda.synchronize()
+        want, _, _ = eager(x, starts, positions, lengths)
+        assert torch.equal(r.view(x.shape), want)
+    for s, m in zip(eager.cache[:4], held.cache[:4]):
+        assert torch.equal(s, m)
