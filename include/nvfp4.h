@@ -567,8 +567,9 @@ int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const
  *   0 <= M < 2^22; 0 <= N < 2^27; 0 < K < 2^30, K % 16 == 0.
  *   y_amax   optional device float, set to max |y| over the bf16 outputs (0 if
  *            there are none; not finite if one is NaN).
- * Made for up to 64 rows, over which the weight is read once; more rows read it
- * once for each 64 (nvfp4_gemm is the one for those).  Deterministic.
+ * Made for up to 32 rows, over which the weight is read once; more rows read it
+ * once for each 32 (nvfp4_gemm is the one for many).  Deterministic; how many rows
+ * a call has decides the order of a row's additions.
  */
 int w4_gemm_weight_only(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_scales,
                            const float* w_tensor_scale, const void* bias_bf16, int64_t M, int64_t N,

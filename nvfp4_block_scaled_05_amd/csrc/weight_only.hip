@@ -45,6 +45,46 @@ __device__ __forceinline__ uint32_t finish(const WeightOnly& a, float y, float s
   return bf16x2_rne(z, 0.0f);
 }
 
+// The waves' sums of a workgroup's tiles, in wave order, to outputs.
+template <int RT, int MT, int WAVES>
+__device__ __forceinline__ void join_waves(const WeightOnly& a, const f32x4 (&acc)[RT][MT], f32x4 (*park)[RT * MT][64],
+                                           int n0, int64_t m0) {
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_id();
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) park[wave][rt * MT + mt][lane] = acc[rt][mt];
+  __syncthreads();
+  const float sw = *a.tensor_scale;
+  uint32_t top = 0;
+  for (int tile = wave; tile < RT * MT; tile += WAVES) {
+    f32x4 y = park[0][tile][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) y += park[w][tile][lane];
+    const int n = n0 + 16 * (tile / MT) + 4 * g;
+    const int64_t row = m0 + 16 * (tile % MT) + m;
+    if (row >= a.M || n >= a.N) continue;
+    uint16_t out[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      out[r] = (uint16_t)finish(a, y[r], sw, min(n + r, a.N - 1));
+      if (n + r < a.N) top = max(top, (uint32_t)out[r] & 0x7FFFu);
+    }
+    uint16_t* to = a.y + row * a.N + n;
+    if (a.N % 4 == 0) {
+      *reinterpret_cast<u32x2*>(to) = u32x2{(uint32_t)out[0] | (uint32_t)out[1] << 16, (uint32_t)out[2] | (uint32_t)out[3] << 16};
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < a.N) to[r] = out[r];
+    }
+  }
+  if (a.amax) {
+    top = wave_max_u32(top);
+    if (lane == 0 && top) raise_amax(a.amax, top << 16);
+  }
+}
+
 template <int RT, int MT, int U, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void weight_only_kernel(WeightOnly a) {
   __shared__ f32x4 park[WAVES][RT * MT][64];
@@ -110,39 +150,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_only_kernel(WeightOnly a) {
       }
     }
   }
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) park[wave][rt * MT + mt][lane] = acc[rt][mt];
-  __syncthreads();
-  const float sw = *a.tensor_scale;
-  uint32_t top = 0;
-  for (int tile = wave; tile < RT * MT; tile += WAVES) {
-    f32x4 y = park[0][tile][lane];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) y += park[w][tile][lane];
-    const int n = n0 + 16 * (tile / MT) + 4 * g;
-    const int64_t row = m0 + 16 * (tile % MT) + m;
-    if (row >= a.M || n >= a.N) continue;
-    uint16_t out[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      out[r] = (uint16_t)finish(a, y[r], sw, min(n + r, a.N - 1));
-      if (n + r < a.N) top = max(top, (uint32_t)out[r] & 0x7FFFu);
-    }
-    uint16_t* to = a.y + row * a.N + n;
-    if (a.N % 4 == 0) {
-      *reinterpret_cast<u32x2*>(to) = u32x2{(uint32_t)out[0] | (uint32_t)out[1] << 16, (uint32_t)out[2] | (uint32_t)out[3] << 16};
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (n + r < a.N) to[r] = out[r];
-    }
-  }
-  if (a.amax) {
-    top = wave_max_u32(top);
-    if (lane == 0 && top) raise_amax(a.amax, top << 16);
-  }
+  join_waves<RT, MT, WAVES>(a, acc, park, n0, m0);
 }
 
 // One or two rows of x: the lanes lie along k, 32 each, so a wave reads 1 KiB of a
@@ -233,10 +241,130 @@ __global__ __launch_bounds__(256) void weight_only_vector_kernel(WeightOnly a, i
   }
 }
 
+// Straight into LDS, past the caches: 16 or 4 bytes of each lane to `lds` + lane * BYTES.
+template <int BYTES>
+__device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* lds) {
+  auto* to = (__attribute__((address_space(3))) void*)lds;
+  auto* at = (__attribute__((address_space(1))) void*)const_cast<uint8_t*>(from);
+  if constexpr (BYTES == 16)
+    __builtin_amdgcn_global_load_lds(at, to, 16, 0, 2);                       // 2: nt
+  else
+    __builtin_amdgcn_global_load_lds(at, to, 4, 0, 2);
+}
+
+template <int RT, int MT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void weight_only_lds_kernel(WeightOnly a) {
+  constexpr int kK = 256, kCodes = 16 * 128, kStage = RT * (kCodes + 256);
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[WAVES * 2 * kStage];
+  static_assert(sizeof(ring) >= WAVES * RT * MT * 1024, "the waves' sums meet in the ring");
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_id();
+  const int n0 = (int)blockIdx.x * (16 * RT);
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  const uint8_t *codes[RT][2], *scales[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 8 * i + lane / 8, piece = (lane & 7) ^ (row >> 1);
+      codes[rt][i] = a.codes + (int64_t)min(n0 + 16 * rt + row, a.N - 1) * (a.K / 2) + 16 * piece;
+    }
+    scales[rt] = a.scales + (int64_t)min(n0 + 16 * rt + lane / 4, a.N - 1) * (a.K / 16) + 4 * (lane & 3);
+  }
+  const uint16_t* x[MT];
+  bool live[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    live[mt] = m0 + 16 * mt + m < a.M;
+    x[mt] = a.x + (live[mt] ? m0 + 16 * mt + m : 0) * a.K + 32 * g;
+  }
+  uint8_t* own = ring + wave * (2 * kStage);
+  const uint32_t own_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)own;
+  const uint32_t at0 = own_at + (uint32_t)(m * 128 + ((g ^ (m >> 1)) << 4));
+  const uint32_t at1 = own_at + (uint32_t)(m * 128 + (((4 + g) ^ (m >> 1)) << 4));
+  const uint32_t at_s = own_at + (uint32_t)(RT * kCodes + m * 16 + 2 * g);
+  constexpr int kLoads = 3 * RT, kXLoads = 8 * MT;
+  auto fetch = [&](int step, int stage) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) to_lds<16>(codes[rt][i] + (uint32_t)step * 128u, own + stage * kStage + rt * kCodes + i * 1024);
+      to_lds<4>(scales[rt] + (uint32_t)step * 16u, own + stage * kStage + RT * kCodes + rt * 256);
+    }
+  };
+  u32x4 xv[2][2][MT][4];
+  auto load_x = [&](int step, u32x4 (&v)[2][MT][4]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][mt][i] = *reinterpret_cast<const u32x4*>(x[mt] + step * kK + 128 * u + 8 * i);
+  };
+  f32x4 acc[RT][MT] = {};
+  auto multiply = [&](int stage, const u32x4 (&v)[2][MT][4]) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      u32x4 c[2];
+      uint32_t sc[2];
+      const uint32_t to = (uint32_t)(stage * kStage + rt * kCodes), to_s = (uint32_t)(stage * kStage + rt * 256);
+      asm volatile(
+          "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_u16 %2, %6\n\tds_read_u16 %3, %6 offset:8\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(c[0]), "=&v"(c[1]), "=&v"(sc[0]), "=&v"(sc[1])
+          : "v"(at0 + to), "v"(at1 + to), "v"(at_s + to_s)
+          : "memory");
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float s0 = __builtin_amdgcn_cvt_f32_fp8(sc[u], 0), s1 = __builtin_amdgcn_cvt_f32_fp8(sc[u], 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bf16x8 w = decode8_bf16(c[u][i], i < 2 ? s0 : s1);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            acc[rt][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, v[u][mt][i]), acc[rt][mt], 0, 0, 0);
+        }
+      }
+    }
+  };
+  const int steps = a.K / kK;
+  static_assert(kLoads + kXLoads < 64, "the wait's count is 6 bits");
+  constexpr int kWait = kLoads + kXLoads;
+  auto turn = [&](int t, int stage, u32x4 (&now)[2][MT][4], u32x4 (&next)[2][MT][4]) {
+    if (t + WAVES < steps) {
+      load_x(t + WAVES, next);
+      fetch(t + WAVES, stage ^ 1);
+      __builtin_amdgcn_s_waitcnt(0x0F70 | (kWait & 15) | (kWait >> 4) << 14);    // vmcnt: this step's are in
+    } else {
+      __builtin_amdgcn_s_waitcnt(0x0F70);
+    }
+    asm volatile("" ::: "memory");
+    multiply(stage, now);
+  };
+  int t = wave;
+  if (t < steps) {
+    load_x(t, xv[0]);
+    fetch(t, 0);
+  }
+  while (t < steps) {
+    turn(t, 0, xv[0], xv[1]);
+    t += WAVES;
+    if (t >= steps) break;
+    turn(t, 1, xv[1], xv[0]);
+    t += WAVES;
+  }
+  __syncthreads();                             // the rings are free
+  join_waves<RT, MT, WAVES>(a, acc, reinterpret_cast<f32x4(*)[RT * MT][64]>(ring), n0, m0);
+}
+
 template <int RT, int MT, int U, int WAVES>
 void launch_rows(const WeightOnly& a, hipStream_t stream) {
   const dim3 grid((unsigned)((a.N + 16 * RT - 1) / (16 * RT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
   weight_only_kernel<RT, MT, U, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a);
+}
+template <int RT, int MT, int WAVES>
+void launch_lds(const WeightOnly& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.N + 16 * RT - 1) / (16 * RT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+  weight_only_lds_kernel<RT, MT, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -253,17 +381,22 @@ hipError_t launch_weight_only(WeightOnly a, hipStream_t stream) {
       weight_only_vector_kernel<2><<<grid, 256, 0, stream>>>(a, ways);
     return hipGetLastError();
   }
-  const int64_t tiles = (a.N + 15) / 16;
-  if (a.M <= 32 && tiles >= 4 * 192)
-    a.M <= 16 ? launch_rows<4, 1, 1, 8>(a, stream) : launch_rows<4, 2, 1, 8>(a, stream);
-  else if (tiles >= 2 * 192)
-    a.M <= 16   ? launch_rows<2, 1, 2, 8>(a, stream)
-    : a.M <= 32 ? launch_rows<2, 2, 1, 8>(a, stream)
-                : launch_rows<2, 4, 1, 8>(a, stream);
-  else
-    a.M <= 16   ? launch_rows<1, 1, 4, 8>(a, stream)
-    : a.M <= 32 ? launch_rows<1, 2, 2, 8>(a, stream)
-                : launch_rows<1, 4, 1, 8>(a, stream);
+  const int64_t tiles = (a.N + 15) / 16, cus = compute_units();
+  const bool one = a.M <= 16, large = tiles >= 3 * cus;
+  if (a.K % 256 == 0 && (one || large)) {
+    if (!one)
+      launch_lds<4, 2, 8>(a, stream);
+    else if (large && a.M > 8)
+      tiles > 4 * cus ? launch_lds<4, 1, 4>(a, stream) : launch_lds<4, 1, 8>(a, stream);
+    else if (2 * tiles >= 3 * cus)
+      launch_lds<2, 1, 8>(a, stream);
+    else
+      launch_lds<1, 1, 8>(a, stream);
+  } else if (2 * tiles >= 3 * cus) {
+    one ? launch_rows<2, 1, 2, 8>(a, stream) : launch_rows<2, 2, 1, 8>(a, stream);
+  } else {
+    one ? launch_rows<1, 1, 4, 8>(a, stream) : launch_rows<1, 2, 2, 8>(a, stream);
+  }
   return hipGetLastError();
 }
 

@@ -49,6 +49,24 @@ def test_shapes(rows, n, k):
     check(nv.gemm_weight_only(x, w), x, w)
 
 
+@pytest.mark.parametrize("n,k", [(6150, 256), (6144, 528), (12300, 512), (12288, 272), (16500, 768), (500, 4096)])
+@pytest.mark.parametrize("rows", [1, 2, 3, 8, 9, 16, 31, 50])
+def test_every_kernel(rows, n, k):
+    """Output counts and inner sizes on both sides of the launch's rules, ragged last tiles; NaN and
+    infinite rows of x beside the others."""
+    rng = np.random.default_rng(n + k + rows)
+    x, w = normal(rng, (rows, k)), weight(rng, n, k)
+    bias, amax = normal(rng, (n,)), torch.zeros(1, device="cuda")
+    got = nv.gemm_weight_only(x, w, bias=bias, y_amax=amax)
+    check(got, x, w, bias)
+    assert amax.item() == got.abs().max().item()
+    if rows > 1:
+        x[rows // 2, k - 1] = float("nan")
+        bad = nv.gemm_weight_only(x, w, bias=bias)
+        keep = [r for r in range(rows) if r != rows // 2]
+        assert torch.isnan(bad[rows // 2]).all() and torch.equal(bad[keep], got[keep])
+
+
 @pytest.mark.parametrize("rows", [65, 129, 300])
 def test_more_rows_than_one_pass(rows):
     rng = np.random.default_rng(rows)
@@ -73,12 +91,12 @@ def test_bias_epilogue_and_amax(rows, n, gelu):
 
 
 def test_rows_do_not_depend_on_each_other():
-    """A row's bits are the same alone and among others of the same tile count; NaN stays in its row."""
+    """A row's bits are the same wherever it stands; NaN stays in its row."""
     rng = np.random.default_rng(1)
     x, w = normal(rng, (16, 1040)), weight(rng, 50, 1040)
     y = nv.gemm_weight_only(x, w)
-    for r in (0, 7, 15):
-        assert np.array_equal(bits_of(nv.gemm_weight_only(x[r:r + 1], w)), bits_of(y[r:r + 1]))
+    order = torch.from_numpy(rng.permutation(16)).cuda()
+    assert np.array_equal(bits_of(nv.gemm_weight_only(x[order].contiguous(), w)), bits_of(y[order]))
     x[3, 1000] = float("nan")
     x[5, 0] = float("inf")
     amax = torch.zeros(1, device="cuda")
