@@ -564,7 +564,7 @@ int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const
  *   x_bf16 [M, K], 16-byte aligned; w_codes [N, K/2], w_scales [N, K/16],
  *   w_tensor_scale [1] as nvfp4_quantize wrote them (codes 8-byte aligned);
  *   bias_bf16 optional [N]; y_bf16 [M, N], 8-byte aligned.
- *   0 <= M < 2^22; 0 <= N < 2^27; 0 < K < 2^30, K % 16 == 0.
+ *   0 <= M < 2^20; 0 <= N < 2^27; 0 < K < 2^30, K % 16 == 0.
  *   y_amax   optional device float, set to max |y| over the bf16 outputs (0 if
  *            there are none; not finite if one is NaN).
  * Made for up to 32 rows, over which the weight is read once; more rows read it
@@ -579,7 +579,7 @@ int w4_gemm_weight_only(const void* x_bf16, const uint8_t* w_codes, const uint8_
  * A cache: pages of tokens' keys and values, a page's tokens one after another
  * for each head.
  *   k_codes, v_codes    [pages, kv_heads, page_size, dim/2], 16-byte aligned.
- *   k_scales, v_scales  [pages, kv_heads, page_size, dim/16], 2-byte aligned.
+ *   k_scales, v_scales  [pages, kv_heads, page_size, dim/16], 4-byte aligned.
  *   amax        device float [2]: the static amax of keys and of values, finite
  *               and positive; they stay as they are while the cache is in use.
  *   table       optional [batch, table_pages] int32: the pages of each entry's

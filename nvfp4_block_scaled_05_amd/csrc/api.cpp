@@ -107,8 +107,8 @@ bool null_cache(const kv_cache& c) {
   return !c.k_codes || !c.k_scales || !c.v_codes || !c.v_scales || !c.amax;
 }
 bool misaligned_cache(const kv_cache& c) {
-  return !aligned(c.k_codes, 16) || !aligned(c.v_codes, 16) || !aligned(c.k_scales, 2) ||
-         !aligned(c.v_scales, 2) || !aligned(c.amax, 4) || !aligned(c.table, 4);
+  return !aligned(c.k_codes, 16) || !aligned(c.v_codes, 16) || !aligned(c.k_scales, 4) ||
+         !aligned(c.v_scales, 4) || !aligned(c.amax, 4) || !aligned(c.table, 4);
 }
 nvfp4::Cache cache_of(const kv_cache& c) {
   int shift = 0;
@@ -577,7 +577,7 @@ int w4_gemm_weight_only(const void* x_bf16, const uint8_t* w_codes, const uint8_
   const bool empty = M == 0 || N == 0;
   if (!empty && (!x_bf16 || !w_codes || !w_scales || !w_tensor_scale || !y_bf16))
     return NVFP4_ERR_NULL;
-  if (K == 0 || K % 16 != 0 || K >= (1 << 30) || M >= (1 << 22) || N >= (1 << 27))
+  if (K == 0 || K % 16 != 0 || K >= (1 << 30) || M >= (1 << 20) || N >= (1 << 27))
     return NVFP4_ERR_SHAPE;
   if (!aligned(x_bf16, 16) || !aligned(w_codes, 8) || !aligned(w_tensor_scale, 4) ||
       !aligned(bias_bf16, 2) || !aligned(y_bf16, 8) || !aligned(y_amax, 4))

@@ -10,7 +10,7 @@
 // rounded to fp16 (2^-11 relative; their sum is not rounded); all else is binary32, and
 // the values' tensor scale is applied with the division by the sum.
 //
-// cache_few_kernel: up to 64 query rows a kv head, bound by the stream of codes, which
+// cache_few_kernel: up to 32 query rows a kv head, bound by the stream of codes, which
 // go from memory to registers in the order in which the matrix instructions take them.
 // cache_many_kernel: tiles of keys decoded into LDS for all of a workgroup's rows.
 // cache_join_kernel: joins the workgroups that share a unit's keys.
@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {               // inc
 // The lengths of the first 64 entries are kept, a lane each: one wait for most calls.
 template <int KEYS>
 struct Work {
-  static constexpr uint32_t kStart = KEYS == 128 ? 2 : 3;
+  static constexpr uint32_t kStart = KEYS == 128 ? 3 : 5;
   uint32_t total, share;         // what all units count, and a workgroup's part
   uint32_t units;                // of an entry
   int seen0;                     // keys that this lane's entry sees, and what a unit of it and
@@ -522,7 +522,7 @@ struct FewRows {
 };
 
 template <int D, bool EXACT, int RT>
-__global__ __launch_bounds__(256, RT == 4 ? 1 : 2) void cache_few_kernel(CacheAttention a) {
+__global__ __launch_bounds__(256, 2) void cache_few_kernel(CacheAttention a) {
   constexpr int kKeys = 128;                   // of a tile: a step of 32 for each wave
   constexpr int kRow = D + 4;                  // of LDS, in floats
   using F = FewRows<D, EXACT, RT>;
@@ -1091,7 +1091,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
 
 // How a call is run.
 struct Plan {
-  int few;                       // 16-row tiles of cache_few_kernel: 1, 2, 4; 0: cache_many_kernel
+  int few;                       // 16-row tiles of cache_few_kernel, 1 or 2; 0: cache_many_kernel
   int64_t rows, row_tiles, units, slot_rows;
   int workers, least;
 };
@@ -1102,14 +1102,14 @@ Plan plan_for(int64_t batch, int64_t queries, int64_t heads, int64_t kv_heads, i
   Plan p{};
   const int64_t cus = compute_units();
   p.rows = queries * (heads / kv_heads);
-  if (p.rows <= 64) {
-    p.few = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+  if (p.rows <= 32) {
+    p.few = p.rows <= 16 ? 1 : 2;
     p.row_tiles = 1;
     p.units = batch * kv_heads;
     p.slot_rows = p.rows;
     const int64_t tiles = (capacity + 127) / 128;
     p.least = 2;
-    if (tiles > 2) p.workers = (int)(2 * cus);
+    if (p.units <= cus ? tiles > 2 : p.units < 4 * cus && tiles > 8) p.workers = (int)(2 * cus);
   } else {
     p.row_tiles = (p.rows + 127) / 128;
     p.units = batch * kv_heads * p.row_tiles;
@@ -1129,10 +1129,8 @@ template <int D, bool EXACT>
 void launch_few(const CacheAttention& a, int few, dim3 grid, hipStream_t stream) {
   if (few == 1)
     cache_few_kernel<D, EXACT, 1><<<grid, 256, 0, stream>>>(a);
-  else if (few == 2)
-    cache_few_kernel<D, EXACT, 2><<<grid, 256, 0, stream>>>(a);
   else
-    cache_few_kernel<D, EXACT, 4><<<grid, 256, 0, stream>>>(a);
+    cache_few_kernel<D, EXACT, 2><<<grid, 256, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -1173,11 +1171,11 @@ hipError_t launch_cache_attention(CacheAttention a, void* workspace, size_t work
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.workers) return e;
   const int n = p.few ? (dp == 64 ? 16 : 8) : 1, per = 256 / (dp / 4) / n;        // rows a workgroup of the join has
-  const int64_t rows = std::min<int64_t>(p.rows, p.few ? 64 : 128);
+  const int64_t rows = std::min<int64_t>(p.rows, p.few ? 32 : 128);
   const dim3 join((unsigned)(p.units * ((rows + per - 1) / per)));
   if (p.few)
-    dp == 64 ? cache_join_kernel<64, 128, 64, 16><<<join, 256, 0, stream>>>(a)
-             : cache_join_kernel<128, 128, 64, 8><<<join, 256, 0, stream>>>(a);
+    dp == 64 ? cache_join_kernel<64, 128, 32, 16><<<join, 256, 0, stream>>>(a)
+             : cache_join_kernel<128, 128, 32, 8><<<join, 256, 0, stream>>>(a);
   else
     dp == 64 ? cache_join_kernel<64, 64, 128, 1><<<join, 256, 0, stream>>>(a)
              : cache_join_kernel<128, 64, 128, 1><<<join, 256, 0, stream>>>(a);

@@ -383,7 +383,9 @@ hipError_t launch_weight_only(WeightOnly a, hipStream_t stream) {
   }
   const int64_t tiles = (a.N + 15) / 16, cus = compute_units();
   const bool one = a.M <= 16, large = tiles >= 3 * cus;
-  if (a.K % 256 == 0 && (one || large)) {
+  // (the rings take 16 and 4 bytes at a time from rows that begin so)
+  const bool placed = a.K % 256 == 0 && ((uintptr_t)a.codes & 15) == 0 && ((uintptr_t)a.scales & 3) == 0;
+  if (placed && (one || large)) {
     if (!one)
       launch_lds<4, 2, 8>(a, stream);
     else if (large && a.M > 8)

@@ -61,7 +61,8 @@ def test_without_a_table(queries):
     (1, 1, 8, 2, 64, 80, [5100], False), (5, 1, 4, 1, 256, 12, [3000, 1, 0, 700, 2049], False),
     (1, 90, 1, 1, 64, 30, [1900], False), (3, 25, 3, 1, 64, 30, [1900, 5, 1200], True),
     (2, 9, 4, 1, 128, 18, [2300, 1111], True), (2, 100, 2, 1, 64, 30, [1900, 700], True),
-    (70, 1, 2, 1, 16, 24, [(37 * i) % 385 for i in range(70)], False)])
+    (70, 1, 2, 1, 16, 24, [(37 * i) % 385 for i in range(70)], False),
+    (150, 1, 8, 4, 64, 20, [(97 * i) % 1281 for i in range(150)], False)])
 def test_keys_dealt_over_workgroups(dim, batch, queries, heads, kv, page, per, lengths, causal):
     run(np.random.default_rng(page + dim), batch, queries, heads, kv, dim, page, per, lengths, causal=causal)
 

@@ -173,7 +173,7 @@ BAD_CACHES = [dict(pages=0), dict(pages=1 << 31), dict(size=0), dict(size=24), d
               dict(heads=1 << 17), dict(dim=0), dict(dim=72), dict(dim=144), dict(pages=1),
               dict(table=A, per=-1), dict(table=A, per=2, size=48), dict(table=A, per=1 << 28),
               dict(size=(1 << 31) - 16)]
-BAD_PLACES = [dict(kc=A + 8), dict(vc=A + 4), dict(ks=A + 1), dict(vs=A + 1), dict(amax=A + 2),
+BAD_PLACES = [dict(kc=A + 8), dict(vc=A + 4), dict(ks=A + 2), dict(vs=A + 1), dict(amax=A + 2),
               dict(table=A + 2, per=2)]
 
 
@@ -234,7 +234,7 @@ def test_weight_only_c(lib):  # noqa: F811
     assert late(f()) and late(f(m=0, x=None)) and late(f(n=0, codes=None))
     for kw in (dict(x=None), dict(codes=None), dict(scales=None), dict(ts=None), dict(y=None)):
         assert f(**kw) == NULL
-    for kw in (dict(m=-1), dict(k=0), dict(k=72), dict(k=1 << 30), dict(m=1 << 22), dict(n=1 << 27)):
+    for kw in (dict(m=-1), dict(k=0), dict(k=72), dict(k=1 << 30), dict(m=1 << 20), dict(n=1 << 27)):
         assert f(**kw) == SHAPE, kw
     for kw in (dict(x=A + 8), dict(codes=A + 4), dict(ts=A + 2), dict(bias=A + 1), dict(y=A + 4), dict(amax=A + 2)):
         assert f(**kw) == ALIGN, kw

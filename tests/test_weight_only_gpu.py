@@ -67,6 +67,22 @@ def test_every_kernel(rows, n, k):
         assert torch.isnan(bad[rows // 2]).all() and torch.equal(bad[keep], got[keep])
 
 
+@pytest.mark.parametrize("rows", [1, 2, 7, 20])
+def test_weights_at_any_place(rows):
+    """Codes at 8 bytes and scales at any byte, as slices of one checkpoint buffer lie."""
+    rng = np.random.default_rng(rows)
+    n, k = 12300, 512
+    w, x = weight(rng, n, k), normal(rng, (rows, k))
+    buffer = torch.zeros(n * k // 2 + n * k // 16 + 64, dtype=torch.uint8, device="cuda")
+    codes = buffer[8:8 + n * k // 2].view(n, k // 2)
+    scales = buffer[8 + n * k // 2 + 3:][:n * k // 16].view(n, k // 16)
+    codes.copy_(w.codes)
+    scales.copy_(w.scales)
+    moved = nv.Nvfp4Tensor(codes, scales, w.tensor_scale, k)
+    assert codes.data_ptr() % 16 == 8 and scales.data_ptr() % 2 == 1
+    check(nv.gemm_weight_only(x, moved), x, w)
+
+
 @pytest.mark.parametrize("rows", [65, 129, 300])
 def test_more_rows_than_one_pass(rows):
     rng = np.random.default_rng(rows)
