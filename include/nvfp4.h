@@ -2,7 +2,8 @@
  * nvfp4.h -- C ABI of the MI355X (gfx950) NVFP4 library: two-level NVFP4
  * quantize / dequantize, the block-scaled W4A4 GEMM that consumes the
  * quantized operands, a bf16 passthrough GEMM for layers kept in higher
- * precision, and the layer predicate that chooses between the two.
+ * precision, the layer predicate that chooses between the two, the operators
+ * between the linears and a key/value cache in NVFP4.
  *
  * Sources.  The pages this library follows describe NVFP4 only in outline:
  *   [P1] "英伟达B200狂飙10.2倍！AI绘图告别龟速！" (nmedialink.com), section

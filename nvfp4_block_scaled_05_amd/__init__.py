@@ -1,6 +1,7 @@
 """MI355X (gfx950) NVFP4: two-level quantize / dequantize, the block-scaled
-W4A4 GEMM of the DiT linear layers, a bf16 passthrough GEMM, and the layer
-predicate -- Python face of the C ABI in include/nvfp4.h.
+W4A4 GEMM of the DiT linear layers, a bf16 passthrough GEMM, the layer
+predicate, the operators between the linears, and a key/value cache in the
+same format -- Python face of the C ABI in include/nvfp4.h.
 
 Functions mirror the C entry points by name.  Tensors are torch tensors on the
 current HIP device (bf16 data as ``torch.bfloat16``, codes and scales as

@@ -29,7 +29,7 @@ namespace {
 // of KEYS, at least one (an entry that sees nothing still has zeros to write).  All
 // units' tiles, entry after entry, are dealt to the workgroups in equal ranges, whatever
 // the lengths.  A unit's beginning costs about as much as kStart tiles, and counts as so
-// many before its first: with 16 entries of 1 to 8192 keys @@
+// many before its first: 16 entries of 0 to 8192 keys take 23 us instead of 36.
 
 // The keys that some query of entry b sees.
 __device__ __forceinline__ int seen_by(const CacheAttention& a, int64_t b) {
@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {               // inc
 // The lengths of the first 64 entries are kept, a lane each: one wait for most calls.
 template <int KEYS>
 struct Work {
-  static constexpr uint32_t kStart = KEYS == 128 ? 3 : 5;
+  static constexpr uint32_t kStart = KEYS == 128 ? 3 : 5;       // (1 and 2: 27 and 26 us there, 3: 25)
   uint32_t total, share;         // what all units count, and a workgroup's part
   uint32_t units;                // of an entry
   int seen0;                     // keys that this lane's entry sees, and what a unit of it and
@@ -191,6 +191,13 @@ __device__ __forceinline__ float rows_sum(float v) {
 //   V operand   columns m D / 16 ..., of those keys; pairs of keys are zipped nibble by
 //               nibble before the conversion, which then gives pairs along the keys
 // so nothing is exchanged between lanes.
+//
+// An element of K costs one instruction to decode and one of V one and a quarter, a
+// quarter of the vector units' time at the rate of memory; what counts is bytes in flight:
+// 131071 keys of 8 heads (151 MB, 29 us at a copy's rate) take 34 us and 4.7 for the join,
+// 50 with a step ahead in registers; 16 entries of 0 to 8192 keys (61 MB) 20 and 4.  Of
+// both, about 8 us are the chain of a workgroup's first loads (lengths, queries and table,
+// codes) and its end.
 constexpr int kStages = 4;
 
 template <int D>
@@ -679,7 +686,9 @@ __global__ __launch_bounds__(256, 2) void cache_few_kernel(CacheAttention a) {
 
 // Joins what the workgroups left of a unit whose tiles several of them had: partial
 // sums weighted by 2^(their maximum - the largest).  A row has N groups of D / 4 lanes,
-// each of which takes every N-th of its parts in order; they meet in LDS.
+// each of which takes every N-th of its parts in order; they meet in LDS.  4 to 5 us where
+// rows are few (the lengths' and the parts' latencies), 8.4 for 64 units of 128 rows, whose
+// parts (up to 67 MB) are still in the last-level cache.
 template <int D, int KEYS, int TILE_ROWS, int N>
 __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttention a) {
   constexpr int G = D / 4, R = 256 / G / N;    // rows of a workgroup
@@ -754,8 +763,18 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttention a) {
 // ------------------------------------------------------------------ many query rows
 //
 // The waves of a workgroup have 32 rows each and share tiles of 64 keys, decoded into
-// LDS in fp16: while a tile is used, the next one's blocks (a thread has kItems of
-// them) are decoded into the other buffers and the one after that is on its way.
+// LDS in fp16: while a tile is used, the next one's blocks are decoded into the other
+// buffers, between the matrix instructions of the scores, and the one after that is on
+// its way.
+//
+// 4096 queries of 4608 keys of 24 heads: 253 to 272 us (the kernel over bf16 keys: 237 to
+// 250), 0.85 to 0.92 PFLOP/s; decoding costs 54 of them (timed without), since each of 32 row
+// tiles does it again.  A SIMD's time is nearly the sum of its matrix products (41%) and
+// its vector instructions (52%, a third of them the decode).  2 x 16384 queries of 512 and
+// 77 keys: 206 to 230; 2 x 128 queries of four heads over 16384 and 9001 keys in pages of
+// 64: 76 to 85 and 8 for the join.  Not faster: one block of 32 keys after the other (309 us
+// for 291, the same otherwise), V's pieces in an order without bank conflicts, wave
+// priorities around the products, pages looked up tile by tile (108 us for 97).
 template <int DP, int WAVES, bool PAGED>
 struct ManyRows {
   using A = Attend<DP, 2, true>;
@@ -1090,12 +1109,21 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
 }
 
 // How a call is run.
+//   Up to 32 rows a kv head: cache_few_kernel (32 rows of 16 entries of 4096 keys 44 us,
+// 66 by tiles in LDS; 48 rows 92 in three tiles of 16 against 70).
+//   Otherwise tiles of 128 rows.
+//   Keys are dealt to two workgroups a compute unit, all that fit, where units alone leave
+// some idle: 8 units of 131071 keys; from 256 units on only long ones (512 units of 512 keys
+// 17.9 us dealt, 14.6 whole; lengths may be very unequal), from 1024 on none (2048 units of
+// 1 to 512 keys 173 and 42, 1024 of 1 to 2048 55 and 53).
 struct Plan {
   int few;                       // 16-row tiles of cache_few_kernel, 1 or 2; 0: cache_many_kernel
   int64_t rows, row_tiles, units, slot_rows;
   int workers, least;
 };
 
+// A cache holds head sizes as they are; the kernels pad them to one of two in registers and
+// LDS.
 int padded_dim(int64_t dim) { return dim <= 64 ? 64 : 128; }
 
 Plan plan_for(int64_t batch, int64_t queries, int64_t heads, int64_t kv_heads, int64_t capacity) {
@@ -1116,6 +1144,7 @@ Plan plan_for(int64_t batch, int64_t queries, int64_t heads, int64_t kv_heads, i
     p.slot_rows = 128;
     const int64_t tiles = (capacity + 63) / 64;
     p.least = 4;
+    // (768 units of 72 tiles: 283 us dealt, 261 whole; 64 units of 397 tiles on average 84 + 8)
     if (tiles > 4 && p.units <= cus) p.workers = (int)(2 * cus);
   }
   return p;

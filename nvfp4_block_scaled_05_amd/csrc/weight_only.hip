@@ -1,10 +1,16 @@
 // w4_gemm_weight_only: a few rows of bf16 activations, not quantized, times an NVFP4
 // weight.
 //
-// A wave has 16 weight rows and up to 64 rows of x and every WAVES-th step of 128 k; the
-// waves of a workgroup are joined in LDS, in wave order.  A code times its block scale
+// Bound by the stream of codes, 0.5625 bytes an element: at a copy's 5.16 TB/s a weight
+// of 28672 x 8192 takes 25.6 us, one of 4096 x 4096 1.8.  A code times its block scale
 // has at most six significant bits, so bf16 holds it and the products are those of the
-// formula.  Bound by the stream of codes.
+// formula; sums are binary32.
+//
+// weight_only_vector_kernel: one or two rows, by dot products along k.
+// weight_only_lds_kernel: matrix instructions over codes that reach LDS in whole lines.
+// weight_only_kernel: the same with codes straight to registers, for any K and any place
+// of the codes, and for 17 to 32 rows of a small weight.
+// All of them split K over the waves of a workgroup, which meet in LDS in a fixed order.
 #include "device_common.hpp"
 #include "kernels.hpp"
 
@@ -85,6 +91,11 @@ __device__ __forceinline__ void join_waves(const WeightOnly& a, const f32x4 (&ac
   }
 }
 
+// A wave has RT tiles of 16 weight rows and MT of 16 rows of x, and steps of U times 128
+// k, whose codes are on their way together; x is read from the caches step by step.  The
+// matrix instruction wants 16 bytes of 16 weight rows from neighbouring lanes, so every
+// load touches 64 places, one a cycle: 28672 x 8192 takes 45 to 58 us for 4 rows, whatever
+// RT (1, 2, 4), U (1 to 8) and WAVES (2 to 16), and no longer for more bytes in flight.
 template <int RT, int MT, int U, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void weight_only_kernel(WeightOnly a) {
   __shared__ f32x4 park[WAVES][RT * MT][64];
@@ -156,7 +167,10 @@ __global__ __launch_bounds__(64 * WAVES) void weight_only_kernel(WeightOnly a) {
 // One or two rows of x: the lanes lie along k, 32 each, so a wave reads 1 KiB of a
 // weight row at a time and keeps its part of x in registers over kRows weight rows.
 // Sums over the lanes come last.  The dot instruction takes pairs of codes as bf16
-// without their scale; a block's sum is multiplied by it in binary32.
+// without their scale; a block's sum is multiplied by it in binary32, so an element costs
+// about one instruction (with matrix instructions, two to decode it).  28672 x 8192: 24 to
+// 25 us for one row (43 with matrix instructions), 5.2 TB/s, 31 for two; 8192 x 28672 28;
+// 4096 x 4096 4.7, of which the codes' stream is 1.8 and the rest is a launch's latencies.
 constexpr int kRows = 8;                       // weight rows of a wave
 constexpr int kChunk = 2048;                   // k of a wave
 
@@ -252,6 +266,14 @@ __device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* lds) {
     __builtin_amdgcn_global_load_lds(at, to, 4, 0, 2);
 }
 
+// Steps of 256 k, 128 bytes of each weight row, in a ring of two stages of LDS of each
+// wave's own, loaded 8 rows at a time so that a load touches 16 places instead of 64; the
+// 16-byte pieces of a row are permuted by XOR, so that the reads of 16 rows spread over
+// the banks.  x goes to registers a step ahead, before the codes (loads return in order).
+// 28672 x 8192: 37 us for 4 rows (45 by the kernel above), 46 for 16 (56), 65 for 32 (71);
+// 4096 x 4096 5.7 and 7.3 for 3 and 16 (6.8 and 8.5); 14336 x 4096 15.1 for 16, 17 to 19
+// with bias, GELU and amax.  What is left for 16 rows is x: its loads touch 64 places
+// each, four times as many as the codes'.
 template <int RT, int MT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void weight_only_lds_kernel(WeightOnly a) {
   constexpr int kK = 256, kCodes = 16 * 128, kStage = RT * (kCodes + 256);
@@ -381,6 +403,13 @@ hipError_t launch_weight_only(WeightOnly a, hipStream_t stream) {
       weight_only_vector_kernel<2><<<grid, 256, 0, stream>>>(a, ways);
     return hipGetLastError();
   }
+  // More weight rows a wave read x less often, fewer leave more workgroups: four tiles from
+  // 3 of them a compute unit on (16 rows of 14336 x 4096: 15.0 us with four tiles, 15.7 with
+  // two, 20.2 with one; of 4096 x 4096 12.6, 9.0 and 7.2), in workgroups of four waves, two a
+  // compute unit, where those are more than one each (28672 x 8192: 46 us against 50); up to 8
+  // rows, where x is small, two (13.1 against 13.9; 37.5 against 42).  17 to 32 rows of a large
+  // weight 18.6 against 20.0 in registers, of a small one 40 against 12.  More than 32 rows in
+  // passes of 32: 64 rows of 28672 x 8192 124 us, in one pass of four tiles of x 159.
   const int64_t tiles = (a.N + 15) / 16, cus = compute_units();
   const bool one = a.M <= 16, large = tiles >= 3 * cus;
   // (the rings take 16 and 4 bytes at a time from rows that begin so)
