@@ -44,52 +44,81 @@ __device__ __forceinline__ uint32_t load2(const uint8_t* p) {
 }
 
 // One output: tensor scale, bias, GELU, bf16.
-__device__ __forceinline__ uint32_t finish(const WeightOnly& a, float y, float sw, int n) {
-  float z = y * sw;
-  if (a.bias) z += bf16_bits_to_f32(a.bias[n]);
+__device__ __forceinline__ uint32_t finish(const WeightOnly& a, float y, float sw, float bias) {
+  float z = __builtin_fmaf(y, sw, bias);
   if (a.epilogue == NVFP4_EPI_GELU) z = gelu_erf(z);
   return bf16x2_rne(z, 0.0f);
 }
 
-// The waves' sums of a workgroup's tiles, in wave order, to outputs.
-template <int RT, int MT, int WAVES>
-__device__ __forceinline__ void join_waves(const WeightOnly& a, const f32x4 (&acc)[RT][MT], f32x4 (*park)[RT * MT][64],
-                                           int n0, int64_t m0) {
-  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_id();
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) park[wave][rt * MT + mt][lane] = acc[rt][mt];
+// Raises the amax word to the largest magnitude of a workgroup, each wave's in its lanes'
+// `top`.  One atomic a workgroup, without a look at the word before: few end at a time,
+// and a look would be waited for.
+template <int WAVES>
+__device__ __forceinline__ void raise_by(const WeightOnly& a, uint32_t top) {
+  __shared__ uint32_t tops[WAVES];
+  if (!a.amax) return;
+  top = wave_max_u32(top);
+  if ((threadIdx.x & 63) == 0) tops[wave_id()] = top;
   __syncthreads();
-  const float sw = *a.tensor_scale;
-  uint32_t top = 0;
-  for (int tile = wave; tile < RT * MT; tile += WAVES) {
-    f32x4 y = park[0][tile][lane];
+  if (threadIdx.x == 0) {
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) y += park[w][tile][lane];
-    const int n = n0 + 16 * (tile / MT) + 4 * g;
-    const int64_t row = m0 + 16 * (tile % MT) + m;
-    if (row >= a.M || n >= a.N) continue;
-    uint16_t out[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      out[r] = (uint16_t)finish(a, y[r], sw, min(n + r, a.N - 1));
-      if (n + r < a.N) top = max(top, (uint32_t)out[r] & 0x7FFFu);
-    }
-    uint16_t* to = a.y + row * a.N + n;
-    if (a.N % 4 == 0) {
-      *reinterpret_cast<u32x2*>(to) = u32x2{(uint32_t)out[0] | (uint32_t)out[1] << 16, (uint32_t)out[2] | (uint32_t)out[3] << 16};
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (n + r < a.N) to[r] = out[r];
-    }
-  }
-  if (a.amax) {
-    top = wave_max_u32(top);
-    if (lane == 0 && top) raise_amax(a.amax, top << 16);
+    for (int w = 1; w < WAVES; ++w) top = max(top, tops[w]);
+    if (top) atomicMax(a.amax, top << 16);
   }
 }
+
+// The end of a workgroup: the waves' sums of its tiles, in wave order, to outputs, a tile
+// a wave.  Bias and tensor scale are on their way from the start.
+template <int RT, int MT, int WAVES>
+struct Ending {
+  static_assert(RT * MT <= WAVES, "a tile a wave");
+  int n;
+  int64_t row;
+  bool live;
+  float sw, bias[4];
+
+  __device__ __forceinline__ void start(const WeightOnly& a, int n0, int64_t m0) {
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    n = n0 + 16 * (wave / MT) + 4 * (lane >> 4);
+    row = m0 + 16 * (wave % MT) + (lane & 15);
+    live = wave < RT * MT && row < a.M && n < a.N;
+    sw = *a.tensor_scale;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      bias[r] = 0.0f;
+      if (a.bias && live) bias[r] = bf16_bits_to_f32(a.bias[min(n + r, a.N - 1)]);
+    }
+  }
+  __device__ __forceinline__ void write(const WeightOnly& a, const f32x4 (&acc)[RT][MT], f32x4 (*park)[RT * MT][64]) const {
+    const int lane = threadIdx.x & 63, wave = wave_id();
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) park[wave][rt * MT + mt][lane] = acc[rt][mt];
+    __syncthreads();
+    uint32_t top = 0;
+    if (live) {
+      f32x4 y = park[0][wave][lane];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) y += park[w][wave][lane];
+      uint32_t out[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        out[r] = finish(a, y[r], sw, bias[r]);
+        if (n + r < a.N) top = max(top, out[r] & 0x7FFFu);
+      }
+      uint16_t* to = a.y + row * a.N + n;
+      if (a.N % 4 == 0) {
+        *reinterpret_cast<u32x2*>(to) = u32x2{(out[0] & 0xFFFFu) | out[1] << 16, (out[2] & 0xFFFFu) | out[3] << 16};
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + r < a.N) to[r] = (uint16_t)out[r];
+      }
+    }
+    raise_by<WAVES>(a, top);
+  }
+};
 
 // A wave has RT tiles of 16 weight rows and MT of 16 rows of x, and steps of U times 128
 // k, whose codes are on their way together; x is read from the caches step by step.  The
@@ -102,6 +131,8 @@ __global__ __launch_bounds__(64 * WAVES) void weight_only_kernel(WeightOnly a) {
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_id();
   const int n0 = (int)blockIdx.x * (16 * RT);
   const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  Ending<RT, MT, WAVES> ending;
+  ending.start(a, n0, m0);
   const uint8_t *codes[RT], *scales[RT];
   const uint16_t* x[MT];
   bool live[MT];
@@ -161,7 +192,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_only_kernel(WeightOnly a) {
       }
     }
   }
-  join_waves<RT, MT, WAVES>(a, acc, park, n0, m0);
+  ending.write(a, acc, park);
 }
 
 // One or two rows of x: the lanes lie along k, 32 each, so a wave reads 1 KiB of a
@@ -244,7 +275,7 @@ __global__ __launch_bounds__(256) void weight_only_vector_kernel(WeightOnly a, i
     for (int w = 1; w < ways; ++w) y += park[of * ways + w][r][m];
     const int n = ((int)blockIdx.x * (4 / ways) + of) * kRows + r;
     if (n < a.N && m0 + m < a.M) {
-      const uint32_t out = finish(a, y, *a.tensor_scale, n);
+      const uint32_t out = finish(a, y, *a.tensor_scale, a.bias ? bf16_bits_to_f32(a.bias[n]) : 0.0f);
       a.y[(m0 + m) * a.N + n] = (uint16_t)out;
       top = out & 0x7FFFu;
     }
@@ -282,6 +313,8 @@ __global__ __launch_bounds__(64 * WAVES) void weight_only_lds_kernel(WeightOnly 
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_id();
   const int n0 = (int)blockIdx.x * (16 * RT);
   const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  Ending<RT, MT, WAVES> ending;
+  ending.start(a, n0, m0);
   const uint8_t *codes[RT][2], *scales[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -375,7 +408,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_only_lds_kernel(WeightOnly 
     t += WAVES;
   }
   __syncthreads();                             // the rings are free
-  join_waves<RT, MT, WAVES>(a, acc, reinterpret_cast<f32x4(*)[RT * MT][64]>(ring), n0, m0);
+  ending.write(a, acc, reinterpret_cast<f32x4(*)[RT * MT][64]>(ring));
 }
 
 template <int RT, int MT, int U, int WAVES>
