@@ -803,6 +803,7 @@ struct ManyRows {
   const int32_t* table;
   int64_t page_blocks;
   int pages, shift, seen, last_group;
+  int entries, held, held_from;        // of the table; 64 of them from held_from on, a lane each
 
   __device__ __forceinline__ void start(const CacheAttention& a) {
     const int lane = threadIdx.x & 63;
@@ -822,6 +823,8 @@ struct ManyRows {
     table = PAGED ? a.c.table + b * a.c.table_pages : nullptr;
     pages = (int)a.c.pages;
     shift = a.c.page_shift;
+    entries = (int)a.c.table_pages;
+    held_from = -64;
     seen = seen_;
     last_group = (seen - 1) & ~(kGroupKeys - 1);
   }
@@ -830,9 +833,20 @@ struct ManyRows {
   __device__ __forceinline__ int first(int t, int i) const {
     return min(64 * t + (i * WAVES + wave) * kGroupKeys, last_group);
   }
-  __device__ __forceinline__ void look_up(int t, int (&page)[kGroups]) const {
+  // (Tiles come in order, so the table is read 64 entries at a time.)
+  __device__ __forceinline__ void look_up(int t, int (&page)[kGroups]) {
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) page[i] = PAGED ? table[first(t, i) >> shift] : 0;
+    for (int i = 0; i < kGroups; ++i) {
+      page[i] = 0;
+      if constexpr (PAGED) {
+        const int n = first(t, i) >> shift;
+        if (n >= held_from + 64) {
+          held_from = n;
+          held = table[min(n + (int)(threadIdx.x & 63), entries - 1)];
+        }
+        page[i] = __builtin_amdgcn_readlane(held, n - held_from);
+      }
+    }
   }
   __device__ __forceinline__ void load(int t, const int (&page)[kGroups], Tile& x) const {
 #pragma unroll
