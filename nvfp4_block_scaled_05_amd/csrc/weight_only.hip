@@ -302,7 +302,7 @@ __device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* lds) {
 // 16-byte pieces of a row are permuted by XOR, so that the reads of 16 rows spread over
 // the banks.  x goes to registers a step ahead, before the codes (loads return in order).
 // 28672 x 8192: 37 us for 4 rows (45 by the kernel above), 46 for 16 (56), 65 for 32 (71);
-// 4096 x 4096 5.7 and 7.3 for 3 and 16 (6.8 and 8.5); 14336 x 4096 15.1 for 16, 17 to 19
+// 4096 x 4096 5.7 and 7.3 for 3 and 16 (6.8 and 8.5); 14336 x 4096 15.1 for 16, 16.4
 // with bias, GELU and amax.  What is left for 16 rows is x: its loads touch 64 places
 // each, four times as many as the codes'.
 template <int RT, int MT, int WAVES>
