@@ -129,7 +129,8 @@ bool bad_cache_attention(int64_t batch, int64_t queries, int64_t heads, int64_t 
   if (dim <= 0 || dim % 16 != 0 || dim > 128) return true;
   if (batch * heads >= kMaxDim || (queries > 0 && batch * heads >= kMaxDim / queries)) return true;
   const int64_t units = batch * kv_heads * ((queries * (heads / kv_heads) + 127) / 128);
-  return units > (1 << 23) || (units > 0 && (capacity + 63) / 64 + 1 >= kMaxDim / units);
+  // a unit counts its tiles and up to 6 for its beginning
+  return units > (1 << 23) || (units > 0 && (capacity + 63) / 64 + 6 >= kMaxDim / units);
 }
 
 // Positive, finite and not subnormal (the kernels' reciprocal square root takes a

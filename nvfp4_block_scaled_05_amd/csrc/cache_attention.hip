@@ -11,7 +11,7 @@
 // the values' tensor scale is applied with the division by the sum.
 //
 // cache_few_kernel: up to 32 query rows a kv head, bound by the stream of codes, which
-// go from memory to registers in the order in which the matrix instructions take them.
+// reach the waves through rings of LDS of their own and are decoded in registers.
 // cache_many_kernel: tiles of keys decoded into LDS for all of a workgroup's rows.
 // cache_join_kernel: joins the workgroups that share a unit's keys.
 #include <algorithm>
@@ -127,8 +127,9 @@ __device__ __forceinline__ float stored_scale(float amax) {
   return s_dec;
 }
 
-// A row's power of two, from its largest magnitude (infinity and NaN stay what they are): `up` brings it into [2^13, 2^14),
-// `down` is 1 / up.  Rows below 2^-100 are taken as if they reached it.
+// A row's power of two, from its largest magnitude (infinity and NaN stay what they
+// are): `up` brings it into [2^13, 2^14), `down` is 1 / up.  Rows below 2^-100 are taken
+// as if they reached it.
 __device__ __forceinline__ void row_power(float top, float& up, float& down) {
   const int e = max((int)(__float_as_uint(top) >> 23), 27);
   up = __uint_as_float((uint32_t)(267 - e) << 23);
@@ -212,17 +213,6 @@ struct Codes<64> {
   u32x2 k[2];
   uint32_t ks[2], v[2][4], vs[2][4];
 };
-
-// Straight into LDS, past the caches: 16 or 4 bytes of each lane to `lds` + lane * BYTES.
-template <int BYTES>
-__device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* lds) {
-  auto* to = (__attribute__((address_space(3))) void*)lds;
-  auto* at = (__attribute__((address_space(1))) void*)const_cast<uint8_t*>(from);
-  if constexpr (BYTES == 16)
-    __builtin_amdgcn_global_load_lds(at, to, 16, 0, 2);                       // 2: nt
-  else
-    __builtin_amdgcn_global_load_lds(at, to, 4, 0, 2);
-}
 
 template <int D, bool EXACT, int RT>
 struct FewRows {
@@ -567,9 +557,9 @@ __global__ __launch_bounds__(256, 2) void cache_few_kernel(CacheAttention a) {
     const uint32_t upto_part = a.workers ? min(in + (end - at), parts) : parts;
     const uint32_t from = in - min(in, Work<kKeys>::kStart), upto = upto_part - min(upto_part, Work<kKeys>::kStart);
     const bool whole = upto - from == tiles;
+    if (upto == 0) return;                     // the range ends in the unit's beginning
     const uint32_t done = at;
     at += upto_part - in;
-    if (upto > 0) {
     w.load_rows(a, b, (int)kvh);               // on their way while the pages are looked up
     // the least that a row sees; rows are in the order of their tokens
     const int least = row_limit(a, b, 0, seen);
@@ -673,7 +663,6 @@ __global__ __launch_bounds__(256, 2) void cache_few_kernel(CacheAttention a) {
         }
       }
       __syncthreads();
-    }
     }
     if (!a.workers) return;
     // the next unit is the entry's next head, or the next entry's first
@@ -975,9 +964,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
     const uint32_t upto_part = a.workers ? min(in + (end - at), parts) : parts;
     const uint32_t from = in - min(in, Work<kKeys>::kStart), upto = upto_part - min(upto_part, Work<kKeys>::kStart);
     const bool whole = upto - from == tiles;
+    if (upto == 0) return;                     // the range ends in the unit's beginning
     const uint32_t done = at;
     at += upto_part - in;
-    if (upto > 0) {
     const int kvh = (int)(of / (uint32_t)a.row_tiles), row0 = (int)(of - (uint32_t)(kvh * a.row_tiles)) * kTileRows + wave * 32;
 
     // the queries and the first tile are on their way before anything is waited for
@@ -1113,7 +1102,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
       }
     }
     __syncthreads();
-    }
     if (!a.workers) return;
     if (at - first == parts * units) {
       first = at;

@@ -286,17 +286,6 @@ __global__ __launch_bounds__(256) void weight_only_vector_kernel(WeightOnly a, i
   }
 }
 
-// Straight into LDS, past the caches: 16 or 4 bytes of each lane to `lds` + lane * BYTES.
-template <int BYTES>
-__device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* lds) {
-  auto* to = (__attribute__((address_space(3))) void*)lds;
-  auto* at = (__attribute__((address_space(1))) void*)const_cast<uint8_t*>(from);
-  if constexpr (BYTES == 16)
-    __builtin_amdgcn_global_load_lds(at, to, 16, 0, 2);                       // 2: nt
-  else
-    __builtin_amdgcn_global_load_lds(at, to, 4, 0, 2);
-}
-
 // Steps of 256 k, 128 bytes of each weight row, in a ring of two stages of LDS of each
 // wave's own, loaded 8 rows at a time so that a load touches 16 places instead of 64; the
 // 16-byte pieces of a row are permuted by XOR, so that the reads of 16 rows spread over

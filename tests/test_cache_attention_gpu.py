@@ -67,6 +67,15 @@ def test_keys_dealt_over_workgroups(dim, batch, queries, heads, kv, page, per, l
     run(np.random.default_rng(page + dim), batch, queries, heads, kv, dim, page, per, lengths, causal=causal)
 
 
+@pytest.mark.parametrize("batch,queries,heads,kv,page,per,lengths,causal", [
+    (300, 1, 8, 4, 64, 20, [(53 * i) % 1281 for i in range(300)], False),
+    (5, 40, 64, 64, 64, 6, [384, 1, 0, 200, 333], False), (5, 40, 64, 64, 32, 12, [384, 40, 41, 200, 333], True)])
+def test_units_that_fill_the_card(batch, queries, heads, kv, page, per, lengths, causal):
+    """More units than are dealt: each is one workgroup's, whatever the lengths."""
+    assert nv.cache_attention_workspace(batch, queries, heads, kv, 64, page * per) is None
+    run(np.random.default_rng(batch), batch, queries, heads, kv, 64, page, per, lengths, causal=causal)
+
+
 @pytest.mark.parametrize("queries", [1, 30, 100])
 def test_lengths_outside_the_capacity_are_taken_within(queries):
     rng = np.random.default_rng(5)
