@@ -651,7 +651,8 @@ size_t kv_cache_attention_workspace_bytes(int64_t batch, int64_t queries, int64_
  *               int32.
  *   heads       a positive multiple of kv_heads, at most 65536; batch * heads *
  *               queries below 2^31, and in rows of 128 per kv head at most 2^23
- *               and, times the capacity's tiles of 64 keys and six, below 2^31.  scale > 0, at least 2^-126.
+ *               and, times the capacity's tiles of 64 keys and six, below 2^31.
+ *               scale > 0, at least 2^-126.
  *   workspace   optional, 256-byte aligned, contents on entry irrelevant, owned by
  *               the call until it completes: with at least
  *               kv_cache_attention_workspace_bytes bytes the keys of all entries

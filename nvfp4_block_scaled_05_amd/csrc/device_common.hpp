@@ -253,16 +253,16 @@ __device__ __forceinline__ void buffer_load_lds(const void* base, uint32_t lane_
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 4, lane_off, scalar_off, 0, 0);
 }
 
-// The same from a 64-bit address of each lane, past the caches: BYTES (16 or 4) of lane L
-// to lds + L * BYTES.
-template <int BYTES>
+// The same from a 64-bit address of each lane: BYTES (16 or 4) of lane L to lds + L * BYTES;
+// POLICY 2 (nt) for what is read once, 0 for what the caches should hold.
+template <int BYTES, int POLICY = 2>
 __device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* lds) {
   auto* to = (__attribute__((address_space(3))) void*)lds;
   auto* at = (__attribute__((address_space(1))) void*)const_cast<uint8_t*>(from);
   if constexpr (BYTES == 16)
-    __builtin_amdgcn_global_load_lds(at, to, 16, 0, 2);                       // 2: nt
+    __builtin_amdgcn_global_load_lds(at, to, 16, 0, POLICY);
   else
-    __builtin_amdgcn_global_load_lds(at, to, 4, 0, 2);
+    __builtin_amdgcn_global_load_lds(at, to, 4, 0, POLICY);
 }
 
 // Sums over neighbouring lanes in the vector ALU's lane-permuting operand: after

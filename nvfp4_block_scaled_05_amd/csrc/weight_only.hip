@@ -7,9 +7,11 @@
 // formula; sums are binary32.
 //
 // weight_only_vector_kernel: one or two rows, by dot products along k.
-// weight_only_lds_kernel: matrix instructions over codes that reach LDS in whole lines.
-// weight_only_kernel: the same with codes straight to registers, for any K and any place
-// of the codes, and for 17 to 32 rows of a small weight.
+// weight_only_ring_kernel: up to 16, by matrix instructions; codes and x reach LDS in whole
+// lines.
+// weight_only_lds_kernel: more rows of a large weight; x to registers.
+// weight_only_kernel: codes straight to registers too, for any K and any place of the
+// codes, and for more than 16 rows of a small weight.
 // All of them split K over the waves of a workgroup, which meet in LDS in a fixed order.
 #include "device_common.hpp"
 #include "kernels.hpp"
@@ -75,7 +77,8 @@ struct Ending {
   int n;
   int64_t row;
   bool live;
-  float sw, bias[4];
+  float sw;
+  uint32_t bias[4];                            // bf16
 
   __device__ __forceinline__ void start(const WeightOnly& a, int n0, int64_t m0) {
     const int lane = threadIdx.x & 63, wave = wave_id();
@@ -83,11 +86,10 @@ struct Ending {
     row = m0 + 16 * (wave % MT) + (lane & 15);
     live = wave < RT * MT && row < a.M && n < a.N;
     sw = *a.tensor_scale;
+    // (without a bias the loads are of the tensor scale: a branch would be waited for here)
+    const uint16_t* from = a.bias ? a.bias : reinterpret_cast<const uint16_t*>(a.tensor_scale);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      bias[r] = 0.0f;
-      if (a.bias && live) bias[r] = bf16_bits_to_f32(a.bias[min(n + r, a.N - 1)]);
-    }
+    for (int r = 0; r < 4; ++r) bias[r] = from[a.bias ? min(n + r, a.N - 1) : 0];
   }
   __device__ __forceinline__ void write(const WeightOnly& a, const f32x4 (&acc)[RT][MT], f32x4 (*park)[RT * MT][64]) const {
     const int lane = threadIdx.x & 63, wave = wave_id();
@@ -104,7 +106,7 @@ struct Ending {
       uint32_t out[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        out[r] = finish(a, y[r], sw, bias[r]);
+        out[r] = finish(a, y[r], sw, a.bias ? bf16_bits_to_f32(bias[r]) : 0.0f);
         if (n + r < a.N) top = max(top, out[r] & 0x7FFFu);
       }
       uint16_t* to = a.y + row * a.N + n;
@@ -286,76 +288,55 @@ __global__ __launch_bounds__(256) void weight_only_vector_kernel(WeightOnly a, i
   }
 }
 
-// Steps of 256 k, 128 bytes of each weight row, in a ring of two stages of LDS of each
-// wave's own, loaded 8 rows at a time so that a load touches 16 places instead of 64; the
-// 16-byte pieces of a row are permuted by XOR, so that the reads of 16 rows spread over
-// the banks.  x goes to registers a step ahead, before the codes (loads return in order).
-// 28672 x 8192: 37 us for 4 rows (45 by the kernel above), 46 for 16 (56), 65 for 32 (71);
-// 4096 x 4096 5.7 and 7.3 for 3 and 16 (6.8 and 8.5); 14336 x 4096 15.1 for 16, 16.4
-// with bias, GELU and amax.  What is left for 16 rows is x: its loads touch 64 places
-// each, four times as many as the codes'.
-template <int RT, int MT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void weight_only_lds_kernel(WeightOnly a) {
-  constexpr int kK = 256, kCodes = 16 * 128, kStage = RT * (kCodes + 256);
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[WAVES * 2 * kStage];
-  static_assert(sizeof(ring) >= WAVES * RT * MT * 1024, "the waves' sums meet in the ring");
-  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_id();
-  const int n0 = (int)blockIdx.x * (16 * RT);
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-  Ending<RT, MT, WAVES> ending;
-  ending.start(a, n0, m0);
+// Steps of 256 k, 128 bytes of each of 16 RT weight rows, on their way to LDS of a wave's
+// own, 8 rows to a load, so that a load touches 16 places instead of 64; the 16-byte
+// pieces of a row are permuted by XOR, so that the reads of 16 rows spread over the banks.
+constexpr int kRingK = 256, kCodes = 16 * 128;
+
+template <int RT>
+struct WeightRing {
+  static constexpr int kBytes = RT * (kCodes + 256), kLoads = 3 * RT;     // of a step
   const uint8_t *codes[RT][2], *scales[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = 8 * i + lane / 8, piece = (lane & 7) ^ (row >> 1);
-      codes[rt][i] = a.codes + (int64_t)min(n0 + 16 * rt + row, a.N - 1) * (a.K / 2) + 16 * piece;
-    }
-    scales[rt] = a.scales + (int64_t)min(n0 + 16 * rt + lane / 4, a.N - 1) * (a.K / 16) + 4 * (lane & 3);
-  }
-  const uint16_t* x[MT];
-  bool live[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    live[mt] = m0 + 16 * mt + m < a.M;
-    x[mt] = a.x + (live[mt] ? m0 + 16 * mt + m : 0) * a.K + 32 * g;
-  }
-  uint8_t* own = ring + wave * (2 * kStage);
-  const uint32_t own_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)own;
-  const uint32_t at0 = own_at + (uint32_t)(m * 128 + ((g ^ (m >> 1)) << 4));
-  const uint32_t at1 = own_at + (uint32_t)(m * 128 + (((4 + g) ^ (m >> 1)) << 4));
-  const uint32_t at_s = own_at + (uint32_t)(RT * kCodes + m * 16 + 2 * g);
-  constexpr int kLoads = 3 * RT, kXLoads = 8 * MT;
-  auto fetch = [&](int step, int stage) {
+  uint32_t at[2], at_s;
+
+  // own_at: the LDS address of the wave's first stage.
+  __device__ __forceinline__ void start(const WeightOnly& a, int n0, uint32_t own_at) {
+    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) to_lds<16>(codes[rt][i] + (uint32_t)step * 128u, own + stage * kStage + rt * kCodes + i * 1024);
-      to_lds<4>(scales[rt] + (uint32_t)step * 16u, own + stage * kStage + RT * kCodes + rt * 256);
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * i + lane / 8, piece = (lane & 7) ^ (row >> 1);
+        codes[rt][i] = a.codes + (int64_t)min(n0 + 16 * rt + row, a.N - 1) * (a.K / 2) + 16 * piece;
+      }
+      scales[rt] = a.scales + (int64_t)min(n0 + 16 * rt + lane / 4, a.N - 1) * (a.K / 16) + 4 * (lane & 3);
     }
-  };
-  u32x4 xv[2][2][MT][4];
-  auto load_x = [&](int step, u32x4 (&v)[2][MT][4]) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) at[u] = own_at + (uint32_t)(m * 128 + (((4 * u + g) ^ (m >> 1)) << 4));
+    at_s = own_at + (uint32_t)(RT * kCodes + m * 16 + 2 * g);
+  }
+  __device__ __forceinline__ void fetch(int step, uint8_t* stage) const {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[u][mt][i] = *reinterpret_cast<const u32x4*>(x[mt] + step * kK + 128 * u + 8 * i);
-  };
-  f32x4 acc[RT][MT] = {};
-  auto multiply = [&](int stage, const u32x4 (&v)[2][MT][4]) {
+      for (int i = 0; i < 2; ++i) to_lds<16>(codes[rt][i] + (uint32_t)step * 128u, stage + rt * kCodes + i * 1024);
+      to_lds<4>(scales[rt] + (uint32_t)step * 16u, stage + RT * kCodes + rt * 256);
+    }
+  }
+  // Adds the products of a step that has arrived, `stage` bytes behind the first stage;
+  // v: x at k 128 u + 32 g + 8 i.
+  template <int MT>
+  __device__ __forceinline__ void multiply(uint32_t stage, const u32x4 (&v)[2][MT][4], f32x4 (&acc)[RT][MT]) const {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       u32x4 c[2];
       uint32_t sc[2];
-      const uint32_t to = (uint32_t)(stage * kStage + rt * kCodes), to_s = (uint32_t)(stage * kStage + rt * 256);
+      const uint32_t to = stage + (uint32_t)(rt * kCodes), to_s = stage + (uint32_t)(rt * 256);
       asm volatile(
           "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_u16 %2, %6\n\tds_read_u16 %3, %6 offset:8\n\t"
           "s_waitcnt lgkmcnt(0)"
           : "=&v"(c[0]), "=&v"(c[1]), "=&v"(sc[0]), "=&v"(sc[1])
-          : "v"(at0 + to), "v"(at1 + to), "v"(at_s + to_s)
+          : "v"(at[0] + to), "v"(at[1] + to), "v"(at_s + to_s)
           : "memory");
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -369,25 +350,123 @@ __global__ __launch_bounds__(64 * WAVES) void weight_only_lds_kernel(WeightOnly 
         }
       }
     }
+  }
+};
+
+// Waits until all but the last N loads have arrived.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "the count is 6 bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
+
+// 3 to 16 rows of x, which goes to LDS as well, two rows of 512 bytes to a load, its pieces
+// permuted the same way (loaded as the matrix instruction wants it, each load touches 64
+// places: 14336 x 4096 13.5 us instead of 12.1, 28672 x 8192 45 instead of 39 to 41, 8192 x
+// 28672 48 instead of 38 to 42, for 16 rows; 14336 x 4096 with bias, GELU and amax 16.9
+// instead of 14.9).  A ring of two stages a wave.  What is left is decoding, about two
+// instructions an element, with one wave a SIMD to hide the rest.
+template <int RT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void weight_only_ring_kernel(WeightOnly a) {
+  constexpr int kAtX = WeightRing<RT>::kBytes, kStage = kAtX + 16 * 2 * kRingK, kXLoads = 8;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[WAVES * 2 * kStage];
+  static_assert(sizeof(ring) >= WAVES * RT * 1024, "the waves' sums meet in the ring");
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_id();
+  const int n0 = (int)blockIdx.x * (16 * RT);
+  Ending<RT, 1, WAVES> ending;
+  ending.start(a, n0, 0);
+  uint8_t* own = ring + wave * (2 * kStage);
+  const uint32_t own_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)own;
+  WeightRing<RT> weight;
+  weight.start(a, n0, own_at);
+  const uint16_t* x[kXLoads];                  // (rows past the last are the last's)
+#pragma unroll
+  for (int j = 0; j < kXLoads; ++j) {
+    const int row = 2 * j + lane / 32, piece = (lane & 31) ^ row;
+    x[j] = a.x + min((int64_t)row, a.M - 1) * a.K + 8 * piece;
+  }
+  uint32_t at_x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) at_x[i] = own_at + (uint32_t)(kAtX + m * 512 + (((4 * g + i) ^ m) << 4));
+  auto fetch = [&](int step, int stage) {
+    uint8_t* to = own + stage * kStage;
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j)
+      to_lds<16, 0>(reinterpret_cast<const uint8_t*>(x[j] + (uint32_t)(step * kRingK)), to + kAtX + j * 1024);
+    weight.fetch(step, to);
   };
-  const int steps = a.K / kK;
-  static_assert(kLoads + kXLoads < 64, "the wait's count is 6 bits");
-  constexpr int kWait = kLoads + kXLoads;
+  const int steps = a.K / kRingK;
+  f32x4 acc[RT][1] = {};
+  if (wave < steps) fetch(wave, 0);
+  int stage = 0;
+  for (int t = wave; t < steps; t += WAVES, stage ^= 1) {
+    if (t + WAVES < steps) {
+      fetch(t + WAVES, stage ^ 1);
+      wait_loads<WeightRing<RT>::kLoads + kXLoads>();      // this step's are in
+    } else {
+      wait_loads<0>();
+    }
+    u32x4 v[2][1][4];
+    const uint32_t to = (uint32_t)(stage * kStage);
+    asm volatile(
+        "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
+        "ds_read_b128 %4, %8 offset:256\n\tds_read_b128 %5, %9 offset:256\n\t"
+        "ds_read_b128 %6, %10 offset:256\n\tds_read_b128 %7, %11 offset:256\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0][0][0]), "=&v"(v[0][0][1]), "=&v"(v[0][0][2]), "=&v"(v[0][0][3]), "=&v"(v[1][0][0]),
+          "=&v"(v[1][0][1]), "=&v"(v[1][0][2]), "=&v"(v[1][0][3])
+        : "v"(at_x[0] + to), "v"(at_x[1] + to), "v"(at_x[2] + to), "v"(at_x[3] + to)
+        : "memory");
+    weight.multiply(to, v, acc);
+  }
+  __syncthreads();                             // the rings are free
+  ending.write(a, acc, reinterpret_cast<f32x4(*)[RT][64]>(ring));
+}
+
+// 17 rows and more: two tiles of x, in registers a step ahead, before the codes (loads
+// return in order); in LDS they would leave room for three waves.  28672 x 8192: 65 us for
+// 32 rows, 71 by weight_only_kernel.
+template <int RT, int MT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void weight_only_lds_kernel(WeightOnly a) {
+  constexpr int kStage = WeightRing<RT>::kBytes;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[WAVES * 2 * kStage];
+  static_assert(sizeof(ring) >= WAVES * RT * MT * 1024, "the waves' sums meet in the ring");
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_id();
+  const int n0 = (int)blockIdx.x * (16 * RT);
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  Ending<RT, MT, WAVES> ending;
+  ending.start(a, n0, m0);
+  const uint16_t* x[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) x[mt] = a.x + min(m0 + 16 * mt + m, a.M - 1) * a.K + 32 * g;
+  uint8_t* own = ring + wave * (2 * kStage);
+  WeightRing<RT> weight;
+  weight.start(a, n0, (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)own);
+  u32x4 xv[2][2][MT][4];
+  auto load_x = [&](int step, u32x4 (&v)[2][MT][4]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][mt][i] = *reinterpret_cast<const u32x4*>(x[mt] + step * kRingK + 128 * u + 8 * i);
+  };
+  const int steps = a.K / kRingK;
+  f32x4 acc[RT][MT] = {};
   auto turn = [&](int t, int stage, u32x4 (&now)[2][MT][4], u32x4 (&next)[2][MT][4]) {
     if (t + WAVES < steps) {
       load_x(t + WAVES, next);
-      fetch(t + WAVES, stage ^ 1);
-      __builtin_amdgcn_s_waitcnt(0x0F70 | (kWait & 15) | (kWait >> 4) << 14);    // vmcnt: this step's are in
+      weight.fetch(t + WAVES, own + (stage ^ 1) * kStage);
+      wait_loads<WeightRing<RT>::kLoads + 8 * MT>();       // this step's are in
     } else {
-      __builtin_amdgcn_s_waitcnt(0x0F70);
+      wait_loads<0>();
     }
-    asm volatile("" ::: "memory");
-    multiply(stage, now);
+    weight.multiply((uint32_t)(stage * kStage), now, acc);
   };
   int t = wave;
   if (t < steps) {
     load_x(t, xv[0]);
-    fetch(t, 0);
+    weight.fetch(t, own);
   }
   while (t < steps) {
     turn(t, 0, xv[0], xv[1]);
@@ -405,10 +484,9 @@ void launch_rows(const WeightOnly& a, hipStream_t stream) {
   const dim3 grid((unsigned)((a.N + 16 * RT - 1) / (16 * RT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
   weight_only_kernel<RT, MT, U, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a);
 }
-template <int RT, int MT, int WAVES>
-void launch_lds(const WeightOnly& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.N + 16 * RT - 1) / (16 * RT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
-  weight_only_lds_kernel<RT, MT, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a);
+template <int RT>
+void launch_ring(const WeightOnly& a, hipStream_t stream) {
+  weight_only_ring_kernel<RT, 4><<<(unsigned)((a.N + 16 * RT - 1) / (16 * RT)), 256, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -425,26 +503,27 @@ hipError_t launch_weight_only(WeightOnly a, hipStream_t stream) {
       weight_only_vector_kernel<2><<<grid, 256, 0, stream>>>(a, ways);
     return hipGetLastError();
   }
-  // More weight rows a wave read x less often, fewer leave more workgroups: four tiles from
-  // 3 of them a compute unit on (16 rows of 14336 x 4096: 15.0 us with four tiles, 15.7 with
-  // two, 20.2 with one; of 4096 x 4096 12.6, 9.0 and 7.2), in workgroups of four waves, two a
-  // compute unit, where those are more than one each (28672 x 8192: 46 us against 50); up to 8
-  // rows, where x is small, two (13.1 against 13.9; 37.5 against 42).  17 to 32 rows of a large
-  // weight 18.6 against 20.0 in registers, of a small one 40 against 12.  More than 32 rows in
-  // passes of 32: 64 rows of 28672 x 8192 124 us, in one pass of four tiles of x 159.
   const int64_t tiles = (a.N + 15) / 16, cus = compute_units();
-  const bool one = a.M <= 16, large = tiles >= 3 * cus;
+  const bool one = a.M <= 16;
   // (the rings take 16 and 4 bytes at a time from rows that begin so)
-  const bool placed = a.K % 256 == 0 && ((uintptr_t)a.codes & 15) == 0 && ((uintptr_t)a.scales & 3) == 0;
-  if (placed && (one || large)) {
-    if (!one)
-      launch_lds<4, 2, 8>(a, stream);
-    else if (large && a.M > 8)
-      tiles > 4 * cus ? launch_lds<4, 1, 4>(a, stream) : launch_lds<4, 1, 8>(a, stream);
-    else if (2 * tiles >= 3 * cus)
-      launch_lds<2, 1, 8>(a, stream);
+  const bool placed = a.K % kRingK == 0 && ((uintptr_t)a.codes & 15) == 0 && ((uintptr_t)a.scales & 3) == 0;
+  if (placed && one) {
+    // The fewest tiles a workgroup that leave a compute unit one, whose LDS its rings fill;
+    // four are the most.  16 rows with one, two and four tiles: 4096 x 4096 6.0, 7.2 and
+    // 11.1 us; 8192 x 28672 50, 38 and 54; 14336 x 4096 18.9, 13.9 and 12.2.  In workgroups
+    // of 6 or 7 waves the first two take as long or longer.
+    if (tiles <= cus)
+      launch_ring<1>(a, stream);
+    else if (tiles <= 2 * cus)
+      launch_ring<2>(a, stream);
     else
-      launch_lds<1, 1, 8>(a, stream);
+      launch_ring<4>(a, stream);
+  } else if (placed && tiles >= 3 * cus) {
+    // 17 to 32 rows of a large weight 18.6 us against 20.0 by weight_only_kernel, of a small
+    // one 40 against 12.  More than 32 rows in passes of 32: 64 rows of 28672 x 8192 124 us,
+    // in one pass of four tiles of x 159.
+    const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 31) / 32));
+    weight_only_lds_kernel<4, 2, 8><<<grid, 512, 0, stream>>>(a);
   } else if (2 * tiles >= 3 * cus) {
     one ? launch_rows<2, 1, 2, 8>(a, stream) : launch_rows<2, 2, 1, 8>(a, stream);
   } else {

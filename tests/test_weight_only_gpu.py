@@ -67,6 +67,20 @@ def test_every_kernel(rows, n, k):
         assert torch.isnan(bad[rows // 2]).all() and torch.equal(bad[keep], got[keep])
 
 
+@pytest.mark.parametrize("steps", [1, 3, 4, 9])
+@pytest.mark.parametrize("rows", [3, 15, 16])
+@pytest.mark.parametrize("tiles", [-1, 0, 1])
+@pytest.mark.parametrize("part", [1, 2])
+def test_rings_of_a_compute_unit(part, tiles, rows, steps):
+    """Tiles of 16 outputs on both sides of one and two a compute unit, the last one ragged; steps of 256
+    that leave some waves without one and some with more than others."""
+    n = 16 * (part * torch.cuda.get_device_properties(0).multi_processor_count + tiles) - 5
+    rng = np.random.default_rng(n + rows + steps)
+    x, w, bias = normal(rng, (rows, 256 * steps)), weight(rng, n, 256 * steps), normal(rng, (n,))
+    check(nv.gemm_weight_only(x, w), x, w)
+    check(nv.gemm_weight_only(x, w, bias=bias, epilogue="gelu"), x, w, bias, True)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 7, 20])
 def test_weights_at_any_place(rows):
     """Codes at 8 bytes and scales at any byte, as slices of one checkpoint buffer lie."""
