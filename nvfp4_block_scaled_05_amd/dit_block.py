@@ -120,8 +120,10 @@ class DitCrossBlock:
     ``ids`` of a call says which one each token uses.
     ``held``: "bf16", the prompts' keys and values as the projection and rotary leave
     them, or "nvfp4", in a cache of 4-bit codes (``cache``, a page for each prompt):
-    9/32 of the memory, which every block of a model takes for every prompt over all
-    steps.  Keys are quantized under the bound that their norm gives,
+    9/32 of their memory, which every block of a model takes for every prompt over all
+    steps.  Their bf16 form passes through the buffer of the MLP's hidden activations,
+    which is made larger where it is too small for them, and is not kept: ``k`` and
+    ``v`` are None.  Keys are quantized under the bound that their norm gives,
     sqrt(dim) max |k_norm|, values under the amax that the projection's epilogue
     computes.
     """
@@ -164,10 +166,17 @@ class DitCrossBlock:
         self.result = bf16(batch, tokens, hidden)
         self.attended = bf16(batch, tokens, heads, dim)
         self.k = self.v = None
+        self.encoded = False
         # the block's own, so that a captured call finds the last prompt's lengths in it
         self.lengths = torch.full((batch,), states, dtype=torch.int32, device=dev)
         self.cache = None
         if held == "nvfp4":
+            # no step needs the hidden activations of the one before, so a prompt may come
+            # between any two
+            kv, up = self.out[self.to_kv], self.out[self.up]
+            shared = bf16(max(kv.numel(), up.numel()))
+            self.out[self.to_kv] = shared[:kv.numel()].view(kv.shape)
+            self.out[self.up] = shared[:up.numel()].view(up.shape)
             page = -(-states // 16) * 16
             bound = math.sqrt(dim) * float(k_norm.abs().max()) or 1.0
             self.cache = kv_cache(batch, page, kv_heads, dim, k_amax=bound, device=dev)
@@ -211,12 +220,15 @@ class DitCrossBlock:
         amax = self.cache.amax[1:] if self.cache and self.quantized[self.to_kv] else None
         kv = self._linear(self.to_kv, states.view(-1, states.shape[-1]), amax_out=amax)
         kv = kv.view(self.batch, self.states, 2, self.kv_heads, -1)
-        k, self.v = kv[:, :, 0], kv[:, :, 1]
+        k, v = kv[:, :, 0], kv[:, :, 1]
         # text states carry no position: position 0, without the factor on rotated
         # values that a YaRN plan has, leaves their norm alone
-        self.k = rotary(k, self.no_positions, self.plan._replace(magnitude=1.0), q_weight=self.k_norm, out=k)
+        k = rotary(k, self.no_positions, self.plan._replace(magnitude=1.0), q_weight=self.k_norm, out=k)
         if self.cache:
-            cache_write(self.cache, self.k, self.v, self.first)
+            cache_write(self.cache, k, v, self.first)
+        else:
+            self.k, self.v = k, v
+        self.encoded = True
         if lengths is None:
             self.lengths.fill_(self.states)
         else:
@@ -226,7 +238,7 @@ class DitCrossBlock:
         """temb [batch, cond], x [batch, tokens, hidden], positions as ``rotary``
         takes them, ids: int32 [batch * tokens] or None (no adapters).  Returns
         [batch, tokens, hidden], overwritten by the next call."""
-        if self.k is None:
+        if not self.encoded:
             raise ValueError("encode a prompt first")
         mod = self._linear(self.mod, temb)
         shift_a, scale_a, gate_a, shift_m, scale_m, gate_m = mod.chunk(6, 1)

@@ -166,3 +166,74 @@ def test_a_captured_step():
         assert torch.equal(r.view(x.shape), want)
     for s, m in zip(eager.cache[:4], held.cache[:4]):
         assert torch.equal(s, m)
+
+
+def bytes_held(block):
+    """Of all tensors that a block keeps, each storage once; without the attention's workspace."""
+    found, todo = {}, [v for k, v in vars(block).items() if k != "attn_ws"]
+    while todo:
+        v = todo.pop()
+        if isinstance(v, torch.Tensor):
+            found[v.untyped_storage().data_ptr()] = v.untyped_storage().nbytes()
+        elif isinstance(v, dict):
+            todo += v.values()
+        elif isinstance(v, (list, tuple)):
+            todo += v
+    return sum(found.values())
+
+
+def cross_block(held, states, mlp):
+    rng = np.random.default_rng(4)
+    w = {"w_mod": (6 * HID, HID), "w_q": (HEADS * DIM, HID), "w_kv": (2 * KV * DIM, ENC), "w_o": (HID, HEADS * DIM),
+         "w_up": (mlp, HID), "w_down": (HID, mlp)}
+    weights = {k: normal(rng, s, 0.05) for k, s in w.items()}
+    qn, kn = (normal(rng, (DIM,), 0.1, 1.0, torch.float32) for _ in range(2))
+    args = normal(rng, (B, HID)), normal(rng, (B, T, HID)), torch.zeros((B, T), dtype=torch.int32, device="cuda")
+    return DitCrossBlock(weights, B, T, states, HEADS, KV, qn, kn, nv.rotary_plan(DIM), held=held), args
+
+
+@pytest.mark.parametrize("states,mlp", [(33, 512), (48, 512), (700, 64)])
+def test_block_keeps_no_bf16_keys_and_values(states, mlp):
+    """Beside the cache nothing of the prompt stays: the projection's output lies where the MLP's hidden
+    activations do, before and after a prompt, a step and another prompt."""
+    (b, args), (plain, _) = (cross_block(held, states, mlp) for held in ("nvfp4", "bf16"))
+    projected, hidden = 2 * B * states * 2 * KV * DIM, 2 * B * T * mlp
+    page = -(-states // 16) * 16
+    cache = B * KV * page * 2 * (DIM // 2 + DIM // 16)
+    x = normal(np.random.default_rng(5), (B, states, ENC))
+    for _ in range(2):
+        for one in (b, plain):
+            one.encode(x)
+            one(*args)
+        assert b.k is None and b.v is None
+        # the cache's amax of keys and values, and the entries' first positions
+        assert bytes_held(b) == bytes_held(plain) - min(projected, hidden) + cache + 8 + 4 * B
+        x = x.flip(0).contiguous()
+
+
+@pytest.mark.parametrize("states,mlp", [(33, 512), (700, 64)])
+def test_prompt_and_step_share_a_buffer(states, mlp):
+    """Prompts between steps, eager and in one graph with the step: each result that of a block that has
+    seen this prompt alone."""
+    rng = np.random.default_rng(6)
+    b, args = cross_block("nvfp4", states, mlp)
+    x, lengths = normal(rng, (B, states, ENC)), ints(states, 5)
+    with pytest.raises(ValueError, match="encode"):
+        b(*args)
+    g = capture(lambda: (b.encode(x, lengths), b(*args))[1])
+    for seed in range(3):
+        x.copy_(normal(rng, (B, states, ENC), 1.0 + seed))
+        lengths.copy_(ints(states - seed, 7 + seed))
+        fresh, _ = cross_block("nvfp4", states, mlp)
+        fresh.encode(x, lengths)
+        want = fresh(*args).clone()
+        assert torch.equal(fresh(*args), want)         # a step leaves the prompt alone
+        b.encode(x, lengths)
+        assert torch.equal(b(*args), want)
+        b.result.zero_()
+        got = g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        q = b.out["transformer_blocks.0.attn.to_q"].view(B, T, HEADS, DIM)
+        k, v = numbers_of(b.cache)
+        check(b.attended, q, k, v, [states - seed, 7 + seed])
