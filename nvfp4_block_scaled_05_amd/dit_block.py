@@ -125,7 +125,7 @@ class DitCrossBlock:
     which is made larger where it is too small for them, and is not kept: ``k`` and
     ``v`` are None.  Keys are quantized under the bound that their norm gives,
     sqrt(dim) max |k_norm|, values under the amax that the projection's epilogue
-    computes.
+    computes (so that layer has to be one that runs in NVFP4).
     """
 
     def __init__(self, weights, batch, tokens, states, heads, kv_heads, q_norm, k_norm, plan,
@@ -143,6 +143,9 @@ class DitCrossBlock:
         if unknown:
             raise ValueError(f"lora: not layers over the image tokens: {sorted(unknown)}")
         self.quantized = {name: layer_is_quantized(name) for name in CROSS_LAYERS}
+        if held == "nvfp4" and not self.quantized[self.to_kv]:
+            # (the bf16 passthrough computes no amax)
+            raise ValueError(f"held='nvfp4' needs {self.to_kv} in NVFP4: its epilogue gives the values' amax")
         self.weights, self.out, self.qbuf, self.ws, self.lora_ws = {}, {}, {}, {}, {}
 
         def bf16(*shape):
@@ -217,7 +220,7 @@ class DitCrossBlock:
             _tensor(lengths, "lengths", torch.int32, (self.batch,))
             _device(states=states, lengths=lengths)
         # the amax of keys and values together bounds the values'
-        amax = self.cache.amax[1:] if self.cache and self.quantized[self.to_kv] else None
+        amax = self.cache.amax[1:] if self.cache else None
         kv = self._linear(self.to_kv, states.view(-1, states.shape[-1]), amax_out=amax)
         kv = kv.view(self.batch, self.states, 2, self.kv_heads, -1)
         k, v = kv[:, :, 0], kv[:, :, 1]

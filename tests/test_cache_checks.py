@@ -264,3 +264,11 @@ def test_oracle_held_and_attention():
     bits[0, 20] = 0x7F80
     c, s, _ = oc.quantized_rows(bits, 6.0)
     assert s[0, 1] == 0x7F and s[0, 0] < 0x7F and c[0, :8].all() and not c[0, 8:].any()
+
+
+def test_prompts_in_4_bits_need_the_projections_amax(monkeypatch):
+    """Values are quantized under the amax of the projection's epilogue, which a projection in bf16 has
+    not: a block that would hold them under some other is refused."""
+    from nvfp4_block_scaled_05_amd import dit_block
+    monkeypatch.setattr(dit_block, "layer_is_quantized", lambda name: name != "transformer_blocks.0.attn.add_kv_proj")
+    raises("add_kv_proj", dit_block.DitCrossBlock, {"w_q": bf16(64, 64)}, 1, 16, 16, 1, 1, None, None, None, held="nvfp4")
