@@ -207,3 +207,50 @@ def test_offsets_past_32_bits():
     assert torch.equal(y[:, -32:], nv.gemm_weight_only(x, last)) and not y[:, :-32].any()
     del codes, scales
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("steps", [9, 17, 20])
+def test_many_rows_in_rings_that_turn(steps):
+    """17 rows and more of a large weight, whose steps of 256 are eight waves' in turn: one to three of a
+    wave, unequal over the waves, so that both stages, the wait for all but the next step's loads and
+    both turns of the loop are run."""
+    n = 48 * torch.cuda.get_device_properties(0).multi_processor_count + 5
+    rng = np.random.default_rng(steps)
+    w, bias = weight(rng, n, 256 * steps), normal(rng, (n,))
+    ww = values(w)
+    for rows in (17, 31, 50):
+        x, amax = normal(rng, (rows, 256 * steps)), torch.zeros(1, device="cuda")
+        got = nv.gemm_weight_only(x, w, bias=bias, y_amax=amax)
+        xx = f64(x)
+        want, size = xx @ ww.T + f64(bias), np.abs(xx) @ np.abs(ww).T + np.abs(f64(bias))
+        assert_within(got, want, (256 * steps + 8) * U32 * size * (1 + UBF) + UBF * np.abs(want), f"{rows} rows")
+        assert amax.item() == got.abs().max().item()
+
+
+@pytest.mark.parametrize("k", [8208, 10000, 28672])
+@pytest.mark.parametrize("rows", [1, 2])
+def test_one_or_two_rows_in_several_chunks_a_wave(rows, k):
+    """Inner sizes past four waves' chunks of 2048, a ragged last one among them."""
+    rng = np.random.default_rng(k + rows)
+    x, w, bias = normal(rng, (rows, k)), weight(rng, 70, k), normal(rng, (70,))
+    check(nv.gemm_weight_only(x, w, bias=bias, epilogue="gelu"), x, w, bias, True)
+
+
+@pytest.mark.parametrize("k", [16384, 16400])
+def test_offsets_past_32_bits_of_every_kernel(k):
+    """As above against binary64; 16400 is not a multiple of 256, so its codes go straight to registers."""
+    rng = np.random.default_rng(k)
+    n = 524320
+    codes = torch.zeros((n, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((n, k // 16), dtype=torch.uint8, device="cuda")
+    assert codes.numel() > 2 ** 32
+    last = weight(rng, 32, k)
+    codes[-32:], scales[-32:] = last.codes, last.scales
+    w = nv.Nvfp4Tensor(codes, scales, last.tensor_scale, k)
+    for rows in (1, 2, 9, 20):
+        x = normal(rng, (rows, k))
+        y = nv.gemm_weight_only(x, w)
+        check(y[:, -32:], x, last)
+        assert not y[:, :-32].any()
+    del codes, scales, w
+    torch.cuda.empty_cache()
