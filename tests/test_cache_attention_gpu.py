@@ -337,3 +337,33 @@ def test_offsets_past_32_bits():
         assert np.array_equal(bits_of(got), bits_of(nv.cache_attention(q, small, ints(512, 300), table=little)))
     del cache
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("workspace", ["own", "none"])
+@pytest.mark.parametrize("dim", [16, 48, 80, 96, 112])
+@pytest.mark.parametrize("batch,queries,heads,kv,page,per,lengths,causal", [
+    (2, 1, 8, 2, 64, 80, [5100, 1111], False), (2, 9, 4, 2, 128, 18, [2300, 1000], True),
+    (2, 30, 1, 1, 16, 130, [2079, 0], False), (1, 90, 2, 1, 64, 30, [1900], True),
+    (2, 40, 2, 2, 64, 18, [1100, 1024], False)])
+def test_padded_heads_over_long_caches(dim, batch, queries, heads, kv, page, per, lengths, causal, workspace):
+    """Head sizes between those that the kernels have, over keys enough for the rings to turn, and for
+    parts that are joined."""
+    own = nv.cache_attention_workspace(batch, queries, heads, kv, dim, page * per)
+    assert own is not None
+    run(np.random.default_rng(page + dim), batch, queries, heads, kv, dim, page, per, lengths, causal=causal,
+        workspace=workspace)
+
+
+@pytest.mark.parametrize("dim", [48, 128])
+@pytest.mark.parametrize("queries", [1, 25, 70])
+def test_keys_dealt_without_a_table(queries, dim):
+    run(np.random.default_rng(queries + dim), 2, queries, 2, 2, dim, 2512, 1, [2512, 1777], paged=False)
+    run(np.random.default_rng(queries), 2, queries, 2, 1, dim, 1040, 1, [1040, 601], causal=True, paged=False)
+
+
+@pytest.mark.parametrize("dim", [64, 112])
+def test_many_rows_of_more_entries_than_lanes(dim):
+    lengths = [(37 * i) % 385 for i in range(70)]
+    assert nv.cache_attention_workspace(70, 20, 2, 1, dim, 384) is not None
+    run(np.random.default_rng(dim), 70, 20, 2, 1, dim, 16, 24, lengths)
+    run(np.random.default_rng(dim), 70, 20, 2, 1, dim, 16, 24, lengths, causal=True)
