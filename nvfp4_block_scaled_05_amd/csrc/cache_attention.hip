@@ -136,10 +136,12 @@ __device__ __forceinline__ void row_power(float top, float& up, float& down) {
   down = __uint_as_float((uint32_t)(e - 13) << 23);
 }
 
-// What a row's score is multiplied with, log2(e) in it.  Never zero: a score out of
-// sight is -infinity and has to stay that.
+// What a row's score is multiplied with, log2(e) in it.  The scale meets the row's power
+// first: it may be large because the queries are small, and neither part is past binary32
+// then.  Never zero or infinite: a score out of sight is -infinity and has to stay that,
+// one of zero is zero.
 __device__ __forceinline__ float score_factor(float scale, float k_scale, float down) {
-  return __builtin_fmaxf(scale * 1.44269504f * k_scale * down, 0x1p-126f);
+  return __builtin_fminf(__builtin_fmaxf(scale * down * (1.44269504f * k_scale), 0x1p-126f), kLowest);
 }
 
 __device__ __forceinline__ uint32_t f16x2_rne(float lo, float hi) { return pair_rne<true>(lo, hi); }

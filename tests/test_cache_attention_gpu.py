@@ -367,3 +367,17 @@ def test_many_rows_of_more_entries_than_lanes(dim):
     assert nv.cache_attention_workspace(70, 20, 2, 1, dim, 384) is not None
     run(np.random.default_rng(dim), 70, 20, 2, 1, dim, 16, 24, lengths)
     run(np.random.default_rng(dim), 70, 20, 2, 1, dim, 16, 24, lengths, causal=True)
+
+
+@pytest.mark.parametrize("queries", [1, 20, 100])
+@pytest.mark.parametrize("amax,k_std,q", [(2.0 ** -88, 2.0 ** -90, 2.0 ** -38), (2688.0, 0.25, 2.0 ** -126),
+                                          (2688.0, 2.0 ** -6, 2.0 ** -122)])
+def test_the_largest_scale(queries, amax, k_std, q):
+    """A scale that times log2(e) is past binary32, over keys or queries that bring the scores back into
+    range.  (A row's elements are of one magnitude: at the bottom of bf16's range smaller ones lose bits.)"""
+    rng = np.random.default_rng(24)
+    cache = nv.kv_cache(1, 96, 1, 64, amax, 4.0)
+    nv.cache_write(cache, normal(rng, (1, 96, 1, 64), k_std), normal(rng, (1, 96, 1, 64)), ints(0))
+    k, v = numbers_of(cache)
+    q = torch.from_numpy(np.sign(rng.standard_normal((1, queries, 1, 64))) * q).to(torch.bfloat16).cuda()
+    check(nv.cache_attention(q, cache, ints(96), scale=3.0e38), q, k, v, [96], scale=3.0e38)
