@@ -564,7 +564,7 @@ int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const
  * fp32 accumulation, products exact before it.
  *   x_bf16 [M, K], 16-byte aligned; w_codes [N, K/2], w_scales [N, K/16],
  *   w_tensor_scale [1] as nvfp4_quantize wrote them (codes 8-byte aligned);
- *   bias_bf16 optional [N]; y_bf16 [M, N], 8-byte aligned.
+ *   bias_bf16 optional [N]; y_bf16 [M, N], 8-byte aligned, overlaps no input.
  *   0 <= M < 2^20; 0 <= N < 2^27; 0 < K < 2^30, K % 16 == 0.
  *   y_amax   optional device float, set to max |y| over the bf16 outputs (0 if
  *            there are none; not finite if one is NaN).

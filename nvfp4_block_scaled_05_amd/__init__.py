@@ -313,7 +313,7 @@ def gemm_weight_only(x, w, bias=None, epilogue="none", y_amax=None, out=None):
     x: [rows, K].  Made for up to 32 rows (single tokens of many requests, the
     rows of a timestep embedding), over which the weight is read once; ``gemm`` is
     the one for many rows.  y_amax: optional one-element float32 device tensor, set
-    to max |Y| for ``quantize``.
+    to max |Y| for ``quantize``.  out: overlaps no input.
     """
     # what is common takes one look (block_ops); anything else the checks below
     torch = _torch()
@@ -341,6 +341,8 @@ def gemm_weight_only(x, w, bias=None, epilogue="none", y_amax=None, out=None):
         _tensor(y_amax, "y_amax", torch.float32)
     if out is not None:
         _tensor(out, "out", torch.bfloat16, (M, N))
+        if out.data_ptr() == x.data_ptr() and out.numel():
+            raise ValueError("out and x are the same buffer")
     at = _place((x, codes, scales, tensor_scale, bias, y_amax, out),
                 "x w.codes w.scales w.tensor_scale bias y_amax out")
     if out is None:

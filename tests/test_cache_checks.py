@@ -272,3 +272,11 @@ def test_prompts_in_4_bits_need_the_projections_amax(monkeypatch):
     from nvfp4_block_scaled_05_amd import dit_block
     monkeypatch.setattr(dit_block, "layer_is_quantized", lambda name: name != "transformer_blocks.0.attn.add_kv_proj")
     raises("add_kv_proj", dit_block.DitCrossBlock, {"w_q": bf16(64, 64)}, 1, 16, 16, 1, 1, None, None, None, held="nvfp4")
+
+
+def test_gemm_weight_only_does_not_write_over_its_input():
+    """Workgroups read all of x while others write their columns of out."""
+    x, w = bf16(3, 64), nv.Nvfp4Tensor(u8(64, 32), u8(64, 4), torch.zeros(1), 64)
+    raises("same buffer", nv.gemm_weight_only, x, w, out=x)
+    raises("same buffer", nv.gemm_weight_only, x, w, out=x.view(3, 64))
+    raises("GPU tensor", nv.gemm_weight_only, x, w, out=bf16(3, 64))
