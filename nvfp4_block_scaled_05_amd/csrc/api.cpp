@@ -99,7 +99,7 @@ bool bad_cache(const kv_cache& c, int64_t batch) {
   if (c.pages <= 0 || bad_dim(c.pages) || c.page_size <= 0 || c.page_size % 16 != 0) return true;
   if (c.kv_heads <= 0 || c.kv_heads > (1 << 16) || c.dim <= 0 || c.dim % 16 != 0 || c.dim > 128)
     return true;
-  if (c.page_size > kMaxDim - 256 || c.table_pages < 0 || c.table_pages > kMaxDim) return true;
+  if (c.page_size >= kMaxDim - 256 || c.table_pages < 0 || c.table_pages > kMaxDim) return true;
   if (!c.table) return batch > c.pages;
   return (c.page_size & (c.page_size - 1)) != 0 || c.table_pages * c.page_size >= kMaxDim - 256;
 }
@@ -123,14 +123,14 @@ nvfp4::Cache cache_of(const kv_cache& c) {
 // counted in 32 bits).
 bool bad_cache_attention(int64_t batch, int64_t queries, int64_t heads, int64_t kv_heads,
                          int64_t dim, int64_t capacity) {
-  if (bad_dim(batch) || bad_dim(queries) || capacity < 0 || capacity > kMaxDim - 256) return true;
+  if (bad_dim(batch) || bad_dim(queries) || capacity < 0 || capacity >= kMaxDim - 256) return true;
   if (heads <= 0 || heads > (1 << 16) || kv_heads <= 0 || kv_heads > heads || heads % kv_heads != 0)
     return true;
   if (dim <= 0 || dim % 16 != 0 || dim > 128) return true;
   if (batch * heads >= kMaxDim || (queries > 0 && batch * heads >= kMaxDim / queries)) return true;
   const int64_t units = batch * kv_heads * ((queries * (heads / kv_heads) + 127) / 128);
   // a unit counts its tiles and up to 6 for its beginning
-  return units > (1 << 23) || (units > 0 && (capacity + 63) / 64 + 6 >= kMaxDim / units);
+  return units > (1 << 23) || (units > 0 && (capacity + 63) / 64 + 6 > (kMaxDim - 1) / units);
 }
 
 // Positive, finite and not subnormal (the kernels' reciprocal square root takes a
@@ -600,7 +600,7 @@ int kv_cache_write(const kv_cache* cache, const dit_heads* k, const dit_heads* v
   if (!cache || !k || !v) return NVFP4_ERR_NULL;
   if (!empty && (null_cache(*cache) || !k->data || !v->data || !starts)) return NVFP4_ERR_NULL;
   if (bad_cache(*cache, batch) || bad_heads(*k) || bad_heads(*v)) return NVFP4_ERR_SHAPE;
-  if (!empty && batch * cache->kv_heads >= kMaxDim / tokens / (cache->dim / 16)) return NVFP4_ERR_SHAPE;
+  if (!empty && batch * cache->kv_heads > (kMaxDim - 1) / (tokens * (cache->dim / 16))) return NVFP4_ERR_SHAPE;
   if (misaligned_cache(*cache) || !aligned(k->data, 16) || !aligned(v->data, 16) ||
       !aligned(starts, 4) || !aligned(counts, 4) || !aligned(dev_status, 4))
     return NVFP4_ERR_ALIGN;
@@ -628,7 +628,7 @@ int kv_cache_read(const kv_cache* cache, const dit_heads* k_out, const dit_heads
   if (!cache || !k_out || !v_out) return NVFP4_ERR_NULL;
   if (!empty && (null_cache(*cache) || !k_out->data || !v_out->data)) return NVFP4_ERR_NULL;
   if (bad_cache(*cache, batch) || bad_heads(*k_out) || bad_heads(*v_out)) return NVFP4_ERR_SHAPE;
-  if (!empty && batch * cache->kv_heads >= kMaxDim / tokens / (cache->dim / 16)) return NVFP4_ERR_SHAPE;
+  if (!empty && batch * cache->kv_heads > (kMaxDim - 1) / (tokens * (cache->dim / 16))) return NVFP4_ERR_SHAPE;
   if (misaligned_cache(*cache) || !aligned(k_out->data, 16) || !aligned(v_out->data, 16) ||
       !aligned(starts, 4) || !aligned(counts, 4))
     return NVFP4_ERR_ALIGN;

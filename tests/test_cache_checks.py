@@ -280,3 +280,22 @@ def test_gemm_weight_only_does_not_write_over_its_input():
     raises("same buffer", nv.gemm_weight_only, x, w, out=x)
     raises("same buffer", nv.gemm_weight_only, x, w, out=x.view(3, 64))
     raises("GPU tensor", nv.gemm_weight_only, x, w, out=bf16(3, 64))
+
+
+@pytest.mark.skipif(gpu(), reason="fake pointers")
+def test_sizes_on_both_sides_of_the_documented_limits(lib):  # noqa: F811
+    one = _VIEW(A, 768, 256, 64)
+    # batch * tokens * kv_heads * dim / 16 below 2^31
+    c = cview(table=A, per=2)
+    for batch, tokens, want in ((89478485, 3, DEVICE), (89478486, 3, SHAPE), (1, 268435455, DEVICE), (1, 1 << 28, SHAPE)):
+        assert lib.kv_cache_write(c, one, one, batch, tokens, A, None, None, None) == want, (batch, tokens)
+        assert lib.kv_cache_read(c, one, one, batch, tokens, None, None, None) == want, (batch, tokens)
+    # 192 units of (tiles of 64 keys and six): below 2^31
+    for per, want in ((44739216, DEVICE), (44739220, SHAPE)):
+        assert lib.kv_cache_attention(cview(table=A, per=per), one, A, None, 96, 1, 4, 0.125, one, None, 0, None) == want, per
+    # a capacity below 2^31 - 256
+    for size, want in (((1 << 31) - 272, DEVICE), ((1 << 31) - 256, SHAPE)):
+        assert lib.kv_cache_attention(cview(size=size), one, A, None, 1, 1, 4, 0.125, one, None, 0, None) == want, size
+        assert lib.kv_cache_write(cview(size=size), one, one, 1, 1, A, None, None, None) == want, size
+    assert lib.kv_cache_attention_workspace_bytes(1, 1, 4, 2, 64, (1 << 31) - 272) != 0
+    assert lib.kv_cache_attention_workspace_bytes(1, 1, 4, 2, 64, (1 << 31) - 256) == 0
