@@ -561,7 +561,8 @@ int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const
  * w4_gemm_weight_only -- few rows of bf16 activations, not quantized, times
  * an NVFP4 weight:
  *   Y[m,n] = bf16_rne( epi( sW * sum_k X[m,k] * W[n,k] * S[n,k/16] + bias[n] ) )
- * fp32 accumulation, products exact before it.
+ * fp32 accumulation, products exact before it; the sums are taken before sW, so
+ * 2688 sum_k |X[m,k]| has to be finite in binary32.
  *   x_bf16 [M, K], 16-byte aligned; w_codes [N, K/2], w_scales [N, K/16],
  *   w_tensor_scale [1] as nvfp4_quantize wrote them (codes 8-byte aligned);
  *   bias_bf16 optional [N]; y_bf16 [M, N], 8-byte aligned, overlaps no input.
@@ -573,8 +574,8 @@ int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const
  * a call has decides the order of a row's additions.
  */
 int w4_gemm_weight_only(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_scales,
-                           const float* w_tensor_scale, const void* bias_bf16, int64_t M, int64_t N,
-                           int64_t K, int epilogue, void* y_bf16, float* y_amax, void* stream);
+                        const float* w_tensor_scale, const void* bias_bf16, int64_t M, int64_t N,
+                        int64_t K, int epilogue, void* y_bf16, float* y_amax, void* stream);
 
 /*
  * A cache: pages of tokens' keys and values, a page's tokens one after another
@@ -614,8 +615,8 @@ typedef struct {
  * that they write).  batch * tokens * kv_heads * dim / 16 is below 2^31.
  */
 int kv_cache_write(const kv_cache* cache, const dit_heads* k, const dit_heads* v,
-                      int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
-                      int32_t* dev_status, void* stream);
+                   int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
+                   int32_t* dev_status, void* stream);
 
 /*
  * kv_cache_read -- the values that positions starts[b] + t, t < counts[b],
@@ -625,13 +626,13 @@ int kv_cache_write(const kv_cache* cache, const dit_heads* k, const dit_heads* v
  *   starts, counts  optional [batch] int32 (NULL: 0, all tokens).
  */
 int kv_cache_read(const kv_cache* cache, const dit_heads* k_out, const dit_heads* v_out,
-                     int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
-                     void* stream);
+                  int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
+                  void* stream);
 
 /* Workspace bytes with which kv_cache_attention spreads the keys of a call over
  * the compute units; 0 if it would not (or for invalid sizes). */
 size_t kv_cache_attention_workspace_bytes(int64_t batch, int64_t queries, int64_t heads,
-                                             int64_t kv_heads, int64_t dim, int64_t capacity);
+                                          int64_t kv_heads, int64_t dim, int64_t capacity);
 
 /*
  * kv_cache_attention -- attention over the cache:
@@ -662,9 +663,9 @@ size_t kv_cache_attention_workspace_bytes(int64_t batch, int64_t queries, int64_
  *               the order of the additions.
  */
 int kv_cache_attention(const kv_cache* cache, const dit_heads* q, const int32_t* lengths,
-                          const int32_t* starts, int64_t batch, int64_t queries, int64_t heads,
-                          float scale, const dit_heads* out, void* workspace,
-                          size_t workspace_bytes, void* stream);
+                       const int32_t* starts, int64_t batch, int64_t queries, int64_t heads,
+                       float scale, const dit_heads* out, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

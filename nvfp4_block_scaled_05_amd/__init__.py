@@ -310,9 +310,8 @@ def gemm_weight_only(x, w, bias=None, epilogue="none", y_amax=None, out=None):
     """Y = epi(sW * X @ W_hat^T + bias) in bf16: few rows of bf16 activations, not
     quantized, times an NVFP4 weight (an ``Nvfp4Tensor``).
 
-    x: [rows, K].  Made for up to 32 rows (single tokens of many requests, the
-    rows of a timestep embedding), over which the weight is read once; ``gemm`` is
-    the one for many rows.  y_amax: optional one-element float32 device tensor, set
+    x: [rows, K].  Made for up to 32 rows (single tokens of many requests), over
+    which the weight is read once; ``gemm`` is the one for many rows.  y_amax: optional one-element float32 device tensor, set
     to max |Y| for ``quantize``.  out: overlaps no input.
     """
     # what is common takes one look (block_ops); anything else the checks below

@@ -28,7 +28,7 @@ _F = ctypes.c_float
 _INT = ctypes.c_int
 
 _HEADS = ctypes.c_char_p                # a dit_heads packed into bytes (read only by the call)
-_CACHE = ctypes.c_char_p                # an kv_cache, likewise
+_CACHE = ctypes.c_char_p                # a kv_cache, likewise
 SIGNATURES = {
     "nvfp4_abi_version": (ctypes.c_int, []),
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -66,7 +66,7 @@ SIGNATURES = {
     "kv_cache_read": (_INT, [_CACHE, _HEADS, _HEADS, _I64, _I64, _P, _P, _P]),
     "kv_cache_attention_workspace_bytes": (ctypes.c_size_t, [_I64] * 6),
     "kv_cache_attention": (_INT, [_CACHE, _HEADS, _P, _P, _I64, _I64, _I64, _F, _HEADS, _P,
-                                     ctypes.c_size_t, _P]),
+                                  ctypes.c_size_t, _P]),
 }
 
 _lib = None

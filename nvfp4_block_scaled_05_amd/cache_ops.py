@@ -152,7 +152,7 @@ def cache_write(cache, k, v, starts, counts=None, table=None, dev_status=None):
                 "k v cache.k_codes cache.k_scales cache.v_codes cache.v_scales cache.amax starts counts "
                 "table dev_status")
     status = load().kv_cache_write(view, kv, vv, batch, tokens, _ptr(starts), _ptr(counts),
-                                      _ptr(dev_status), _stream_at(at))
+                                   _ptr(dev_status), _stream_at(at))
     if status:
         raise Nvfp4Error(status, "kv_cache_write")
 
@@ -224,7 +224,7 @@ def cache_attention(q, cache, lengths, starts=None, table=None, scale=None, out=
     each entry's first query; query t then sees positions up to starts[b] + t, its own,
     else all of them.  table: as for ``cache_write``.  A query that sees no key, or
     whose scores are all -infinity, gets zeros; what lies out of sight does not count,
-    whatever it holds.  scale: dim ** -0.5 by default.
+    whatever it holds.  scale: dim ** -0.5 by default.  out: overlaps no input.
 
     ``workspace``: a uint8 device tensor from ``cache_attention_workspace`` (reused
     across calls on one stream), None not to split any entry's keys, or left out to
@@ -260,7 +260,7 @@ def cache_attention(q, cache, lengths, starts=None, table=None, scale=None, out=
     elif ws is not None:
         ws_bytes = ws.numel()
     status = lib.kv_cache_attention(view, qv, _ptr(lengths), _ptr(starts), batch, queries, heads, scale,
-                                       ov, _ptr(ws), ws_bytes, _stream_at(at))
+                                    ov, _ptr(ws), ws_bytes, _stream_at(at))
     if status:
         raise Nvfp4Error(status, "kv_cache_attention")
     return out

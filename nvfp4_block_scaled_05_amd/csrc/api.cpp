@@ -94,7 +94,7 @@ bool bad_lora(int64_t rows, int64_t inner, int64_t outer, int64_t rank, int64_t 
   return rank <= 0 || rank % 8 != 0 || rank > 128 || adapters <= 0 || adapters >= kMaxDim;
 }
 
-// An kv_cache and how many entries it serves.
+// A kv_cache and how many entries it serves.
 bool bad_cache(const kv_cache& c, int64_t batch) {
   if (c.pages <= 0 || bad_dim(c.pages) || c.page_size <= 0 || c.page_size % 16 != 0) return true;
   if (c.kv_heads <= 0 || c.kv_heads > (1 << 16) || c.dim <= 0 || c.dim % 16 != 0 || c.dim > 128)
@@ -572,8 +572,8 @@ int dit_lora_add(const void* y_bf16, const void* x_bf16, const void* down, const
 }
 
 int w4_gemm_weight_only(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_scales,
-                           const float* w_tensor_scale, const void* bias_bf16, int64_t M, int64_t N,
-                           int64_t K, int epilogue, void* y_bf16, float* y_amax, void* stream) {
+                        const float* w_tensor_scale, const void* bias_bf16, int64_t M, int64_t N,
+                        int64_t K, int epilogue, void* y_bf16, float* y_amax, void* stream) {
   if (bad_dim(M) || bad_dim(N) || bad_dim(K)) return NVFP4_ERR_SHAPE;
   const bool empty = M == 0 || N == 0;
   if (!empty && (!x_bf16 || !w_codes || !w_scales || !w_tensor_scale || !y_bf16))
@@ -593,8 +593,8 @@ int w4_gemm_weight_only(const void* x_bf16, const uint8_t* w_codes, const uint8_
 }
 
 int kv_cache_write(const kv_cache* cache, const dit_heads* k, const dit_heads* v,
-                      int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
-                      int32_t* dev_status, void* stream) {
+                   int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
+                   int32_t* dev_status, void* stream) {
   if (bad_dim(batch) || bad_dim(tokens)) return NVFP4_ERR_SHAPE;
   const bool empty = batch == 0 || tokens == 0;
   if (!cache || !k || !v) return NVFP4_ERR_NULL;
@@ -621,8 +621,8 @@ int kv_cache_write(const kv_cache* cache, const dit_heads* k, const dit_heads* v
 }
 
 int kv_cache_read(const kv_cache* cache, const dit_heads* k_out, const dit_heads* v_out,
-                     int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
-                     void* stream) {
+                  int64_t batch, int64_t tokens, const int32_t* starts, const int32_t* counts,
+                  void* stream) {
   if (bad_dim(batch) || bad_dim(tokens)) return NVFP4_ERR_SHAPE;
   const bool empty = batch == 0 || tokens == 0;
   if (!cache || !k_out || !v_out) return NVFP4_ERR_NULL;
@@ -648,15 +648,15 @@ int kv_cache_read(const kv_cache* cache, const dit_heads* k_out, const dit_heads
 }
 
 size_t kv_cache_attention_workspace_bytes(int64_t batch, int64_t queries, int64_t heads,
-                                             int64_t kv_heads, int64_t dim, int64_t capacity) {
+                                          int64_t kv_heads, int64_t dim, int64_t capacity) {
   if (bad_cache_attention(batch, queries, heads, kv_heads, dim, capacity)) return 0;
   return nvfp4::cache_attention_workspace_bytes(batch, queries, heads, kv_heads, dim, capacity);
 }
 
 int kv_cache_attention(const kv_cache* cache, const dit_heads* q, const int32_t* lengths,
-                          const int32_t* starts, int64_t batch, int64_t queries, int64_t heads,
-                          float scale, const dit_heads* out, void* workspace,
-                          size_t workspace_bytes, void* stream) {
+                       const int32_t* starts, int64_t batch, int64_t queries, int64_t heads,
+                       float scale, const dit_heads* out, void* workspace,
+                       size_t workspace_bytes, void* stream) {
   if (bad_dim(batch) || bad_dim(queries)) return NVFP4_ERR_SHAPE;
   const bool empty = batch == 0 || queries == 0;
   if (!cache || !q || !out) return NVFP4_ERR_NULL;

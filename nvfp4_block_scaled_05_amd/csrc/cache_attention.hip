@@ -185,8 +185,11 @@ __device__ __forceinline__ float rows_sum(float v) {
 // ------------------------------------------------------------------- few query rows
 //
 // A wave has RT tiles of 16 query rows and steps of 32 keys, two 16-key blocks T, in a
-// ring of LDS of its own: kStages - 1 steps are on their way while one is used, straight
-// from memory to LDS, so the bytes in flight take no registers.  With 16x16x32 products
+// ring of LDS of its own: up to kStages - 1 steps are on their way while one is used,
+// straight from memory to LDS, so the bytes in flight take no registers.  (With a table
+// fewer are: the compiler puts a wait for all loads before a look-up, also where it reads
+// no new entries.  131071 keys in pages of 64 take 43 us with the join, without a table
+// 42; 16 entries of 4096 keys 27.3 and 26.6.)  With 16x16x32 products
 // S^T = K Q^T, O^T += V^T P^T, and lane = 16 g + m:
 //   K operand   key 16 T + 4 (m % 4) + m / 4, elements g D / 4 ...
 //   scores      row m, keys 16 T + 4 r + g, r = 0..3
@@ -824,7 +827,8 @@ struct ManyRows {
   __device__ __forceinline__ int first(int t, int i) const {
     return min(64 * t + (i * WAVES + wave) * kGroupKeys, last_group);
   }
-  // (Tiles come in order, so the table is read 64 entries at a time.)
+  // (Tiles come in order, so the table is read 64 entries at a time.  As with few rows, a
+  // look-up waits for all loads on their way, the next tile's among them.)
   __device__ __forceinline__ void look_up(int t, int (&page)[kGroups]) {
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
@@ -1119,7 +1123,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_many_kernel(CacheAttentio
 //   Keys are dealt to two workgroups a compute unit, all that fit, where units alone leave
 // some idle: 8 units of 131071 keys; from 256 units on only long ones (512 units of 512 keys
 // 17.9 us dealt, 14.6 whole; lengths may be very unequal), from 1024 on none (2048 units of
-// 1 to 512 keys 173 and 42, 1024 of 1 to 2048 55 and 53).
+// 1 to 512 keys 173 and 42, 1024 of 1 to 2048 55 and 53).  The host knows the capacity, not
+// the lengths: where units alone fill the card, one long entry among many is its few
+// workgroups' alone (128 entries of 8 kv heads: 27 us for 512 keys each, 487 with 65536 in
+// one of them, whose bytes take 29 at a copy's rate).
 struct Plan {
   int few;                       // 16-row tiles of cache_few_kernel, 1 or 2; 0: cache_many_kernel
   int64_t rows, row_tiles, units, slot_rows;

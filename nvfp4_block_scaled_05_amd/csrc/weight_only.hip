@@ -424,8 +424,11 @@ __global__ __launch_bounds__(64 * WAVES) void weight_only_ring_kernel(WeightOnly
 }
 
 // 17 rows and more: two tiles of x, in registers a step ahead, before the codes (loads
-// return in order); in LDS they would leave room for three waves.  28672 x 8192: 65 us for
-// 32 rows, 71 by weight_only_kernel.
+// return in order); in LDS they would leave room for three waves.  The next step is on its
+// way in every second turn alone: in the others the compiler waits for all loads before
+// the products (x's registers come from two paths, with and without a next step; turns
+// with one path spill).  28672 x 8192: 55 us for 17 rows, 65 for 32, 71 by
+// weight_only_kernel; 8192 x 28672 77 and 90.
 template <int RT, int MT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void weight_only_lds_kernel(WeightOnly a) {
   constexpr int kStage = WeightRing<RT>::kBytes;

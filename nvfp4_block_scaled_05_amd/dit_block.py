@@ -125,7 +125,9 @@ class DitCrossBlock:
     which is made larger where it is too small for them, and is not kept: ``k`` and
     ``v`` are None.  Keys are quantized under the bound that their norm gives,
     sqrt(dim) max |k_norm|, values under the amax that the projection's epilogue
-    computes (so that layer has to be one that runs in NVFP4).
+    computes (so that layer has to be one that runs in NVFP4).  The attention is of
+    what 4 bits hold of them, and takes a fifth longer than over bf16 (2 x 16384
+    queries of 512 and 77 states, 24 heads of 128: 207 us).
     """
 
     def __init__(self, weights, batch, tokens, states, heads, kv_heads, q_norm, k_norm, plan,
